@@ -83,6 +83,10 @@ extern "C" {
  * n_kv_heads*head_dim multiples of 8, prompts of at least 10 tokens. */
 #define SPEC_DTYPE_Q4       2
 
+/* Cache rows of 8 bits (struct spec_kv_cache only): each row of head_dim
+ * values is e4m3 codes times one power of two. */
+#define SPEC_DTYPE_E4M3     3
+
 /* ---- per-step flags (spec_step out_flags) ---- */
 #define SPEC_FLAG_RESID_ZERO   0x1u  /* rejection with zero residual mass; drew from p */
 #define SPEC_FLAG_ALL_ACCEPTED 0x2u  /* all K drafts accepted; last token is the bonus */
@@ -306,6 +310,149 @@ SPEC_API int spec_accept_rows_noalloc(const float* p_logits, int64_t p_row_strid
 SPEC_API int spec_sample_rows(const float* logits, int64_t row_stride, int rows, int V,
                      float temperature, uint64_t seed, uint64_t step_base, int position,
                      int32_t* tokens, void* stream);
+
+/* ---- stateless operators of a paged KV cache ----
+ * For programs that keep their own cache and run their own forward around
+ * spec_accept_rows: rotary positions, the cache's write and read-back,
+ * attention of a chunk of new tokens (a verify step's K + 1, a prompt's next
+ * chunk, one decoded token) over the pages, and causal attention of packed
+ * prompts.  "Speculative Decoding 101", Floor 3 (one pass scores every
+ * position) names what they serve; the pages fix no cache layout.
+ *
+ * All are asynchronous on `stream` (cudaStream_t; NULL = default stream) of
+ * the current device, allocate nothing, keep nothing from one call for the
+ * next, may be captured into a CUDA graph, and give the same bits for the
+ * same arguments.  Device index arrays (positions, sequences, lengths, page
+ * tables) are read by the kernels: what they hold is checked there and never
+ * makes a kernel read or write outside its buffers (see each call). */
+
+/* A paged cache: pages of page_size positions, k and v each
+ * [pages][n_kv_heads][page_size][head_dim] (bf16 or e4m3 codes) with
+ * page_stride elements between pages (0: packed; k and v may share one buffer
+ * [pages][2]...).  SPEC_DTYPE_E4M3 adds k_scale and v_scale,
+ * [pages][n_kv_heads][page_size] bytes (scale_page_stride bytes between
+ * pages, 0: packed): value = code * 2^(byte - 127), and byte 255 marks a row
+ * of NaN.  Position p of sequence s is slot p mod page_size of page
+ * table[s * table_stride + p / page_size] (device int32 [seqs][max_pages];
+ * table_stride 0: max_pages).
+ * Checked: dtype; head_dim 32, 64 or 128; page_size a power of two in
+ * 16..256; 16-byte aligned pools and page strides; pages, heads, seqs and
+ * max_pages >= 1.  Two entries of a table may name one page (a shared
+ * prefix). */
+typedef struct spec_kv_cache {
+    void*    k;
+    void*    v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int      dtype;              /* SPEC_DTYPE_BF16 or SPEC_DTYPE_E4M3 */
+    int      pages, page_size, n_kv_heads, head_dim;
+    int64_t  page_stride, scale_page_stride;
+    const int32_t* table;
+    int64_t  table_stride;
+    int      seqs, max_pages;
+} spec_kv_cache;
+
+/* Rotary recipe.  Pair i of rot_dim / 2 turns by theta^(-2i/rot_dim) radians
+ * per position, changed for longer contexts by `scaling`:
+ *   SPEC_ROPE_PLAIN   not at all;
+ *   SPEC_ROPE_LINEAR  divided by factor;
+ *   SPEC_ROPE_NTK     theta grown to theta * factor^(rot_dim / (rot_dim - 2));
+ *   SPEC_ROPE_PARTS   by the turns r that a pair makes over orig_ctx
+ *                     positions: r >= high unchanged, r <= low divided by
+ *                     factor, linear in r between (low 1, high 4 or 32 are
+ *                     usual).
+ * mscale (0: 1) multiplies the rotated part (attention temperature of long
+ * contexts). */
+#define SPEC_ROPE_PLAIN   0
+#define SPEC_ROPE_LINEAR  1
+#define SPEC_ROPE_NTK     2
+#define SPEC_ROPE_PARTS   3
+#define SPEC_ROPE_MAX_DIM 256
+typedef struct spec_rope_desc {
+    int    rot_dim;       /* rotated leading elements of a head: even, 2..SPEC_ROPE_MAX_DIM */
+    int    interleaved;   /* pairs (2i, 2i+1); 0: halves (i, i + rot_dim/2) */
+    int    scaling;       /* SPEC_ROPE_* */
+    double theta, factor, orig_ctx, low, high, mscale;
+} spec_rope_desc;
+/* The recipe worked out once (plain memory, caller-owned, no pointers): turns
+ * per position of every pair as a 64-bit fraction, so that a position times
+ * it, modulo 2^64, is the exact angle of positions however far. */
+typedef struct spec_rope {
+    int      rot_dim, interleaved;
+    float    mscale;
+    int      reserved;
+    uint64_t turn[SPEC_ROPE_MAX_DIM / 2];
+} spec_rope;
+SPEC_API int spec_rope_plan(const spec_rope_desc* desc, spec_rope* out);
+
+/* y[t][h] = x[t][h] with its first rot_dim elements rotated by position
+ * pos[t] (device int32 [tokens], any value) and the rest copied; computed in
+ * fp32, rounded once.  x and y: [tokens][heads][head_dim], fp32 or bf16 each,
+ * with strides in elements between tokens and heads (elements of a head are
+ * adjacent).  y may be x (equal dtype and strides); otherwise they must not
+ * overlap.  inverse != 0 rotates back by the same angles (the gradient of
+ * the forward call; it keeps the factor mscale).  tokens may be 0. */
+SPEC_API int spec_rope_rows(const void* x, int x_dtype, int64_t x_tok_stride, int64_t x_head_stride,
+                   void* y, int y_dtype, int64_t y_tok_stride, int64_t y_head_stride,
+                   const int32_t* pos, int tokens, int heads, int head_dim,
+                   const spec_rope* plan, int inverse, void* stream);
+
+/* Write `tokens` new rows into the cache: row t of k (rotated by its position
+ * when plan is given) and v, [tokens][n_kv_heads][head_dim] fp32 or bf16 with
+ * strides in elements, goes to position pos[t] of sequence seq[t] (device
+ * int32).  Rotation and scaling in fp32, one rounding.  E4M3 rows take the
+ * smallest power of two 2^e, -60 <= e <= 60, that keeps the row's largest
+ * magnitude within 448 (a power of two loses nothing of a float's relative
+ * precision, and makes the read-back exact in bf16); a row that holds an
+ * infinity, a NaN or a magnitude past 448 * 2^60 becomes a NaN row.
+ * A token whose seq or pos is negative or outside the table, or whose table
+ * entry is not a page of the pool, is skipped (padding).  Positions written
+ * by one call must be distinct: two tokens for one slot leave either row, or
+ * a mixture. */
+SPEC_API int spec_kv_append(const spec_kv_cache* cache, const void* k, int64_t k_tok_stride, int64_t k_head_stride,
+                   const void* v, int64_t v_tok_stride, int64_t v_head_stride, int dtype,
+                   const int32_t* seq, const int32_t* pos, int tokens, const spec_rope* plan, void* stream);
+
+/* Read rows back: position pos[t] of sequence seq[t] to k_out and v_out (fp32
+ * or bf16 [tokens][n_kv_heads][head_dim], packed; either may be NULL).  The
+ * value of an e4m3 row is exact in both.  A row outside the table or the pool
+ * (as for spec_kv_append) reads as zeros. */
+SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, const int32_t* pos, int tokens,
+                   void* k_out, void* v_out, int out_dtype, void* stream);
+
+/* Causal attention of each sequence's newest tokens over its cache (which
+ * holds their keys already).  q: bf16 [tokens][n_heads][head_dim], strides in
+ * elements; sequence b's rows are cu_q[b] .. cu_q[b+1] - 1 (device int32
+ * [seqs + 1], ascending from >= 0), its keys the kv_lens[b] first positions
+ * (device int32 [seqs]), and row i of its n rows sees positions
+ * 0 .. kv_lens[b] - n + i; query head h reads KV head h * n_kv_heads /
+ * n_heads.  out: bf16 like q with its own strides; lse (may be NULL): fp32
+ * [tokens][n_heads], the log of the row's sum of exp(scale * q.k).  A row
+ * that sees nothing gets zeros and lse -inf.  Rows outside every sequence, and
+ * rows past a sequence's first max_q (a bound on the chunks' lengths, sizing
+ * the grid), are left as they were.  A length past the table's positions is cut
+ * there; a table entry that is not a page of the pool reads as zero rows.
+ * scale 0: 1/sqrt(head_dim).  Scores, softmax statistics and sums are fp32,
+ * probabilities bf16 in the product with v.  Cache slots past a sequence's
+ * length are never used, whatever they hold; a value row that is not finite
+ * within the length reaches the outputs of the whole chunk.
+ * Checked: n_heads a multiple of n_kv_heads; 16-byte aligned q and out with
+ * strides multiples of 8. */
+SPEC_API int spec_attn_paged(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const int32_t* cu_q, const int32_t* kv_lens, int tokens, int max_q, int n_heads,
+                    float scale, void* out, int64_t out_tok_stride, int64_t out_head_stride, float* lse,
+                    void* stream);
+
+/* Causal attention within packed sequences: rows cu[b] .. cu[b+1] - 1 of q
+ * [tokens][n_heads][head_dim] and of k and v [tokens][n_kv_heads][head_dim]
+ * (bf16, strides in elements: they may be slices of one projection) are
+ * sequence b; row i sees rows 0 .. i of its own.  The rest as for
+ * spec_attn_paged, with max_len for max_q. */
+SPEC_API int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* k,
+                     int64_t k_tok_stride, int64_t k_head_stride, const void* v, int64_t v_tok_stride,
+                     int64_t v_head_stride, const int32_t* cu, int seqs, int tokens, int max_len,
+                     int n_heads, int n_kv_heads, int head_dim, float scale, void* out,
+                     int64_t out_tok_stride, int64_t out_head_stride, float* lse, void* stream);
 
 /* Phase timing of the step as run in production (CUDA graphs, CUDA events
  * on the context's stream), averaged over `iters` replays after two

@@ -14,7 +14,8 @@ from ._build import LIB, build
 
 __all__ = ["build", "lib", "SpecError", "SpecDecoder", "accept_rows", "sample_rows",
            "SPEC_DTYPE_F32", "SPEC_DTYPE_BF16", "SPEC_OPT_NO_GRAPH", "SPEC_OPT_TIMING",
-           "SPEC_FLAG_RESID_ZERO", "SPEC_FLAG_ALL_ACCEPTED"]
+           "SPEC_FLAG_RESID_ZERO", "SPEC_FLAG_ALL_ACCEPTED", "KVCache", "rope_plan", "rope_rows",
+           "kv_append", "kv_gather", "attn_paged", "attn_prompt"]
 
 SPEC_OK = 0
 ERRORS = {-1: "SPEC_E_ARG", -2: "SPEC_E_VOCAB", -3: "SPEC_E_SHAPE", -4: "SPEC_E_CAPACITY",
@@ -22,6 +23,9 @@ ERRORS = {-1: "SPEC_E_ARG", -2: "SPEC_E_VOCAB", -3: "SPEC_E_SHAPE", -4: "SPEC_E_
 SPEC_DTYPE_F32 = 0
 SPEC_DTYPE_BF16 = 1
 SPEC_DTYPE_Q4 = 2
+SPEC_DTYPE_E4M3 = 3
+SPEC_ROPE_MAX_DIM = 256
+_ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "parts": 3}
 _DTYPES = {"f32": SPEC_DTYPE_F32, "bf16": SPEC_DTYPE_BF16, "q4": SPEC_DTYPE_Q4}
 SPEC_MAX_BATCH = 64
 SPEC_FLAG_RESID_ZERO = 0x1
@@ -86,10 +90,32 @@ class Profile(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("orig_ctx", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int), ("turn", ctypes.c_uint64 * (SPEC_ROPE_MAX_DIM // 2))]
+
+
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _U32P = ctypes.POINTER(ctypes.c_uint32)
 _F32P = ctypes.POINTER(ctypes.c_float)
 _VP = ctypes.c_void_p
+_INT = ctypes.c_int
+_I64 = ctypes.c_int64
 
 # name -> (restype, argtypes); every function declared in include/specverify.h
 SIGNATURES = {
@@ -116,6 +142,15 @@ SIGNATURES = {
     "spec_sample_rows": (ctypes.c_int, [_VP, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                                         ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64,
                                         ctypes.c_int, _VP, _VP]),
+    "spec_rope_plan": (ctypes.c_int, [_VP, _VP]),
+    "spec_rope_rows": (ctypes.c_int, [_VP, _INT, _I64, _I64, _VP, _INT, _I64, _I64, _VP, _INT, _INT, _INT,
+                                      _VP, _INT, _VP]),
+    "spec_kv_append": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _INT, _VP, _VP, _INT, _VP, _VP]),
+    "spec_kv_gather": (ctypes.c_int, [_VP, _VP, _VP, _INT, _VP, _VP, _INT, _VP]),
+    "spec_attn_paged": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _VP, _INT, _INT, _INT, ctypes.c_float,
+                                       _VP, _I64, _I64, _VP, _VP]),
+    "spec_attn_prompt": (ctypes.c_int, [_VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _INT, _INT,
+                                        _INT, _INT, _INT, _INT, ctypes.c_float, _VP, _I64, _I64, _VP, _VP]),
     "spec_profile": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.POINTER(Profile)]),
     "spec_phase_times": (ctypes.c_int, [_VP, ctypes.c_int, _VP, ctypes.c_int,
                                         ctypes.POINTER(ctypes.c_int)]),
@@ -395,3 +430,208 @@ def sample_rows(logits, temperature, seed, step_base=0, position=1, stream=None,
     _check(lib().spec_sample_rows(_ptr(logits), rs, R, V, float(temperature), int(seed),
                                   int(step_base), int(position), _ptr(out), ctypes.c_void_p(st)))
     return out
+
+
+# ---- paged-cache operators (see include/specverify.h) ----
+# The calls run on the current stream of the tensors' device (or the raw
+# stream given), with that device current; tensors are read by pointer.
+def _need(ok, msg):
+    if not ok:
+        raise SpecError(-1, msg)
+
+
+def _io_dtype(t):
+    import torch
+    _need(t.dtype in (torch.float32, torch.bfloat16), f"rows are fp32 or bf16, not {t.dtype}")
+    return SPEC_DTYPE_F32 if t.dtype == torch.float32 else SPEC_DTYPE_BF16
+
+
+def _rows3(name, t):
+    _need(t.is_cuda and t.dim() == 3, f"{name}: a CUDA tensor [tokens, heads, head_dim]")
+    st = t.stride()
+    _need(st[2] == 1 or t.shape[2] == 1 or t.numel() == 0, f"{name}: the elements of a head must be adjacent")
+    return st
+
+
+def _index(name, t, n, device):
+    import torch
+    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.device == device and t.is_contiguous(),
+          f"{name}: a contiguous int32 tensor of {n} on the rows' device")
+
+
+def _call(device, stream, fn, *args):
+    import torch
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+    if rc:
+        _check(rc)
+
+
+class KVCache:
+    """A paged cache over caller-owned CUDA tensors: k, v [pages, n_kv_heads,
+    page_size, head_dim] (bf16, or torch.float8_e4m3fn with uint8 k_scale,
+    v_scale [pages, n_kv_heads, page_size]; pages may be strided, a page is
+    contiguous) and the page table, int32 [seqs, max_pages].  The tensors are
+    kept and read in place: write the table's rows as sequences grow."""
+
+    def __init__(self, k, v, table, k_scale=None, v_scale=None):
+        import torch
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype, "k and v: equal [pages, heads, page, dim]")
+        _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn), f"the cache is bf16 or float8_e4m3fn, not {k.dtype}")
+        f8 = k.dtype == torch.float8_e4m3fn
+        _need(table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1, "table: int32 [seqs, max_pages]")
+        pages, heads, ps, hd = k.shape
+        for t in (k, v):
+            _need(t.stride()[1:] == (ps * hd, hd, 1), "a page must be contiguous")
+        _need(k.stride(0) == v.stride(0), "k and v must have one page stride")
+        if f8:
+            for t in (k_scale, v_scale):
+                _need(t is not None and t.dtype == torch.uint8 and t.shape == (pages, heads, ps) and
+                      t.stride()[1:] == (ps, 1), "an e4m3 cache needs uint8 scales [pages, heads, page]")
+            _need(k_scale.stride(0) == v_scale.stride(0), "the scales must have one page stride")
+        else:
+            _need(k_scale is None and v_scale is None, "a bf16 cache has no scales")
+        for t in (k, v, table) + ((k_scale, v_scale) if f8 else ()):
+            _need(t.is_cuda and t.device == k.device, "the cache's tensors must be on one CUDA device")
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self.n_kv_heads, self.head_dim, self.page_size = heads, hd, ps
+        self.seqs, self.max_pages = table.shape
+        self.device = k.device
+        self._c = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if f8 else None,
+                              v_scale.data_ptr() if f8 else None, SPEC_DTYPE_E4M3 if f8 else SPEC_DTYPE_BF16,
+                              pages, ps, heads, hd, k.stride(0), k_scale.stride(0) if f8 else 0,
+                              table.data_ptr(), table.stride(0), self.seqs, self.max_pages)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages, page_size, n_kv_heads, head_dim, table, dtype="bf16"):
+        """A zeroed pool of `pages` pages ('bf16' or 'e4m3') on the table's device."""
+        import torch
+        _need(dtype in ("bf16", "e4m3"), f"the cache is 'bf16' or 'e4m3', not {dtype!r}")
+        shape = (pages, n_kv_heads, page_size, head_dim)
+        if dtype == "bf16":
+            k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=table.device) for _ in range(2))
+            return cls(k, v, table)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=table.device).view(torch.float8_e4m3fn)
+                for _ in range(2))
+        ks, vs = (torch.full(shape[:3], 127, dtype=torch.uint8, device=table.device) for _ in range(2))
+        return cls(k, v, table, ks, vs)
+
+
+def rope_plan(rot_dim, theta, interleaved=False, scaling="plain", factor=1.0, orig_ctx=0.0, low=1.0, high=4.0,
+              mscale=1.0):
+    """The rotation of rot_dim leading elements of a head, worked out once on
+    the host: scaling 'plain', 'linear', 'ntk' or 'parts' (see spec_rope_desc)."""
+    _need(scaling in _ROPE_SCALING, f"unknown scaling {scaling!r}")
+    d = RopeDesc(rot_dim, int(bool(interleaved)), _ROPE_SCALING[scaling], theta, factor, orig_ctx, low, high, mscale)
+    plan = RopePlan()
+    _check(lib().spec_rope_plan(ctypes.byref(d), ctypes.byref(plan)))
+    plan._ref = ctypes.byref(plan)
+    return plan
+
+
+def rope_rows(x, pos, plan, out=None, dtype=None, inverse=False, stream=None):
+    """x [tokens, heads, head_dim] (fp32 or bf16, strided) rotated by the
+    positions pos [tokens] int32; returns out (given, may be x itself, or new
+    in `dtype`, by default x's).  inverse rotates back."""
+    import torch
+    n, h, d = x.shape if x.dim() == 3 else (0, 0, 0)
+    xs = _rows3("x", x)
+    _index("pos", pos, n, x.device)
+    if out is None:
+        out = torch.empty((n, h, d), dtype=x.dtype if dtype is None else dtype, device=x.device)
+    else:
+        _need(out.shape == x.shape and out.device == x.device and dtype in (None, out.dtype), "out: x's shape and device")
+    ys = _rows3("out", out)
+    _call(x.device, stream, lib().spec_rope_rows, x.data_ptr(), _io_dtype(x), xs[0], xs[1], out.data_ptr(),
+          _io_dtype(out), ys[0], ys[1], pos.data_ptr(), n, h, d, plan._ref, 1 if inverse else 0)
+    return out
+
+
+def kv_append(cache, k, v, seq, pos, plan=None, stream=None):
+    """Write rows k (rotated by plan, if given) and v [tokens, n_kv_heads,
+    head_dim] to positions pos of sequences seq (int32 [tokens]; a negative
+    one skips the row).  Positions of one call must be distinct."""
+    ks, vs = _rows3("k", k), _rows3("v", v)
+    n = k.shape[0]
+    _need(k.shape == v.shape and k.dtype == v.dtype and k.shape[1:] == (cache.n_kv_heads, cache.head_dim),
+          "k and v: equal [tokens, n_kv_heads, head_dim] of the cache")
+    _need(k.device == v.device == cache.device, "k, v and the cache must be on one device")
+    _index("seq", seq, n, cache.device)
+    _index("pos", pos, n, cache.device)
+    _call(cache.device, stream, lib().spec_kv_append, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+          vs[1], _io_dtype(k), seq.data_ptr(), pos.data_ptr(), n, plan._ref if plan is not None else None)
+
+
+def kv_gather(cache, seq, pos, dtype=None, stream=None):
+    """(k, v) [tokens, n_kv_heads, head_dim] read back from positions pos of
+    sequences seq, bf16 or fp32; rows that do not exist read as zeros."""
+    import torch
+    n = seq.shape[0]
+    _index("seq", seq, n, cache.device)
+    _index("pos", pos, n, cache.device)
+    k = torch.empty((n, cache.n_kv_heads, cache.head_dim), dtype=torch.bfloat16 if dtype is None else dtype,
+                    device=cache.device)
+    v = torch.empty_like(k)
+    _call(cache.device, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
+          v.data_ptr(), _io_dtype(k))
+    return k, v
+
+
+def _attn_out(q, out, lse):
+    import torch
+    _need(q.dtype == torch.bfloat16, f"q is bf16, not {q.dtype}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == q.device, "out: like q")
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse is not False:
+        _need(lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.device == q.device and
+              lse.is_contiguous(), "lse: contiguous fp32 [tokens, heads]")
+    return out, lse
+
+
+def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=None, stream=None):
+    """Causal attention of the sequences' newest tokens over the cache.  q
+    [tokens, n_heads, head_dim] bf16; sequence b (row b of the cache's table)
+    owns rows cu_q[b] .. cu_q[b+1]-1 and kv_lens[b] cached positions, its new
+    ones included (int32 [seqs + 1], [seqs]); max_q bounds the rows of one
+    sequence (default: tokens).  Returns (out, lse [tokens, n_heads] fp32, or
+    None with lse=False); rows outside every sequence are not written."""
+    qs = _rows3("q", q)
+    n, h, d = q.shape
+    _need(d == cache.head_dim and q.device == cache.device, "q must have the cache's head_dim and device")
+    _index("cu_q", cu_q, cache.seqs + 1, q.device)
+    _index("kv_lens", kv_lens, cache.seqs, q.device)
+    out, lse = _attn_out(q, out, lse)
+    os_ = _rows3("out", out)
+    _call(q.device, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
+          kv_lens.data_ptr(), n, n if max_q is None else max_q, h, scale, out.data_ptr(), os_[0], os_[1],
+          lse.data_ptr() if lse is not False else None)
+    return out, (lse if lse is not False else None)
+
+
+def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream=None):
+    """Causal attention within packed sequences: rows cu[b] .. cu[b+1]-1 of q
+    [tokens, n_heads, head_dim] and k, v [tokens, n_kv_heads, head_dim] (bf16,
+    may be slices of one projection) are sequence b; max_len bounds their
+    lengths (default: tokens).  Returns (out, lse) as attn_paged."""
+    import torch
+    qs, ks, vs = _rows3("q", q), _rows3("k", k), _rows3("v", v)
+    n, h, d = q.shape
+    _need(k.shape == v.shape and k.shape[0] == n and k.shape[2] == d, "k and v: equal [tokens, n_kv_heads, head_dim]")
+    _need(k.dtype == v.dtype == torch.bfloat16, "k and v are bf16")
+    _need(k.device == v.device == q.device, "q, k and v must be on one device")
+    _need(cu.dim() == 1 and cu.shape[0] >= 2, "cu: int32 [sequences + 1]")
+    _index("cu", cu, cu.shape[0], q.device)
+    out, lse = _attn_out(q, out, lse)
+    os_ = _rows3("out", out)
+    _call(q.device, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+          v.data_ptr(), vs[0], vs[1], cu.data_ptr(), cu.shape[0] - 1, n, n if max_len is None else max_len, h,
+          k.shape[1], d, scale, out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None)
+    return out, (lse if lse is not False else None)

@@ -1,0 +1,76 @@
+// Internal interface of the paged-cache operators (kvrows.cu: rotary
+// positions, cache write and read-back; pattn.cu, pattn_tc.cu: attention).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <string>
+#include <utility>
+
+#include "specverify.h"
+
+namespace sv {
+
+void set_thread_error(const std::string& msg);  // engine.cu
+
+// A launch in plain stream order (these kernels take no part in programmatic
+// dependent launch), optionally in clusters of `cluster` blocks along x.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_rows(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                               cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Checks of a cache description shared by the entry points; SPEC_OK or the
+// code to return, with the message set.
+int check_cache(const spec_kv_cache* c, const char* who);
+
+// One attention call.  Row r of sequence b's KV head g is token r / G, query
+// head g * G + r % G (G = hq / hkv).  Keys come from pages (paged = 1) or
+// from packed rows (kcu = cu, the rows of the sequence itself).
+struct PAttn {
+  const void* q;
+  int64_t q_ts, q_hs;            // strides in elements between tokens and heads
+  const int32_t* cu;             // [seqs + 1] rows of q of each sequence
+  const int32_t* lens;           // [seqs] keys (paged); packed: the rows themselves
+  int seqs, tokens, max_q;
+  int hq, hkv, hd;
+  float scale_log2;              // softmax scale * log2(e)
+  void* out;
+  int64_t o_ts, o_hs;
+  float* lse;                    // [tokens][hq] or null
+  int paged, f8;
+  const void* k;                 // pools, or packed rows
+  const void* v;
+  int64_t k_ts, k_hs, v_ts, v_hs;   // packed: strides of k and v
+  const uint8_t* ks;
+  const uint8_t* vs;
+  int64_t page_stride, scale_stride;
+  const int32_t* table;
+  int64_t table_stride;
+  int pages, page_shift, max_pages;
+  // sequences with more than max_rows rows (tokens * G) are left to the
+  // tensor-memory kernel, which takes those only
+  int max_rows;
+};
+// Rows per KV head up to which the register-tile kernel takes a sequence
+// when both kernels can.
+constexpr int kPaMaxRows = 64;
+cudaError_t launch_pattn(const PAttn& a, int num_sms, cudaStream_t st);
+// Tensor-memory kernel: bf16 or e4m3 keys, head dim 64 or 128.
+bool pattn_tc_supported(const PAttn& a);
+cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st);
+
+}  // namespace sv

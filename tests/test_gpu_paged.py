@@ -1,0 +1,580 @@
+"""Paged-cache operators against plain 64-bit forms: rotary positions, the
+cache's write and read-back, chunk attention over the pages, packed prompts.
+
+Tolerances count roundings.  A rounding is off by at most half a step of its
+type (bf16 2^-8, fp32 2^-24, e4m3 2^-4 relative, and half of e4m3's smallest
+step for its subnormals):
+* rotation: the angle, a 32-bit fraction of a turn turned into fp32 (2^-24 of
+  at most pi), sincospif (2 units, 2^-22), two products and one sum: under
+  8 * 2^-23 of |a| + |b|, then the output's rounding;
+* attention: a score is a sum of head_dim products, off by at most
+  d = (head_dim + 8) 2^-24 scale sum|q k|; a weight by 2 d and, once for the
+  product with v, by a bf16 rounding; so |out - ref| <= (2^-8 + 4 d + keys
+  2^-23 + 2^-20) sum w|v| + 2^-8 |ref|, and lse is within 2 d + keys 2^-23 +
+  2^-20 + |lse| 2^-22 (a fp32 sum of `keys` terms, exp2's 2^-22).
+"""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_verification_step_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    sv.build()
+    sv.lib()
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ rotary
+def _freqs(rot, theta, scaling="plain", factor=1.0, orig=0.0, low=1.0, high=4.0):
+    f = []
+    if scaling == "ntk":
+        theta = theta * factor ** (rot / (rot - 2))
+    for i in range(rot // 2):
+        w = theta ** (-2.0 * i / rot)
+        if scaling == "linear":
+            w /= factor
+        if scaling == "parts":
+            keep = min(1.0, max(0.0, (orig * w / (2 * math.pi) - low) / (high - low)))
+            w *= keep + (1 - keep) / factor
+        f.append(w)
+    return f
+
+
+def _rope_ref(x, pos, freqs, inter, sign=1.0, mscale=1.0):
+    """64-bit rotation by the complex product; also the pair sizes |a| + |b|."""
+    x = x.to(F64)
+    r = 2 * len(freqs)
+    # angles in turns with integer positions: the fractional part is exact enough in 64 bits
+    turns = torch.outer(pos.to(F64), torch.tensor(freqs, dtype=F64, device="cuda") / (2 * math.pi))
+    ang = (turns - turns.round()) * (2 * math.pi) * sign
+    z = torch.polar(torch.full_like(ang, mscale), ang)[:, None]
+    y, size = x.clone(), x.abs()
+    a, b = (x[..., 0:r:2], x[..., 1:r:2]) if inter else (x[..., :r // 2], x[..., r // 2:r])
+    w = torch.complex(a, b) * z
+    s = a.abs() + b.abs()
+    if inter:
+        y[..., 0:r:2], y[..., 1:r:2] = w.real, w.imag
+        size[..., 0:r:2], size[..., 1:r:2] = s, s
+    else:
+        y[..., :r // 2], y[..., r // 2:r] = w.real, w.imag
+        size[..., :r // 2], size[..., r // 2:r] = s, s
+    return y, size
+
+
+ROPE = [  # tokens, heads, hd, rot, interleaved, in, out, plan options, first position
+    (6, 40, 128, 128, False, torch.float32, torch.bfloat16, {}, 511),
+    (1, 1, 64, 64, False, torch.bfloat16, torch.bfloat16, {}, 0),
+    (33, 10, 64, 32, True, torch.bfloat16, torch.float32, {"scaling": "parts", "factor": 8.0, "orig_ctx": 8192.0}, 900000),
+    (700, 40, 64, 16, False, torch.bfloat16, torch.bfloat16, {"scaling": "linear", "factor": 4.0}, 70000),
+    (17, 3, 128, 128, True, torch.float32, torch.float32, {"scaling": "ntk", "factor": 4.0, "mscale": 1.25}, 3),
+    (5, 7, 32, 6, False, torch.float32, torch.bfloat16, {}, 2 ** 31 - 10),      # odd split: one element at a time
+    (5, 7, 34, 34, True, torch.bfloat16, torch.bfloat16, {}, 100),
+    (4, 2, 256, 256, False, torch.float32, torch.float32, {"scaling": "parts", "factor": 32.0, "orig_ctx": 4096.0, "high": 32.0}, 1 << 20),
+]
+
+
+@pytest.mark.parametrize("t,h,hd,rot,inter,tin,tout,opt,first", ROPE)
+def test_rope_rows(t, h, hd, rot, inter, tin, tout, opt, first):
+    g = _gen(t + h)
+    wide = _randn(g, t, h + 2, hd).to(tin)
+    x = wide[:, 1:h + 1]                       # a slice of a projection
+    pos = (first + torch.arange(t, device="cuda")).int()
+    plan = sv.rope_plan(rot, 500000.0, interleaved=inter, **opt)
+    y = sv.rope_rows(x, pos, plan, dtype=tout)
+    o = dict(opt)
+    ms = o.pop("mscale", 1.0)
+    f = _freqs(rot, 500000.0, o.get("scaling", "plain"), o.get("factor", 1.0), o.get("orig_ctx", 0.0),
+               o.get("low", 1.0), o.get("high", 4.0))
+    ref, size = _rope_ref(x, pos, f, inter, mscale=ms)
+    # the reference's own angles: positions times 64-bit frequencies, 2^-52 relative
+    tol = size * ms * (8 * 2.0 ** -23 + (first + t) * 2.0 ** -50) + ref.abs() * HALF[tout]
+    err = (y.to(F64) - ref).abs()
+    assert (err <= tol).all(), float((err - tol).max())
+    if rot < hd and tin == tout:
+        assert torch.equal(y[..., rot:], x[..., rot:])
+    # the gradient: <rotated x, u> = <x, rotated-back u>, and a difference quotient of the same
+    u = _randn(g, t, h, hd)
+    back = sv.rope_rows(u, pos, plan, inverse=True)
+    bref, bsize = _rope_ref(u, pos, f, inter, sign=-1.0, mscale=ms)
+    assert ((back.to(F64) - bref).abs() <= bsize * ms * (8 * 2.0 ** -23 + (first + t) * 2.0 ** -50)
+            + bref.abs() * 2.0 ** -24).all()
+    lhs = (ref * u.to(F64)).sum()
+    rhs = (x.to(F64) * bref).sum()
+    assert abs(lhs - rhs) <= 1e-10 * float((size * u.to(F64).abs()).sum())
+
+
+def test_rope_rows_in_place_and_negative():
+    g = _gen(3)
+    x = _randn(g, 9, 4, 64).bfloat16()
+    pos = _i32([-5, 0, 7, 7, 2 ** 31 - 1, -2 ** 31, 1, 2, 3])
+    plan = sv.rope_plan(64, 10000.0)
+    y = sv.rope_rows(x, pos, plan)
+    ref, size = _rope_ref(x, pos, _freqs(64, 10000.0), False)
+    far = pos.to(F64).abs()[:, None, None] * 2.0 ** -50
+    assert ((y.to(F64) - ref).abs() <= size * (8 * 2.0 ** -23 + far) + ref.abs() * 2.0 ** -8).all()
+    z = x.clone()
+    assert sv.rope_rows(z, pos, plan, out=z) is z
+    assert torch.equal(z, y)
+    assert sv.rope_rows(x[:0], pos[:0], plan).shape == (0, 4, 64)
+
+
+# ------------------------------------------------------------------- cache
+def _times2(x, e):
+    """x * 2^e, exact (a device pow or ldexp of 2 is not, in its last place)."""
+    powers = torch.tensor([2.0 ** i for i in range(-140, 141)], dtype=F64, device=x.device)
+    return x * powers[e.long() + 140]
+
+
+def _round_e4m3(y):
+    """Nearest e4m3 value (ties to even) of 64-bit values within +-448."""
+    _, e = torch.frexp(y.abs().clamp_min(2.0 ** -6))      # y = m 2^e, 1/2 <= m < 1: steps of 2^(e - 4)
+    return _times2(torch.round(_times2(y, 4 - e)), e - 4)
+
+
+def _exponent(x):
+    """Smallest e in -60..60 with max|x| <= 448 2^e (0 for zero rows)."""
+    top = x.abs().amax(-1)
+    m, e = torch.frexp(top)
+    e = torch.where(top > 0, (e - 9 + (m > 0.875).int()), torch.zeros_like(e))
+    return e.clamp(-60, 60)
+
+
+def _cache(g, seqs, ctx, heads, ps, hd, dtype, extra=3):
+    need = -(-ctx // ps)
+    pages = seqs * need + extra
+    table = torch.randperm(pages, generator=g, device="cuda")[:seqs * need].int().view(seqs, need).contiguous()
+    return sv.KVCache.empty(pages, ps, heads, hd, table, dtype)
+
+
+def _values(cache):
+    out = []
+    for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        v = x.to(F64)
+        if s is not None:
+            v = _times2(v, (s.int() - 127).clamp(-140, 140).unsqueeze(-1))
+            v[s == 255] = math.nan
+        out.append(v)
+    return out
+
+
+def _read(cache, values, seq, pos):
+    page = cache.table.long()[seq.long(), (pos // cache.page_size).long()]
+    return [v[page, :, (pos % cache.page_size).long()] for v in values]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tin", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hd,heads,ps,n", [(32, 2, 16, 5), (64, 8, 32, 1), (128, 8, 16, 70), (128, 1, 256, 300),
+                                           (64, 3, 64, 2500)])
+def test_append_and_gather(dtype, tin, hd, heads, ps, n):
+    g = _gen(hd + n)
+    seqs, ctx = 3, max(n, 40)
+    cache = _cache(g, seqs, ctx, heads, ps, hd, dtype)
+    x = (_randn(g, n, 2 * heads + 1, hd) * torch.exp(2 * _randn(g, n, 1, 1))).to(tin)
+    k, v = x[:, :heads], x[:, heads:2 * heads]
+    seq = torch.randint(0, seqs, (n,), generator=g, device="cuda").int()
+    pos = torch.randperm(ctx, generator=g, device="cuda")[:n].int()
+    before = [t.clone() for t in _values(cache)]
+    sv.kv_append(cache, k, v, seq, pos)
+    got = _read(cache, _values(cache), seq, pos)
+    for y, src in zip(got, (k, v)):
+        s = src.to(F64)
+        if dtype == "bf16":
+            assert torch.equal(y, src.bfloat16().to(F64))
+        else:
+            e = _exponent(s).unsqueeze(-1)
+            bad = int((y != _times2(_round_e4m3(_times2(s, -e)), e)).sum())
+            assert bad == 0, bad
+    # every other slot is as it was
+    mask = torch.ones(before[0].shape[0], ps, dtype=torch.bool, device="cuda")
+    mask[cache.table.long()[seq.long(), (pos // ps).long()], (pos % ps).long()] = False
+    for y, z in zip(_values(cache), before):
+        assert torch.equal(y.transpose(1, 2)[mask], z.transpose(1, 2)[mask])
+    for out in (torch.bfloat16, torch.float32):
+        for y, z in zip(sv.kv_gather(cache, seq, pos, dtype=out), got):
+            assert y.dtype == out and torch.equal(y.to(F64), z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("inter,rot,hd", [(False, 128, 128), (True, 64, 64), (False, 16, 32), (True, 8, 64),
+                                          (False, 20, 64), (True, 30, 128)])
+def test_append_rotates(dtype, inter, rot, hd):
+    g = _gen(rot)
+    n, heads = 37, 2
+    cache = _cache(g, 2, 64, heads, 16, hd, dtype)
+    k, v = _randn(g, n, heads, hd), _randn(g, n, heads, hd)
+    seq = (torch.arange(n, device="cuda") % 2).int()
+    pos = (torch.arange(n, device="cuda") // 2 + 20).int()
+    sv.kv_append(cache, k, v, seq, pos, sv.rope_plan(rot, 500000.0, interleaved=inter))
+    ref, size = _rope_ref(k, pos, _freqs(rot, 500000.0), inter)
+    got, gv = _read(cache, _values(cache), seq, pos)
+    rope = size * 8 * 2.0 ** -23
+    if dtype == "bf16":
+        assert ((got - ref).abs() <= ref.abs() * 2.0 ** -8 + 2 * rope).all()
+        assert torch.equal(gv, v.bfloat16().to(F64))
+    else:
+        e = _exponent(ref)   # a row at a power's border may take the next one: twice the smallest step
+        assert ((got - ref).abs() <= ref.abs() * 2.0 ** -4 + torch.pow(2.0, e.to(F64) - 9).unsqueeze(-1) + 2 * rope).all()
+
+
+def test_append_skips_and_special_rows():
+    g = _gen(8)
+    cache = _cache(g, 2, 32, 1, 16, 32, "e4m3")
+    cache.table[1, 1] = cache.k.shape[0]          # not a page of the pool
+    cache.table[0, 1] = -7
+    n = 8
+    k = _randn(g, n, 1, 32)
+    k[0] = 0
+    k[1, 0, 3] = math.inf
+    k[2, 0, 31] = math.nan
+    k[3] *= 2.0 ** 100
+    k[4] *= 2.0 ** -90
+    k[5, 0, 0] = 448.0
+    k[5, 0, 1:] /= 10
+    v = _randn(g, n, 1, 32)
+    before = [t.clone().view(torch.uint8) for t in (cache.k, cache.v)]
+    skip_seq = _i32([-1, 2, 0, 0, 0, 1, 0, 1])
+    skip_pos = _i32([0, 0, -1, 32, 16, 16, 31, 31])
+    sv.kv_append(cache, k, v, skip_seq, skip_pos)
+    assert all(torch.equal(t.view(torch.uint8), b) for t, b in zip((cache.k, cache.v), before))
+    kk, vv = sv.kv_gather(cache, skip_seq, skip_pos)
+    assert not kk.any() and not vv.any()
+    seq, pos = _i32([0] * n), _i32(list(range(n)))
+    sv.kv_append(cache, k, v, seq, pos)
+    y, _ = sv.kv_gather(cache, seq, pos, dtype=torch.float32)
+    assert not y[0].any()
+    assert torch.isnan(y[1:4]).all()              # an infinity, a NaN, past 448 * 2^60
+    assert not y[4].any()                         # under 2^-70
+    assert y[5, 0, 0] == 448.0
+    assert torch.isfinite(y[5:]).all()
+
+
+def test_gather_one_side_of_nan_and_strided_pool():
+    """k and v interleaved in one buffer [pages][2]...: a page stride twice a page."""
+    g = _gen(9)
+    both = _randn(g, 6, 2, 2, 16, 64).bfloat16()
+    table = _i32([[5, 0], [2, 2]])                # a shared page
+    cache = sv.KVCache(both[:, 0], both[:, 1], table)
+    seq, pos = _i32([0, 0, 1, 1]), _i32([3, 20, 3, 19])
+    k, v = sv.kv_gather(cache, seq, pos)
+    for i, (p, s) in enumerate([(5, 3), (0, 4), (2, 3), (2, 3)]):
+        assert torch.equal(k[i], both[p, 0, :, s]) and torch.equal(v[i], both[p, 1, :, s])
+
+
+# --------------------------------------------------------------- attention
+def _attend_ref(q, ks, vs, n, scale):
+    """Rows q [n, hq, d] over keys ks, vs [keys, hk, d] in 64 bits: out, lse and
+    the bounds' sums (sum w|v|, largest scale sum|q k|)."""
+    keys, hk, _ = ks.shape
+    hq = q.shape[1]
+    rep = hq // hk
+    q, ks, vs = q.to(F64), ks.to(F64).repeat_interleave(rep, 1), vs.to(F64).repeat_interleave(rep, 1)
+    if keys == 0:
+        z = torch.zeros_like(q)
+        return z, torch.full(q.shape[:2], -math.inf, dtype=F64, device="cuda"), z, torch.zeros(1, 1, 1, device="cuda")
+    s = torch.einsum("nhd,khd->hnk", q, ks) * scale
+    size = torch.einsum("nhd,khd->hnk", q.abs(), ks.abs()) * scale
+    see = torch.arange(keys, device="cuda")[None] <= (keys - n + torch.arange(n, device="cuda"))[:, None]
+    s = s.masked_fill(~see, -math.inf)
+    lse = torch.logsumexp(s, -1)
+    w = torch.where(see, torch.exp(s - lse.clamp_min(-1e300).unsqueeze(-1)), torch.zeros_like(s))
+    dot = size.masked_fill(~see, 0).amax(-1)
+    return (torch.einsum("hnk,khd->nhd", w, vs), lse.T, torch.einsum("hnk,khd->nhd", w, vs.abs()), dot.T.unsqueeze(-1))
+
+
+def _check_rows(out, lse, ref, keys, d):
+    o, l, wv, dot = ref
+    assert torch.isfinite(out).all()
+    delta = (d + 8) * 2.0 ** -24 * dot
+    tol = (2.0 ** -8 + 4 * delta + keys * 2.0 ** -23 + 2.0 ** -20) * wv + 2.0 ** -8 * o.abs() + 1e-30
+    err = (out.to(F64) - o).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    none = torch.isinf(l)
+    assert torch.equal(none, torch.isinf(lse)) and (lse[none] < 0).all()
+    lt = 2 * delta.expand(*l.shape, 1)[..., 0] + keys * 2.0 ** -23 + 2.0 ** -20 + l.abs() * 2.0 ** -22
+    assert ((lse.to(F64) - l).abs()[~none] <= lt[~none]).all()
+
+
+def _paged_case(seed, hq, hk, hd, ps, dtype, ns, lens, pad=0, poison=True, sharp=1.0):
+    """A cache whose slots past the lengths hold NaN, its queries and its rows' values."""
+    g = _gen(seed)
+    seqs = len(ns)
+    cache = _cache(g, seqs, max(max(lens), 1), hk, ps, hd, dtype)
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).fill_(0x7f) if dtype == "e4m3" else t.fill_(math.nan if poison else 0.0)
+    if dtype == "e4m3":
+        cache.k_scale.fill_(255)
+        cache.v_scale.fill_(255)
+    rows = [(b, p) for b, c in enumerate(lens) for p in range(c)]
+    if rows:
+        seq, pos = _i32([r[0] for r in rows]), _i32([r[1] for r in rows])
+        sv.kv_append(cache, _randn(g, len(rows), hk, hd) * sharp, _randn(g, len(rows), hk, hd), seq, pos)
+    cu = [0]
+    for n in ns:
+        cu.append(cu[-1] + n)
+    q = _randn(g, cu[-1] + pad, hq + 1, hd).bfloat16()[:, :hq]
+    return cache, q, _i32(cu), _i32(lens)
+
+
+def _paged_check(cache, q, cu, lens, ns, ctx, max_q=None, **kw):
+    hd = q.shape[2]
+    out = torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    got = sv.attn_paged(q, cache, cu, lens, max_q=max_q, out=out, lse=lse, **kw)
+    assert got[0] is out and got[1] is lse
+    values = _values(cache)
+    r = 0
+    for b, (n, c) in enumerate(zip(ns, ctx)):
+        pos = torch.arange(c, device="cuda").int()
+        k, v = _read(cache, values, torch.full_like(pos, b), pos)
+        _check_rows(out[r:r + n], lse[r:r + n], _attend_ref(q[r:r + n], k, v, n, kw.get("scale") or hd ** -0.5), c, hd)
+        r += n
+    assert (out[r:] == 7.0).all() and (lse[r:] == 9.0).all()
+    return out
+
+
+PAGED = [  # hq, hk, hd, page, new tokens, contexts
+    (32, 8, 128, 16, [6], [512]),
+    (32, 8, 128, 16, [6, 6, 6], [513, 47, 1000]),
+    (32, 8, 64, 32, [1] * 5, [1, 2, 16, 17, 3000]),
+    (8, 2, 32, 16, [5, 1, 9], [5, 333, 64]),
+    (4, 4, 64, 64, [1, 17, 16], [129, 17, 700]),
+    (7, 1, 128, 32, [3, 5], [300, 5]),                # seven heads on one, odd row tiles
+    (12, 4, 128, 256, [2, 0, 4], [40, 10, 600]),      # a sequence without new tokens
+    (8, 2, 64, 16, [4, 3, 2], [2, 0, 1]),             # chunks longer than their contexts: empty rows
+    (16, 2, 128, 16, [8], [8]),
+    (2, 2, 64, 16, [1], [20000]),
+    (32, 8, 128, 16, [40, 3], [200, 300]),
+    (8, 2, 64, 64, [130, 257, 1], [500, 257, 100]),
+    (32, 8, 128, 32, [129], [1500]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hk,hd,ps,ns,ctx", PAGED)
+def test_attn_paged(hq, hk, hd, ps, ns, ctx, dtype):
+    c, q, cu, lens = _paged_case(sum(ctx) + hd, hq, hk, hd, ps, dtype, ns, ctx, pad=2)
+    _paged_check(c, q, cu, lens, ns, ctx)
+    _paged_check(c, q, cu, lens, ns, ctx, max_q=max(ns))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 70])
+def test_attn_paged_sharp_scores(dtype, n):
+    """Scores of +-hundreds: the exponents' reference moves all along the keys."""
+    c, q, cu, lens = _paged_case(5, 8, 2, 64, 16, dtype, [n], [900], sharp=30.0)
+    _paged_check(c, q, cu, lens, [n], [900])
+    _paged_check(c, q, cu, lens, [n], [900], scale=0.01)
+
+
+@pytest.mark.parametrize("n", [1, 6, 100])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attn_paged_subnormal_codes(hd, n):
+    """Rows whose largest value no query sees: all that counts are e4m3's subnormal codes."""
+    g = _gen(n)
+    hq, hk, ctx = 8, 2, 200
+    cache = _cache(g, 1, ctx, hk, 16, hd, "e4m3")
+    k, v = (torch.randint(-7, 8, (ctx, hk, hd), generator=g, device="cuda").float() * 2.0 ** -9 for _ in range(2))
+    k[..., 0] = v[..., 0] = 448.0
+    pos = torch.arange(ctx, device="cuda").int()
+    sv.kv_append(cache, k, v, torch.zeros_like(pos), pos)
+    q = (_randn(g, n, hq, hd) * 64).bfloat16()
+    q[..., 0] = 0
+    kk, vv = sv.kv_gather(cache, torch.zeros_like(pos), pos, dtype=torch.float32)
+    assert torch.equal(kk, k) and torch.equal(vv, v)
+    out, lse = sv.attn_paged(q, cache, _i32([0, n]), _i32([ctx]))
+    _check_rows(out, lse, _attend_ref(q, k, v, n, hd ** -0.5), ctx, hd)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd,n,g", [(64, 3, 2), (128, 6, 4), (128, 64, 4), (64, 200, 2)])
+def test_attn_paged_batch_and_bad_indices(dtype, hd, n, g):
+    """Many sequences of different lengths; table entries outside the pool read as
+    zero rows, lengths past the table are cut, a broken cu row computes nothing."""
+    seqs = 21 if n < 10 else 3
+    ctx = [max(n, (37 * b * b) % 700) for b in range(seqs)]
+    ns = [n] * seqs
+    c, q, cu, lens = _paged_case(hd + n, 2 * g, 2, hd, 16, dtype, ns, ctx)
+    _paged_check(c, q, cu, lens, ns, ctx, max_q=n)
+    b = max(range(seqs), key=lambda i: ctx[i])
+    for bad in (-3, c.k.shape[0], 2 ** 30):
+        table = c.table.clone()
+        t2 = table.clone()
+        t2[b, 1] = bad
+        c.table.copy_(t2)
+        out, lse = sv.attn_paged(q, c, cu, lens, max_q=n)
+        c.table.copy_(table)
+        pos = torch.arange(ctx[b], device="cuda").int()
+        k, v = _read(c, _values(c), torch.full_like(pos, b), pos)
+        k[16:32], v[16:32] = 0, 0
+        rows = slice(b * n, b * n + n)
+        _check_rows(out[rows], lse[rows], _attend_ref(q[rows], k, v, n, hd ** -0.5), ctx[b], hd)
+    cap = c.max_pages * 16
+    cut = lens.clone()
+    cut[b] = 2 ** 31 - 1
+    if ctx[b] == cap:
+        out, _ = sv.attn_paged(q, c, cu, lens)
+        out2, _ = sv.attn_paged(q, c, cu, cut)
+        assert torch.equal(out, out2)
+    neg = lens.clone()
+    neg[:] = -5
+    out, lse = sv.attn_paged(q, c, cu, neg)
+    assert not out.any() and torch.isinf(lse).all()
+    broken = cu.clone()
+    broken[1] = 10 ** 9
+    keep = torch.full_like(q, 3.0, memory_format=torch.contiguous_format)
+    out, _ = sv.attn_paged(q, c, broken, lens, out=keep)
+    assert (out[:2 * n] == 3.0).all()
+
+
+def test_attn_paged_max_q_leaves_rows():
+    c, q, cu, lens = _paged_case(4, 8, 2, 64, 16, "bf16", [5, 2], [50, 60])
+    full, _ = sv.attn_paged(q, c, cu, lens)
+    out = torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
+    sv.attn_paged(q, c, cu, lens, max_q=3, out=out, lse=False)
+    assert torch.equal(out[:3], full[:3]) and (out[3:5] == 7.0).all() and torch.equal(out[5:], full[5:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 100])
+def test_attn_paged_repeats_streams_and_graphs(dtype, n):
+    """The same bits again, on another stream, and replayed from two graphs at once."""
+    c, q, cu, lens = _paged_case(11, 32, 8, 128, 16, dtype, [n, n], [2000, 900 + n])
+    out, lse = sv.attn_paged(q, c, cu, lens, max_q=n)
+    for _ in range(3):
+        a, b = sv.attn_paged(q, c, cu, lens, max_q=n)
+        assert torch.equal(a, out) and torch.equal(b, lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    for _ in range(2):
+        o = torch.zeros_like(out)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            sv.attn_paged(q, c, cu, lens, max_q=n, out=o, lse=False)
+            side.synchronize()
+            o.zero_()
+            with torch.cuda.graph(gr, stream=side):
+                sv.attn_paged(q, c, cu, lens, max_q=n, out=o, lse=False)
+        graphs.append(gr)
+        outs.append(o)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graphs[0].replay()
+    with torch.cuda.stream(other):
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out) for o in outs)
+    # a replayed graph reads the lengths of the day
+    lens.copy_(_i32([1000, 500 + n]))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], sv.attn_paged(q, c, cu, lens, max_q=n)[0])
+
+
+PROMPT = [  # hq, hk, hd, lengths
+    (8, 2, 64, [130, 1, 77]),
+    (32, 8, 128, [17]),
+    (8, 2, 32, [100, 33]),
+    (7, 1, 128, [64, 0, 65, 200]),
+    (12, 4, 64, [600, 129, 3]),
+    (4, 4, 128, [1025]),
+    (32, 8, 128, [900, 1500]),
+    (16, 2, 64, [2000]),
+]
+
+
+@pytest.mark.parametrize("hq,hk,hd,ns", PROMPT)
+def test_attn_prompt(hq, hk, hd, ns):
+    g = _gen(sum(ns))
+    total = sum(ns)
+    x = _randn(g, total + 3, hq + 2 * hk, hd).bfloat16()
+    x[total:] = math.nan                          # rows behind the last sequence
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    cu = [0]
+    for n in ns:
+        cu.append(cu[-1] + n)
+    for bound in (None, max(ns)):
+        out = torch.full((total + 3, hq, hd), 7.0, device="cuda", dtype=torch.bfloat16)
+        lse = torch.full((total + 3, hq), 9.0, device="cuda")
+        sv.attn_prompt(q, k, v, _i32(cu), max_len=bound, out=out, lse=lse)
+        for b, n in enumerate(ns):
+            r = slice(cu[b], cu[b + 1])
+            if n:
+                _check_rows(out[r], lse[r], _attend_ref(q[r], k[r], v[r], n, hd ** -0.5), n, hd)
+        assert (out[total:] == 7.0).all() and (lse[total:] == 9.0).all()
+
+
+def test_prompt_neighbours_do_not_leak():
+    """A sequence that holds NaN leaves its neighbours alone."""
+    g = _gen(2)
+    for ns in ([40, 50, 30], [300, 333, 290]):
+        x = _randn(g, sum(ns), 4, 64).bfloat16()
+        cu = _i32([0, ns[0], ns[0] + ns[1], sum(ns)])
+        q, k, v = x[:, :2], x[:, 2:3], x[:, 3:]
+        ref, _ = sv.attn_prompt(q, k, v, cu)
+        x[ns[0]:ns[0] + ns[1]] = math.nan
+        out, _ = sv.attn_prompt(q, k, v, cu)
+        assert torch.equal(out[:ns[0]], ref[:ns[0]]) and torch.equal(out[ns[0] + ns[1]:], ref[ns[0] + ns[1]:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd,ps", [(128, 16), (64, 64)])
+def test_decode_loop(dtype, hd, ps):
+    """The operators as a program runs them together: prompts packed and written,
+    then verify steps of 4 tokens and a plain one, all against one 64-bit run."""
+    g = _gen(hd)
+    hq, hk = 8, 2
+    prompts = [37, 90]
+    ctx = 160
+    cache = _cache(g, 2, ctx, hk, ps, hd, dtype)
+    plan = sv.rope_plan(hd, 500000.0)
+    freqs = _freqs(hd, 500000.0)
+    lens = [0, 0]
+    for chunk in (prompts, [4, 4], [1, 1], [4, 0], [64, 3]):
+        n = sum(chunk)
+        qkv = _randn(g, n, hq + 2 * hk, hd).bfloat16()
+        seq = _i32([b for b in range(2) for _ in range(chunk[b])])
+        pos = _i32([lens[b] + i for b in range(2) for i in range(chunk[b])])
+        q = sv.rope_rows(qkv[:, :hq], pos, plan)
+        sv.kv_append(cache, qkv[:, hq:hq + hk], qkv[:, hq + hk:], seq, pos, plan)
+        qref, qsize = _rope_ref(qkv[:, :hq], pos, freqs, False)
+        assert ((q.to(F64) - qref).abs() <= qsize * 2.0 ** -19 + qref.abs() * 2.0 ** -8).all()
+        kref, ksize = _rope_ref(qkv[:, hq:hq + hk], pos, freqs, False)
+        kk, vv = sv.kv_gather(cache, seq, pos, dtype=torch.float32)
+        if dtype == "bf16":
+            assert ((kk.to(F64) - kref).abs() <= ksize * 2.0 ** -19 + kref.abs() * 2.0 ** -8).all()
+            assert torch.equal(vv, qkv[:, hq + hk:].float())
+        else:
+            assert ((kk.to(F64) - kref).abs() <= ksize * 2.0 ** -19 + kref.abs() * 2.0 ** -4 + kref.abs().amax(-1, keepdim=True) * 2.0 ** -16).all()
+        lens = [a + b for a, b in zip(lens, chunk)]
+        cu = _i32([0, chunk[0], n])
+        _paged_check(cache, q, cu, _i32(lens), chunk, lens, max_q=max(chunk))
+        if lens == prompts and dtype == "bf16":   # the prompt form of the same rows
+            k16 = kk.bfloat16()
+            out, lse = sv.attn_prompt(q, k16, vv.bfloat16(), cu)
+            for r, c in ((slice(0, chunk[0]), chunk[0]), (slice(chunk[0], n), chunk[1])):
+                _check_rows(out[r], lse[r], _attend_ref(q[r], k16[r], vv[r], c, hd ** -0.5), c, hd)
