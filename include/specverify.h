@@ -432,7 +432,7 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * rows past a sequence's first max_q (a bound on the chunks' lengths, sizing
  * the grid), are left as they were.  A length past the table's positions is cut
  * there; a table entry that is not a page of the pool reads as zero rows.
- * scale 0: 1/sqrt(head_dim).  Scores, softmax statistics and sums are fp32,
+ * scale >= 0; 0: 1/sqrt(head_dim).  Scores, softmax statistics and sums are fp32,
  * probabilities bf16 in the product with v.  Cache slots past a sequence's
  * length are never used, whatever they hold; a value row that is not finite
  * within the length reaches the outputs of the whole chunk.

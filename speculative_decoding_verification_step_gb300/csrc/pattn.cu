@@ -508,7 +508,7 @@ cudaError_t launch_pa(const PAttn& a, int num_sms, cudaStream_t st) {
   const int64_t items = (int64_t)a.seqs * tpq;
   // blocks of a cluster: until every SM has about one and a half, with at
   // least 64 keys (four steps a block, one per warp) of the longest context each
-  const int64_t max_keys = a.paged ? (int64_t)a.max_pages << a.page_shift : std::min(a.max_q, a.tokens);
+  const int64_t max_keys = a.paged ? (int64_t)a.max_pages << a.page_shift : rows / G;
   int C = 1;
   while (C < 8 && items * a.hkv * C * 2 < 3LL * num_sms && max_keys >= 128 * C) C *= 2;
   if (items * C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -536,7 +536,8 @@ int run_attention(PAttn& a, const char* who, cudaStream_t st) {
     return fail(SPEC_E_SHAPE, w + "n_heads must be a multiple of n_kv_heads (at most 1024)");
   if (a.hd != 32 && a.hd != 64 && a.hd != 128) return fail(SPEC_E_SHAPE, w + "head_dim must be 32, 64 or 128");
   if (a.tokens < 0 || a.max_q < 0 || a.seqs < 1) return fail(SPEC_E_ARG, w + "bad tokens, bound or seqs");
-  if (!(a.scale_log2 == a.scale_log2) || std::isinf(a.scale_log2)) return fail(SPEC_E_ARG, w + "scale must be finite");
+  if (!(a.scale_log2 == a.scale_log2) || std::isinf(a.scale_log2) || a.scale_log2 < 0.f)
+    return fail(SPEC_E_ARG, w + "scale must be finite and not negative");
   if ((int64_t)a.tokens * (a.hq / a.hkv) > 0x7fffffffLL) return fail(SPEC_E_ARG, w + "too many rows");
   if (a.tokens == 0 || a.max_q == 0) return SPEC_OK;
   if (!a.q || !a.out || !a.cu) return fail(SPEC_E_ARG, w + "null pointer");
@@ -548,7 +549,16 @@ int run_attention(PAttn& a, const char* who, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
+  // Sequences of at most kPaMaxRows rows per KV head go to the register-tile
+  // kernel, longer chunks to the tensor-memory one where it applies; a batch
+  // that may hold both kinds launches both, each skipping the other's.
+  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv);
   a.max_rows = INT_MAX;
+  if (rows > kPaMaxRows && pattn_tc_supported(a)) {
+    a.max_rows = kPaMaxRows;
+    e = launch_pattn_tc(a, sms, st);
+    if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
+  }
   e = a.hd == 32 ? launch_pa_hd<32>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64>(a, sms, st) : launch_pa_hd<128>(a, sms, st);
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
 }

@@ -81,7 +81,7 @@ def test_attention_refusals(L):
                                         k.get("out", P), 256, k.get("oh", 64), None, None)
     assert att(q=None) == att(cu=None) == att(lens=None) == att(out=None) == -1
     assert att(q=P + 2) == att(qs=260) == att(oh=4) == att(n=-1) == att(m=-1) == -1
-    assert att(scale=math.nan) == att(scale=math.inf) == -1
+    assert att(scale=math.nan) == att(scale=math.inf) == att(scale=-1.0) == -1
     assert att(h=3) == att(h=0) == -3
     assert att(n=0) == att(m=0) == 0
     pr = lambda **k: L.spec_attn_prompt(k.get("q", P), 256, 64, k.get("k", P), 128, 64, k.get("v", P), k.get("vs", 128),
