@@ -434,38 +434,62 @@ def sample_rows(logits, temperature, seed, step_base=0, position=1, stream=None,
 
 # ---- paged-cache operators (see include/specverify.h) ----
 # The calls run on the current stream of the tensors' device (or the raw
-# stream given), with that device current; tensors are read by pointer.
+# stream given), with that device current; tensors are read by pointer.  A
+# step makes a call per layer and waits for none, so the checks are plain
+# comparisons, and messages are made only where one fails.
+_t = None
+
+
+def _torch():
+    global _t
+    if _t is None:
+        import torch
+        _t = torch
+    return _t
+
+
+def _refuse(msg):
+    raise SpecError(-1, msg)
+
+
 def _need(ok, msg):
     if not ok:
-        raise SpecError(-1, msg)
+        _refuse(msg)
 
 
 def _io_dtype(t):
-    import torch
-    _need(t.dtype in (torch.float32, torch.bfloat16), f"rows are fp32 or bf16, not {t.dtype}")
-    return SPEC_DTYPE_F32 if t.dtype == torch.float32 else SPEC_DTYPE_BF16
+    d = t.dtype
+    if d is _t.bfloat16:
+        return SPEC_DTYPE_BF16
+    if d is _t.float32:
+        return SPEC_DTYPE_F32
+    _refuse(f"rows are fp32 or bf16, not {d}")
 
 
 def _rows3(name, t):
-    _need(t.is_cuda and t.dim() == 3, f"{name}: a CUDA tensor [tokens, heads, head_dim]")
+    """Strides of a CUDA tensor [tokens, heads, head_dim]."""
+    if not t.is_cuda or t.dim() != 3:
+        _refuse(f"{name}: a CUDA tensor [tokens, heads, head_dim]")
     st = t.stride()
-    _need(st[2] == 1 or t.shape[2] == 1 or t.numel() == 0, f"{name}: the elements of a head must be adjacent")
+    if st[2] != 1 and t.shape[2] != 1 and t.numel():
+        _refuse(f"{name}: the elements of a head must be adjacent")
     return st
 
 
-def _index(name, t, n, device):
-    import torch
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.device == device and t.is_contiguous(),
-          f"{name}: a contiguous int32 tensor of {n} on the rows' device")
+def _index(name, t, n, dev):
+    if t.dtype is not _t.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"{name}: a contiguous int32 tensor of {n} on the rows' device")
 
 
-def _call(device, stream, fn, *args):
-    import torch
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+def _call(dev, stream, fn, *args):
+    # the C calls behind torch.cuda.current_device and current_stream, whose
+    # checks and objects cost more than the launch
+    c = _t._C
+    if c._cuda_getDevice() == dev:
+        rc = fn(*args, c._cuda_getCurrentRawStream(dev) if stream is None else stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+        with _t.cuda.device(dev):
+            rc = fn(*args, c._cuda_getCurrentRawStream(dev) if stream is None else stream)
     if rc:
         _check(rc)
 
@@ -500,6 +524,7 @@ class KVCache:
         self.n_kv_heads, self.head_dim, self.page_size = heads, hd, ps
         self.seqs, self.max_pages = table.shape
         self.device = k.device
+        self._dev = k.get_device()
         self._c = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if f8 else None,
                               v_scale.data_ptr() if f8 else None, SPEC_DTYPE_E4M3 if f8 else SPEC_DTYPE_BF16,
                               pages, ps, heads, hd, k.stride(0), k_scale.stride(0) if f8 else 0,
@@ -537,16 +562,20 @@ def rope_rows(x, pos, plan, out=None, dtype=None, inverse=False, stream=None):
     """x [tokens, heads, head_dim] (fp32 or bf16, strided) rotated by the
     positions pos [tokens] int32; returns out (given, may be x itself, or new
     in `dtype`, by default x's).  inverse rotates back."""
-    import torch
-    n, h, d = x.shape if x.dim() == 3 else (0, 0, 0)
+    _torch()
     xs = _rows3("x", x)
-    _index("pos", pos, n, x.device)
+    shape = x.shape
+    n, h, d = shape
+    dev = x.get_device()
+    _index("pos", pos, n, dev)
     if out is None:
-        out = torch.empty((n, h, d), dtype=x.dtype if dtype is None else dtype, device=x.device)
+        out = _t.empty(shape, dtype=x.dtype if dtype is None else dtype, device=x.device)
+        ys = out.stride()
     else:
-        _need(out.shape == x.shape and out.device == x.device and dtype in (None, out.dtype), "out: x's shape and device")
-    ys = _rows3("out", out)
-    _call(x.device, stream, lib().spec_rope_rows, x.data_ptr(), _io_dtype(x), xs[0], xs[1], out.data_ptr(),
+        if out.shape != shape or out.get_device() != dev or (dtype is not None and dtype is not out.dtype):
+            _refuse("out: x's shape and device")
+        ys = _rows3("out", out)
+    _call(dev, stream, lib().spec_rope_rows, x.data_ptr(), _io_dtype(x), xs[0], xs[1], out.data_ptr(),
           _io_dtype(out), ys[0], ys[1], pos.data_ptr(), n, h, d, plan._ref, 1 if inverse else 0)
     return out
 
@@ -555,44 +584,49 @@ def kv_append(cache, k, v, seq, pos, plan=None, stream=None):
     """Write rows k (rotated by plan, if given) and v [tokens, n_kv_heads,
     head_dim] to positions pos of sequences seq (int32 [tokens]; a negative
     one skips the row).  Positions of one call must be distinct."""
+    _torch()
     ks, vs = _rows3("k", k), _rows3("v", v)
-    n = k.shape[0]
-    _need(k.shape == v.shape and k.dtype == v.dtype and k.shape[1:] == (cache.n_kv_heads, cache.head_dim),
-          "k and v: equal [tokens, n_kv_heads, head_dim] of the cache")
-    _need(k.device == v.device == cache.device, "k, v and the cache must be on one device")
-    _index("seq", seq, n, cache.device)
-    _index("pos", pos, n, cache.device)
-    _call(cache.device, stream, lib().spec_kv_append, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
-          vs[1], _io_dtype(k), seq.data_ptr(), pos.data_ptr(), n, plan._ref if plan is not None else None)
+    shape, dev = k.shape, cache._dev
+    n, h, d = shape
+    if v.shape != shape or k.dtype is not v.dtype or h != cache.n_kv_heads or d != cache.head_dim:
+        _refuse("k and v: equal [tokens, n_kv_heads, head_dim] of the cache")
+    if k.get_device() != dev or v.get_device() != dev:
+        _refuse("k, v and the cache must be on one device")
+    _index("seq", seq, n, dev)
+    _index("pos", pos, n, dev)
+    _call(dev, stream, lib().spec_kv_append, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+          _io_dtype(k), seq.data_ptr(), pos.data_ptr(), n, plan._ref if plan is not None else None)
 
 
 def kv_gather(cache, seq, pos, dtype=None, stream=None):
     """(k, v) [tokens, n_kv_heads, head_dim] read back from positions pos of
     sequences seq, bf16 or fp32; rows that do not exist read as zeros."""
-    import torch
-    n = seq.shape[0]
-    _index("seq", seq, n, cache.device)
-    _index("pos", pos, n, cache.device)
-    k = torch.empty((n, cache.n_kv_heads, cache.head_dim), dtype=torch.bfloat16 if dtype is None else dtype,
-                    device=cache.device)
-    v = torch.empty_like(k)
-    _call(cache.device, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
+    _torch()
+    n, dev = seq.shape[0], cache._dev
+    _index("seq", seq, n, dev)
+    _index("pos", pos, n, dev)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    if dtype is None:
+        dtype = _t.bfloat16
+    k = _t.empty(shape, dtype=dtype, device=cache.device)
+    v = _t.empty(shape, dtype=dtype, device=cache.device)
+    _call(dev, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
           v.data_ptr(), _io_dtype(k))
     return k, v
 
 
-def _attn_out(q, out, lse):
-    import torch
-    _need(q.dtype == torch.bfloat16, f"q is bf16, not {q.dtype}")
+def _attn_out(q, shape, dev, out, lse):
+    if q.dtype is not _t.bfloat16:
+        _refuse(f"q is bf16, not {q.dtype}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == q.device, "out: like q")
+        out = _t.empty(shape, dtype=_t.bfloat16, device=q.device)
+    elif out.shape != shape or out.dtype is not _t.bfloat16 or out.get_device() != dev:
+        _refuse("out: like q")
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    elif lse is not False:
-        _need(lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.device == q.device and
-              lse.is_contiguous(), "lse: contiguous fp32 [tokens, heads]")
+        lse = _t.empty(shape[:2], dtype=_t.float32, device=q.device)
+    elif lse is not False and (lse.shape != shape[:2] or lse.dtype is not _t.float32 or lse.get_device() != dev or
+                               not lse.is_contiguous()):
+        _refuse("lse: contiguous fp32 [tokens, heads]")
     return out, lse
 
 
@@ -603,14 +637,17 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
     ones included (int32 [seqs + 1], [seqs]); max_q bounds the rows of one
     sequence (default: tokens).  Returns (out, lse [tokens, n_heads] fp32, or
     None with lse=False); rows outside every sequence are not written."""
+    _torch()
     qs = _rows3("q", q)
-    n, h, d = q.shape
-    _need(d == cache.head_dim and q.device == cache.device, "q must have the cache's head_dim and device")
-    _index("cu_q", cu_q, cache.seqs + 1, q.device)
-    _index("kv_lens", kv_lens, cache.seqs, q.device)
-    out, lse = _attn_out(q, out, lse)
+    shape, dev, seqs = q.shape, cache._dev, cache.seqs
+    n, h, d = shape
+    if d != cache.head_dim or q.get_device() != dev:
+        _refuse("q must have the cache's head_dim and device")
+    _index("cu_q", cu_q, seqs + 1, dev)
+    _index("kv_lens", kv_lens, seqs, dev)
+    out, lse = _attn_out(q, shape, dev, out, lse)
     os_ = _rows3("out", out)
-    _call(q.device, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
+    _call(dev, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
           kv_lens.data_ptr(), n, n if max_q is None else max_q, h, scale, out.data_ptr(), os_[0], os_[1],
           lse.data_ptr() if lse is not False else None)
     return out, (lse if lse is not False else None)
@@ -621,17 +658,23 @@ def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream
     [tokens, n_heads, head_dim] and k, v [tokens, n_kv_heads, head_dim] (bf16,
     may be slices of one projection) are sequence b; max_len bounds their
     lengths (default: tokens).  Returns (out, lse) as attn_paged."""
-    import torch
+    _torch()
     qs, ks, vs = _rows3("q", q), _rows3("k", k), _rows3("v", v)
-    n, h, d = q.shape
-    _need(k.shape == v.shape and k.shape[0] == n and k.shape[2] == d, "k and v: equal [tokens, n_kv_heads, head_dim]")
-    _need(k.dtype == v.dtype == torch.bfloat16, "k and v are bf16")
-    _need(k.device == v.device == q.device, "q, k and v must be on one device")
-    _need(cu.dim() == 1 and cu.shape[0] >= 2, "cu: int32 [sequences + 1]")
-    _index("cu", cu, cu.shape[0], q.device)
-    out, lse = _attn_out(q, out, lse)
+    shape, kshape, dev = q.shape, k.shape, q.get_device()
+    n, h, d = shape
+    if v.shape != kshape or kshape[0] != n or kshape[2] != d:
+        _refuse("k and v: equal [tokens, n_kv_heads, head_dim]")
+    if k.dtype is not _t.bfloat16 or v.dtype is not _t.bfloat16:
+        _refuse("k and v are bf16")
+    if k.get_device() != dev or v.get_device() != dev:
+        _refuse("q, k and v must be on one device")
+    seqs = cu.shape[0] - 1 if cu.dim() == 1 else 0
+    if seqs < 1:
+        _refuse("cu: int32 [sequences + 1]")
+    _index("cu", cu, seqs + 1, dev)
+    out, lse = _attn_out(q, shape, dev, out, lse)
     os_ = _rows3("out", out)
-    _call(q.device, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
-          v.data_ptr(), vs[0], vs[1], cu.data_ptr(), cu.shape[0] - 1, n, n if max_len is None else max_len, h,
-          k.shape[1], d, scale, out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None)
+    _call(dev, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+          v.data_ptr(), vs[0], vs[1], cu.data_ptr(), seqs, n, n if max_len is None else max_len, h, kshape[1], d,
+          scale, out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None)
     return out, (lse if lse is not False else None)

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <utility>
 
@@ -31,6 +32,29 @@ inline cudaError_t launch_rows(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// launch_rows of a kernel that needs `smem` bytes of dynamic shared memory.
+// The kernel's limit is a property of the device's context and is raised at
+// the first launch there (a call of about half the launch's own cost); a
+// launch that fails, as after a device reset, raises it again.
+template <typename Tag, typename... KArgs, typename... Args>
+inline cudaError_t launch_rows_smem(Tag, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                                    cudaStream_t st, Args&&... args) {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (raised.load(std::memory_order_relaxed) & bit) {
+    e = launch_rows(kernel, grid, block, smem, cluster, st, args...);
+    if (e != cudaErrorInvalidValue) return e;
+    (void)cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  raised.fetch_or(bit, std::memory_order_relaxed);
+  return launch_rows(kernel, grid, block, smem, cluster, st, args...);
 }
 
 // Checks of a cache description shared by the entry points; SPEC_OK or the

@@ -1,36 +1,43 @@
 // Attention of a sequence's newest tokens over its keys, for few rows per KV
 // head: a verify step's (K + 1) x G, one decoded token's G, a short prompt.
 //
-// With R = 16 or 32 rows per tile every key costs 4 R head_dim flops and
+// With R rows per tile a key costs 4 R head_dim flops against its
 // 2 head_dim elements of K and V: below ~64 rows the cache's bytes bound the
 // time, so a key is read once per tile, straight from its page into shared
 // memory, and everything else is arranged around keeping those reads going.
 //
-// Block = (row tile, KV head, share of the keys), four warps.  The keys are
-// walked in 16-key steps, step s on warp s mod 4.  Every warp keeps its own
-// ring of kDepth steps filled by 16-byte asynchronous copies (no block
+// Block = (row tile of 8 NT rows, KV head, share of the keys), four warps.
+// The keys are walked in 16-key steps, step s on warp s mod 4.  Every warp
+// keeps its own ring of steps filled by 16-byte asynchronous copies (no block
 // barrier in the walk), swizzled by row so that ldmatrix finds its eight rows
 // in distinct banks; rows past the length are filled with zeros, so whatever
 // those slots hold cannot reach a product.
-//   S = Q K^T and O += P V are m16n8k16 bf16 MMAs with fp32 sums, rows on the
-//   M side: an accumulator of S is, packed to bf16, the A operand of P V, so
-//   nothing is exchanged between lanes but the (rare) row maxima.
+//   S^T = K Q^T and O^T += V^T P^T: the keys (dims) are the 16-row side of the
+//   MMAs and the query rows the 8-column side, so that 4 or 24 rows waste
+//   little (24 rows: 3 column tiles, where rows on the 16-row side took 4),
+//   and the accumulators of 24 rows leave room for three blocks on an SM.
+//   P^T turns from an accumulator into an operand by transposing 8 x 8 blocks
+//   within the warp (movmatrix).  Q waits in shared memory in operand order.
 //   Online softmax with a lazy reference: a row's exponent reference only
 //   moves when a score exceeds it by more than 2^8, so the usual step has no
 //   shuffles and no rescaling of O; p <= 256 and the sums stay in fp32.
-//   Probabilities are rounded to bf16 for P V (relative 2^-9 each, of random
-//   sign: the same size as the output's own rounding); the row sum keeps them
-//   in fp32.
-// 8-bit keys and values: a byte's seven exponent and mantissa bits, moved to
-// bits 4..10 of a bf16 with the sign on top, are the bf16 number code *
-// 2^-120 exactly (subnormal codes too), two integer operations for two codes
-// instead of a conversion.  Q carries 2^60 of it (exact), the rest and the
-// row's power of two meet the scores in fp32, and those of V meet the
-// probabilities before their rounding.
-// The share of the keys: a cluster of up to 16 blocks splits one tile's keys
+//   Probabilities are rounded to bf16 for P V (half a step, 2^-9 of each on
+//   average, of random sign: the size of the output's own rounding); the row
+//   sum keeps them in fp32.
+// 8-bit keys and values become f16, which holds every code exactly, two codes
+// an instruction (the bit moves that make a bf16 of a code cost two and a half
+// times as much, measured, and an e4m3 mma.sync is itself emulated here: 37
+// clocks of an SM partition against 8).  Q rows are f16 too, scaled by a power
+// of two to just below 2^15: exact down to 2^-29 of the row's largest.  The
+// rows' powers of two meet the scores in fp32.  V's meet the probabilities
+// before their rounding to f16, against a reference exponent that keeps
+// usual products around 2^4 p and moves when one would pass 2^15, so that
+// neither large nor small rows leave f16's range.
+// The share of the keys: a cluster of up to 8 blocks splits one tile's keys
 // and merges through distributed shared memory in a fixed order (no scratch
 // memory, no second launch, no atomics): blocks merge their four warps, then
 // block j of the cluster finishes the rows j, j + C, ...
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,16 +56,26 @@ constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaStep = 16;          // keys of a step
 constexpr float kPaLazy = 8.f;       // exponent reference moves past 2^8
+constexpr int kPaVAt = 4;            // 8-bit values: exponent of a usual product with p = 1
 constexpr float kPaNone = -1e30f;    // reference of a row that has seen nothing
 
-template <int HD, bool F8>
+template <int HD, bool F8, int NT>
 struct PaLayout {
   static constexpr int row = HD * (F8 ? 1 : 2);      // bytes of a key row
   static constexpr int chunks = row / 16;
   static constexpr int tile = kPaStep * row;         // K or V of a step
   static constexpr int stage = 2 * tile + (F8 ? 32 : 0);
-  static constexpr int depth = F8 ? 6 : (HD >= 128 ? 3 : 4);
+  static constexpr int q_bytes = NT * 8 * HD * 2;    // Q in operand order: 16 bytes a lane hold two k slices
+  // blocks on an SM: as many as the accumulators allow (NT = 4: 128 of them)
+  static constexpr int blocks = NT == 4 && HD >= 128 ? 2 : 3;
+  static constexpr int room = (blocks == 2 ? 112 : 74) * 1024 - q_bytes;
+  static constexpr int fit = room / (kPaWarps * stage);
+  static constexpr int depth = fit > 6 ? 6 : fit;
+  static_assert(depth >= 2, "the ring holds the step in use and the next");
   static constexpr int ring = kPaWarps * depth * stage;
+  static constexpr int ld = HD + 4;                  // merge rows: odd multiples of 4 banks apart
+  static constexpr int merge = kPaWarps * NT * 8 * ld * 4;
+  static constexpr int smem = q_bytes + (ring > merge ? ring : merge);
   // Byte offset of 16-byte chunk c of row r: rows of less than 128 bytes
   // share a 128-byte line, so the row bits that vary over eight consecutive
   // lines are the ones to mix in.
@@ -68,11 +85,6 @@ struct PaLayout {
     return r * row + ((c ^ (x & m)) << 4);
   }
 };
-template <int HD, bool F8, int MT>
-constexpr int pa_smem() {
-  const int merge = kPaWarps * MT * 16 * HD * 4;
-  return PaLayout<HD, F8>::ring > merge ? PaLayout<HD, F8>::ring : merge;
-}
 
 SV_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -82,18 +94,40 @@ SV_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+// 8 x 8 block of 16-bit elements, two per lane, transposed within the warp.
+SV_DEV uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool F16>
+SV_DEV void pa_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    mma_bf16_16816_acc(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+// Four codes: the two of the lower half, and of the upper, as f16 pairs.
+SV_DEV void f8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
 SV_DEV float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+SV_DEV uint32_t pa_pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 SV_DEV uint32_t pa_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Codes in bytes 0, 2 (even) or 1, 3 (odd) of w as bf16 pairs code * 2^-120.
-SV_DEV uint32_t f8_even(uint32_t w) { return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u); }
-SV_DEV uint32_t f8_odd(uint32_t w) { return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u); }
 // 2^(byte - 127), NaN for 255.
 SV_DEV float f8_scale(uint32_t b) { return __uint_as_float(b == 255u ? 0x7fffffffu : b << 23); }
 
@@ -120,13 +154,14 @@ SV_DEV float4 ld_cluster_f32x4(uint32_t addr) {
 
 // Block x: tile (x / C) % tpq of sequence (x / C) / tpq, share x % C of its
 // keys; y: KV head.
-template <int HD, bool F8, int MT>
-__global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_constant__ PAttn a, int tpq, int C) {
-  using L = PaLayout<HD, F8>;
-  constexpr int kRows = MT * 16, kKs = HD / 16, kNt = HD / 8, D = L::depth;
+template <int HD, bool F8, int NT>
+__global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
+    pattn_kernel(const __grid_constant__ PAttn a, int tpq, int C) {
+  using L = PaLayout<HD, F8, NT>;
+  constexpr int kRows = NT * 8, kMt = HD / 16, D = L::depth;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ float s_m[kPaWarps][kRows], s_l[kPaWarps][kRows];
-  __shared__ float s_cm[kRows], s_cl[kRows];
+  __shared__ float s_cm[kRows], s_cl[kRows], s_qf[kRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   const int share = blockIdx.x % C, item = blockIdx.x / C;
   const int b = item / tpq, tile = item - b * tpq, kvh = blockIdx.y;
@@ -135,13 +170,9 @@ __global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_const
   // the sequence's rows and keys (every block of a cluster sees the same)
   const int r_first = __ldg(a.cu + b);
   const int n = __ldg(a.cu + b + 1) - r_first;
+  int keys = a.paged ? __ldg(a.lens + b) : n;
   if (r_first < 0 || n <= 0 || n > a.tokens - r_first || (int64_t)n * G > a.max_rows) return;
-  int keys = n;
-  if (a.paged) {
-    keys = __ldg(a.lens + b);
-    const int64_t cap = (int64_t)a.max_pages << a.page_shift;
-    keys = keys < 0 ? 0 : (int)min((int64_t)keys, cap);
-  }
+  if (a.paged) keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
   const int rows = min(n, a.max_q) * G;       // rows that are computed
   const int row0 = tile * kRows;
   if (row0 >= rows) return;
@@ -150,295 +181,340 @@ __global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_const
   const int see_max = min(keys, max(0, first_pos + last_row / G + 1));   // keys that any row of the tile sees
   const int see_all = first_pos + row0 / G + 1;                          // keys that every row sees
 
-  // Q fragments: lane's rows g and g + 8 of every 16-row tile.  8-bit keys:
-  // codes come as (even, odd) bytes of four neighbours, so Q's k order is
-  // permuted the same way, and carries 2^60.
-  uint32_t qa[MT][kKs][4];
-  int seen[MT][2];                            // keys seen by the lane's rows
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const int r = row0 + mt * 16 + g + 8 * hr;
-      const bool ok = r < rows;
-      const int t = ok ? r / G : 0;
-      seen[mt][hr] = ok ? min(keys, first_pos + t + 1) : 0;
-      const bf16* qr = (const bf16*)a.q + (int64_t)(r_first + t) * a.q_ts + (int64_t)(kvh * G + (ok ? r - t * G : 0)) * a.q_hs;
-#pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        uint32_t lo = 0, hi = 0;
-        if (ok) {
-          if constexpr (F8) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * q4));   // k 4q .. 4q + 3
-            lo = __byte_perm(w.x, w.y, 0x5410);   // (4q, 4q + 2)
-            hi = __byte_perm(w.x, w.y, 0x7632);   // (4q + 1, 4q + 3)
-            const __nv_bfloat162 up = __floats2bfloat162_rn(1152921504606846976.f, 1152921504606846976.f);   // 2^60
-            __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&lo), up);
-            __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&hi), up);
-            lo = *reinterpret_cast<uint32_t*>(&x);
-            hi = *reinterpret_cast<uint32_t*>(&y);
-          } else {
-            lo = __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * q4));
-            hi = __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * q4 + 8));
-          }
-        }
-        qa[mt][ks][hr] = lo;
-        qa[mt][ks][2 + hr] = hi;
-      }
-    }
-
-  float o[MT][kNt][4];
-  float m[MT][2], l[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-    for (int j = 0; j < kNt; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
-    m[mt][0] = m[mt][1] = kPaNone;
-    l[mt][0] = l[mt][1] = 0.f;
-  }
-
   // this block's steps, and the warp's: s0 + 4 j
   const int steps = (see_max + kPaStep - 1) / kPaStep;
   const int s_beg = (int)((int64_t)steps * share / C), s_end = (int)((int64_t)steps * (share + 1) / C);
   const int s0 = s_beg + warp;
   const int nj = s_end > s0 ? (s_end - s0 + kPaWarps - 1) / kPaWarps : 0;
-  unsigned char* ring = sm + (size_t)warp * D * L::stage;
+  unsigned char* ring = sm + L::q_bytes + (size_t)warp * D * L::stage;
   const uint32_t ring_u = smem_u32(ring);
   const int32_t* table = a.paged ? a.table + b * a.table_stride : nullptr;
-  const int64_t ps_mask = ((int64_t)1 << a.page_shift) - 1;
-  int pid = 0;   // lane i: page of the warp's step (j & ~31) + i
+  const int ps_mask = (1 << a.page_shift) - 1;
+  int pid = 0;   // lane i: page of the warp's step (j & ~31) + i (V's copies follow K's of the same step)
 
-  // copies of the warp's step j into its ring slot
-  auto issue = [&](int j) {
-    if (a.paged && (j & 31) == 0) {
+  // Copies of K (v = 0) or V (v = 1) of the warp's step j into its ring slot;
+  // one group each, so that the scores do not wait for V and K's slot is
+  // filled again as soon as they are done.
+  const uint32_t lane_at = (uint32_t)L::at(lane / L::chunks, lane % L::chunks);
+  auto issue = [&](int j, int v) {
+    if (a.paged && !v && (j & 31) == 0) {
       const int64_t key = (int64_t)(s0 + kPaWarps * (j + lane)) * kPaStep;
       pid = j + lane < nj ? __ldg(table + (key >> a.page_shift)) : -1;
     }
     if (j < nj) {
       const int key0 = (s0 + kPaWarps * j) * kPaStep;
       int valid = min(kPaStep, keys - key0);
-      const unsigned char *kp, *vp;
-      int64_t krs, vrs;
-      const uint8_t *ksp = nullptr, *vsp = nullptr;
+      const unsigned char* p;
+      const uint8_t* sp = nullptr;
       if (a.paged) {
         const int page = __shfl_sync(0xffffffffu, pid, j & 31);
         const bool in = page >= 0 && page < a.pages;
         if (!in) valid = 0;
         const int64_t row = ((int64_t)kvh << a.page_shift) + (key0 & ps_mask);
-        const int64_t off = ((in ? page : 0) * a.page_stride + row * HD) * (F8 ? 1 : 2);
-        kp = (const unsigned char*)a.k + off;
-        vp = (const unsigned char*)a.v + off;
-        krs = vrs = L::row;
-        if constexpr (F8) {
-          const int64_t so = (in ? page : 0) * a.scale_stride + row;
-          ksp = a.ks + so;
-          vsp = a.vs + so;
+        const int64_t pg = in ? page : 0;
+        p = (const unsigned char*)(v ? a.v : a.k) + (pg * a.page_stride + row * HD) * (F8 ? 1 : 2);
+        if constexpr (F8) sp = (v ? a.vs : a.ks) + pg * a.scale_stride + row;
+      } else {
+        p = (const unsigned char*)((const bf16*)(v ? a.v : a.k) + (int64_t)(r_first + key0) * (v ? a.v_ts : a.k_ts) +
+                                   (int64_t)kvh * (v ? a.v_hs : a.k_hs));
+      }
+      const uint32_t slot = (uint32_t)((j % D) * L::stage + v * L::tile);
+      if (a.paged && valid == kPaStep) {      // sixteen rows of a page lie one after the other
+        p += lane * 16;
+#pragma unroll
+        for (int i = 0; i < kPaStep * L::chunks / 32; ++i) {
+          // row i * per + lane / chunks: its swizzle bits are the lane's,
+          // changed by those of i * per (shorter rows: eight rows or more
+          // later the pattern repeats)
+          constexpr int per = 32 / L::chunks;
+          const uint32_t d = lane_at ^ (uint32_t)(per >= 8 ? 0 : ((i * per) & 7) << 4);
+          cp_async16(ring + slot + d + i * 512, p + i * 512, true);
         }
       } else {
-        kp = (const unsigned char*)((const bf16*)a.k + (int64_t)(r_first + key0) * a.k_ts + (int64_t)kvh * a.k_hs);
-        vp = (const unsigned char*)((const bf16*)a.v + (int64_t)(r_first + key0) * a.v_ts + (int64_t)kvh * a.v_hs);
-        krs = a.k_ts * 2;
-        vrs = a.v_ts * 2;
-      }
-      unsigned char* dst = ring + (j % D) * L::stage;
+        const int64_t rs = a.paged ? L::row : (v ? a.v_ts : a.k_ts) * 2;
 #pragma unroll
-      for (int i = 0; i < kPaStep * L::chunks / 32; ++i) {
-        const int e = i * 32 + lane, r = e / L::chunks, c = e % L::chunks;
-        const bool in = r < valid;
-        // rows past the length are not read: the source stays on row 0
-        cp_async16(dst + L::at(r, c), kp + (in ? r : 0) * krs + c * 16, in);
-        cp_async16(dst + L::tile + L::at(r, c), vp + (in ? r : 0) * vrs + c * 16, in);
+        for (int i = 0; i < kPaStep * L::chunks / 32; ++i) {
+          const int e = i * 32 + lane, r = e / L::chunks, c = e % L::chunks;
+          const bool in = r < valid;
+          // rows past the length are not read: the source stays on row 0
+          cp_async16(ring + slot + L::at(r, c), p + (in ? r : 0) * rs + c * 16, in);
+        }
       }
       if constexpr (F8) {
-        if (lane < 2) cp_async16(dst + 2 * L::tile + 16 * lane, lane ? vsp : ksp, valid > 0);
+        if (lane == 0) cp_async16(ring + (j % D) * L::stage + 2 * L::tile + 16 * v, sp, valid > 0);
       }
     }
     cp_async_commit();
   };
-
-  // ldmatrix rows of this lane: K (two key groups x two chunks) and V
-  const int lr = lane & 7, l8 = (lane >> 3) & 1, l16 = lane >> 4;
 #pragma unroll
-  for (int j = 0; j < D - 1; ++j) issue(j);
+  for (int j = 0; j < D; ++j) {
+    issue(j, 0);
+    issue(j, 1);
+  }
+
+  // Q into shared memory as B operands, [slice pair][column tile][lane] of 16
+  // bytes (two 16-element k slices of two words).  A lane's words hold
+  // elements 2 q, 2 q + 1 and 8 more; with 8-bit keys, whose four neighbours
+  // come in one word, elements 4 q .. 4 q + 3.
+  for (int r = warp; r < kRows; r += kPaWarps) {
+    const int R = row0 + r, t = R / G;
+    const bool ok = R < rows;
+    constexpr int kPer = HD / 32;             // elements of a lane: kPer lane .. + kPer - 1
+    const int k = kPer * lane;
+    const bf16* qr = (const bf16*)a.q + (int64_t)(r_first + (ok ? t : 0)) * a.q_ts +
+                     (int64_t)(kvh * G + (ok ? R - t * G : 0)) * a.q_hs + k;
+    float x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = ok ? __bfloat162float(qr[i]) : 0.f;
+    if constexpr (F8) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // 2^e: the row's largest lands in [2^14, 2^15); a row that is not finite scores NaN
+      const bool bad = m >= 0x7f800000u;
+      const int e = m == 0 || bad ? 0 : max((int)(m >> 23) - 127 - 14, -100);
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = bad ? 0.f : x[i] * f;
+      if (lane == 0)
+        s_qf[r] = bad ? __uint_as_float(0x7fffffffu) : fmaxf(__uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2, 1.2e-38f);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int kk = k + i, sl = kk >> 4, in = kk & 15;
+      const int quad = F8 ? in >> 2 : (in & 7) >> 1, word = F8 ? (in >> 1) & 1 : in >> 3;
+      unsigned char* d = sm + (((sl >> 1) * NT + (r >> 3)) * 32 + (r & 7) * 4 + quad) * 16 + (sl & 1) * 8 + word * 4 + (in & 1) * 2;
+      if constexpr (F8) *reinterpret_cast<__half*>(d) = __float2half_rn(x[i]);
+      else *reinterpret_cast<bf16*>(d) = __float2bfloat16_rn(x[i]);
+    }
+  }
+  __syncthreads();
+  int seen[NT][2];                            // the lane's rows: 8 nt + 2 q4, + 1
+  float qf[NT][2];                            // scores to units of log2
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * q4 + e, R = row0 + r;
+      seen[nt][e] = R < rows ? min(keys, first_pos + R / G + 1) : 0;
+      qf[nt][e] = F8 ? s_qf[r] : a.scale_log2;
+    }
+
+  float o[kMt][NT][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < kMt; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][nt][e] = 0.f;
+    m[nt][0] = m[nt][1] = kPaNone;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  const int lr = lane & 7, l8 = (lane >> 3) & 1, l16 = lane >> 4;
+  const uint4* qs = reinterpret_cast<const uint4*>(sm) + lane;
+  int vref = 0;                               // 8-bit values: O holds its sums over 2^vref
+  bool fresh = true;
   for (int j = 0; j < nj; ++j) {
-    cp_async_wait<D - 2>();
+    cp_async_wait<2 * D - 1>();
     __syncwarp();
     const int key0 = (s0 + kPaWarps * j) * kPaStep;
     const uint32_t kt = ring_u + (uint32_t)((j % D) * L::stage), vt = kt + L::tile;
-    float s[MT][2][4];
+    // scores: element e of column tile nt is key key0 + g + 8 (e / 2), row 8 nt + 2 q4 + (e & 1)
+    float s[NT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-    if constexpr (F8) {
+    for (int sl = 0; sl < kMt; sl += 2) {
+      uint32_t ka[2][4];                      // keys 0-7, 8-15 of a slice's first 8 elements, then of its last
+      if constexpr (F8) {
+        uint32_t w[4];                        // keys 0-7, 8-15 of chunk sl, then of sl + 1
+        ldsm4(w, kt + L::at(lr + 8 * l8, sl + l16));
 #pragma unroll
-      for (int c = 0; c < kKs; c += 2) {   // 16 codes a chunk: one k16 slice
-        uint32_t w[4];                     // keys 0-7 chunk c, c + 1; keys 8-15 chunk c, c + 1
-        ldsm4(w, kt + L::at(lr + 8 * l16, c + l8));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t b0 = f8_even(w[x]), b1 = f8_odd(w[x]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            mma_bf16_16816_acc(s[mt][x >> 1], qa[mt][c + (x & 1)][0], qa[mt][c + (x & 1)][1], qa[mt][c + (x & 1)][2],
-                               qa[mt][c + (x & 1)][3], b0, b1);
-        }
+        for (int x = 0; x < 4; ++x) f8_to_f16(w[x], ka[x >> 1][x & 1], ka[x >> 1][2 + (x & 1)]);
+      } else {
+        ldsm4(ka[0], kt + L::at(lr + 8 * l8, 2 * sl + l16));
+        ldsm4(ka[1], kt + L::at(lr + 8 * l8, 2 * sl + 2 + l16));
       }
-    } else {
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        uint32_t w[4];                     // keys 0-7 k 0-7, k 8-15; keys 8-15 k 0-7, k 8-15
-        ldsm4(w, kt + L::at(lr + 8 * l16, 2 * ks + l8));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816_acc(s[mt][0], qa[mt][ks][0], qa[mt][ks][1], qa[mt][ks][2], qa[mt][ks][3], w[0], w[1]);
-          mma_bf16_16816_acc(s[mt][1], qa[mt][ks][0], qa[mt][ks][1], qa[mt][ks][2], qa[mt][ks][3], w[2], w[3]);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 w = qs[((sl / 2) * NT + nt) * 32];
+        pa_mma<F8>(s[nt], ka[0], w.x, w.y);
+        pa_mma<F8>(s[nt], ka[1], w.z, w.w);
       }
     }
-    // scores in units of log2: key of element (nt, e) is key0 + 8 nt + 2 q4 + (e & 1)
-    float vs[2][2];
+    int ve[2] = {0, 0};
+    bool move = false;
     if constexpr (F8) {
       const unsigned char* sc = ring + (j % D) * L::stage + 2 * L::tile;
+      const float k0 = f8_scale(sc[g]), k1 = f8_scale(sc[g + 8]);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint32_t kb = *reinterpret_cast<const uint16_t*>(sc + 8 * nt + 2 * q4);
-        const uint32_t vb = *reinterpret_cast<const uint16_t*>(sc + 16 + 8 * nt + 2 * q4);
-        const float f = a.scale_log2 * 1152921504606846976.f;   // 2^60: codes carry 2^-120, Q 2^60
-        const float k0 = f8_scale(kb & 255u) * f, k1 = f8_scale(kb >> 8) * f;
-        vs[nt][0] = f8_scale(vb & 255u) * 1152921504606846976.f;
-        vs[nt][1] = f8_scale(vb >> 8) * 1152921504606846976.f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          s[mt][nt][0] *= k0; s[mt][nt][1] *= k1;
-          s[mt][nt][2] *= k0; s[mt][nt][3] *= k1;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= a.scale_log2;
+        for (int e = 0; e < 4; ++e) s[nt][e] *= e < 2 ? k0 : k1;
     }
-    if (key0 + kPaStep > see_all) {        // some row does not see all of the step
+    __syncwarp();
+    issue(j + D, 0);
+    const bool edge = key0 + kPaStep > see_all;   // some row does not see all of the step
+    if (edge) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key0 + 8 * nt + 2 * q4 + (e & 1) >= seen[mt][e >> 1]) s[mt][nt][e] = neg_inf();
+        for (int e = 0; e < 4; ++e)
+          if (key0 + g + 8 * (e >> 1) >= seen[nt][e & 1]) s[nt][e] = neg_inf();
     }
-    float top[MT][2];
-    bool move = false;
+    // exponents against the references
+    float x[NT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        top[mt][hr] = fmaxf(fmaxf(s[mt][0][2 * hr], s[mt][0][2 * hr + 1]), fmaxf(s[mt][1][2 * hr], s[mt][1][2 * hr + 1]));
-        move |= top[mt][hr] > m[mt][hr] + kPaLazy;
-      }
+      for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], qf[nt][e & 1], -m[nt][e & 1]);
+      move |= fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) > kPaLazy;
+    }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          float t = top[mt][hr];
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          t = fmaxf(t, m[mt][hr]);
-          const float f = exp2_fast(m[mt][hr] - t);
-          m[mt][hr] = t;
-          l[mt][hr] *= f;
+        for (int e = 0; e < 2; ++e) {
+          float t = fmaxf(s[nt][e], s[nt][e + 2]) * qf[nt][e];
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          t = fmaxf(t, m[nt][e]);
+          const float f = exp2_fast(m[nt][e] - t);
+          m[nt][e] = t;
+          l[nt][e] *= f;
 #pragma unroll
-          for (int jn = 0; jn < kNt; ++jn) {
-            o[mt][jn][2 * hr] *= f;
-            o[mt][jn][2 * hr + 1] *= f;
+          for (int mt = 0; mt < kMt; ++mt) {
+            o[mt][nt][e] *= f;
+            o[mt][nt][e + 2] *= f;
           }
+          x[nt][e] = fmaf(s[nt][e], qf[nt][e], -t);
+          x[nt][e + 2] = fmaf(s[nt][e + 2], qf[nt][e], -t);
         }
     }
-    uint32_t pa[MT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int e = 0; e < 4; ++e) x[nt][e] = exp2_fast(x[nt][e]);
+      l[nt][0] += x[nt][0] + x[nt][2];
+      l[nt][1] += x[nt][1] + x[nt][3];
+    }
+    cp_async_wait<2 * D - 1>();
+    __syncwarp();
+    uint32_t pb[NT][2];
+    if constexpr (F8) {
+      const unsigned char* sc = ring + (j % D) * L::stage + 2 * L::tile + 16;
+      ve[0] = sc[g];
+      ve[1] = sc[g + 8];
+      // p <= 2^8: products stay within 2^15 while the rows' exponents are at most 7 above vref;
+      // beyond, the products themselves decide
+      const bool high = fresh || max(ve[0], ve[1]) - 127 - vref > 7;
+      if (__any_sync(0xffffffffu, high)) {
+        int top = -1000;                      // exponent of the largest product over this step
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (x[nt][e] > 0.f && ve[e >> 1] != 255) top = max(top, (int)(__float_as_uint(x[nt][e]) >> 23) - 127 + ve[e >> 1] - 127);
+#pragma unroll
+        for (int of = 16; of > 0; of >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, of));
+        if (top > -1000 && (fresh || top - vref > 14)) {
+          const int to = top - kPaVAt;        // the largest product lands at 2^kPaVAt
+          const float f = fresh ? 0.f : exp2_fast((float)max(vref - to, -126));
+          if (!fresh) {
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f;
+          }
+          vref = to;
+          fresh = false;
+        }
+      }
+      // 2^(exponent - vref); a NaN row stays NaN
+      float vs[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        vs[e] = __uint_as_float(ve[e] == 255 ? 0x7fffffffu : (uint32_t)min(max(ve[e] - vref, 1), 254) << 23);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = exp2_fast(s[mt][nt][e] - m[mt][e >> 1]);
-        l[mt][0] += p[0] + p[1];
-        l[mt][1] += p[2] + p[3];
-        if constexpr (F8) {
+        for (int e = 0; e < 4; ++e) p[e] = x[nt][e] * vs[e >> 1];
+        if (edge) {                           // a row that does not see a NaN key or its huge scale takes nothing of it
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = p[e] == 0.f ? 0.f : p[e] * vs[nt][e & 1];
+          for (int e = 0; e < 4; ++e)
+            if (x[nt][e] == 0.f) p[e] = 0.f;
         }
-        pa[mt][2 * nt] = pa_pack(p[0], p[1]);
-        pa[mt][2 * nt + 1] = pa_pack(p[2], p[3]);
+        pb[nt][0] = transpose8(pa_pack_f16(p[0], p[1]));
+        pb[nt][1] = transpose8(pa_pack_f16(p[2], p[3]));
       }
-    }
-    if constexpr (F8) {
 #pragma unroll
-      for (int c = 0; c < kKs; c += 2) {   // chunks of 16 dims; keys 0-7, 8-15 of chunk c, then of c + 1
-        uint32_t w[4];
+      for (int c = 0; c < kMt; c += 2) {      // chunks of 16 dims: row g is dim 2 g, row g + 8 dim 2 g + 1
+        uint32_t w[4];                        // keys 0-7, 8-15 of chunk c, then of c + 1
         ldsm4t(w, vt + L::at(lr + 8 * l8, c + l16));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t e0 = f8_even(w[2 * x]), e1 = f8_even(w[2 * x + 1]);
-          const uint32_t d0 = f8_odd(w[2 * x]), d1 = f8_odd(w[2 * x + 1]);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t va[4];                     // two dims of two keys a word: dims apart, keys together
+          f8_to_f16(__byte_perm(w[2 * h], 0, 0x3120), va[0], va[1]);
+          f8_to_f16(__byte_perm(w[2 * h + 1], 0, 0x3120), va[2], va[3]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {   // even dims, odd dims of the chunk
-            mma_bf16_16816_acc(o[mt][2 * (c + x)], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], e0, e1);
-            mma_bf16_16816_acc(o[mt][2 * (c + x) + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], d0, d1);
-          }
+          for (int nt = 0; nt < NT; ++nt) pa_mma<true>(o[c + h][nt], va, pb[nt][0], pb[nt][1]);
         }
       }
     } else {
 #pragma unroll
-      for (int jn = 0; jn < kNt; jn += 2) {
-        uint32_t w[4];                     // keys 0-7, 8-15 of dims 8 jn ..; then of the next eight
-        ldsm4t(w, vt + L::at(lr + 8 * l8, jn + l16));
+      for (int nt = 0; nt < NT; ++nt) {
+        pb[nt][0] = transpose8(pa_pack(x[nt][0], x[nt][1]));
+        pb[nt][1] = transpose8(pa_pack(x[nt][2], x[nt][3]));
+      }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816_acc(o[mt][jn], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], w[0], w[1]);
-          mma_bf16_16816_acc(o[mt][jn + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], w[2], w[3]);
-        }
+      for (int mt = 0; mt < kMt; ++mt) {
+        uint32_t w[4];                        // keys 0-7 of dims 0-7, 8-15; keys 8-15 of the same
+        ldsm4t(w, vt + L::at(lr + 8 * l16, 2 * mt + l8));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) pa_mma<false>(o[mt][nt], w, pb[nt][0], pb[nt][1]);
       }
     }
     __syncwarp();
-    issue(j + D - 1);
+    issue(j + D, 1);
   }
   cp_async_wait<0>();
   __syncthreads();   // the rings become the merge area
 
-  // ---- merge of the four warps: [warp][row][HD] ----
-  float* part = reinterpret_cast<float*>(sm);
+  // ---- merge of the four warps: [warp][row][ld] ----
+  float* part = reinterpret_cast<float*>(sm + L::q_bytes);
+  const float vf = F8 ? exp2f((float)vref) : 1.f;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      float t = l[mt][hr];
-      t += __shfl_xor_sync(0xffffffffu, t, 1);
-      t += __shfl_xor_sync(0xffffffffu, t, 2);
-      const int r = mt * 16 + g + 8 * hr;
-      if (q4 == 0) {
-        s_m[warp][r] = m[mt][hr];
+    for (int e = 0; e < 2; ++e) {
+      float t = l[nt][e];
+      t += __shfl_xor_sync(0xffffffffu, t, 4);
+      t += __shfl_xor_sync(0xffffffffu, t, 8);
+      t += __shfl_xor_sync(0xffffffffu, t, 16);
+      const int r = nt * 8 + 2 * q4 + e;
+      if (g == 0) {
+        s_m[warp][r] = m[nt][e];
         s_l[warp][r] = t;
       }
-      float* d = part + ((size_t)warp * kRows + r) * HD;
-      if constexpr (F8) {
+      float* d = part + ((size_t)warp * kRows + r) * L::ld;
 #pragma unroll
-        for (int c = 0; c < kKs; ++c)   // dims 4 q4 .. + 3 of chunk c
-          *reinterpret_cast<float4*>(d + c * 16 + 4 * q4) =
-              make_float4(o[mt][2 * c][2 * hr], o[mt][2 * c + 1][2 * hr], o[mt][2 * c][2 * hr + 1], o[mt][2 * c + 1][2 * hr + 1]);
-      } else {
-#pragma unroll
-        for (int jn = 0; jn < kNt; ++jn)
-          *reinterpret_cast<float2*>(d + jn * 8 + 2 * q4) = make_float2(o[mt][jn][2 * hr], o[mt][jn][2 * hr + 1]);
+      for (int mt = 0; mt < kMt; ++mt) {
+        if constexpr (F8) {
+          *reinterpret_cast<float2*>(d + mt * 16 + 2 * g) = make_float2(o[mt][nt][e] * vf, o[mt][nt][e + 2] * vf);
+        } else {
+          d[mt * 16 + g] = o[mt][nt][e];
+          d[mt * 16 + g + 8] = o[mt][nt][e + 2];
+        }
       }
     }
   __syncthreads();
@@ -446,7 +522,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_const
   const int col = (tid % kLpr) * 4;
   auto write_row = [&](int r, float4 x, float mm, float ll) {
     const int R = row0 + r, t = R / G, h = kvh * G + R - t * G;
-    const float f = ll > 0.f || !(ll == ll) ? (F8 ? 1152921504606846976.f : 1.f) / ll : 0.f;
+    const float f = ll > 0.f || !(ll == ll) ? 1.f / ll : 0.f;
     bf16* d = (bf16*)a.out + (int64_t)(r_first + t) * a.o_ts + (int64_t)h * a.o_hs + col;
     *reinterpret_cast<uint2*>(d) = make_uint2(pa_pack(x.x * f, x.y * f), pa_pack(x.z * f, x.w * f));
     if (a.lse && col == 0)
@@ -461,14 +537,14 @@ __global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_const
 #pragma unroll
     for (int w = 0; w < kPaWarps; ++w) {
       const float f = exp2_fast(s_m[w][r] - mm);
-      const float4 y = *reinterpret_cast<const float4*>(part + ((size_t)w * kRows + r) * HD + col);
+      const float4 y = *reinterpret_cast<const float4*>(part + ((size_t)w * kRows + r) * L::ld + col);
       ll += s_l[w][r] * f;
       x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
     }
     if (C == 1) {
       write_row(r, x, mm, ll);
     } else {
-      *reinterpret_cast<float4*>(part + (size_t)r * HD + col) = x;   // warp 0's slot of this element, read above
+      *reinterpret_cast<float4*>(part + (size_t)r * L::ld + col) = x;   // warp 0's slot of this element, read above
       if (col == 0) {
         s_cm[r] = mm;
         s_cl[r] = ll;
@@ -486,7 +562,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_const
 #pragma unroll 4
     for (int c = 0; c < C; ++c) {
       const float f = exp2_fast(ld_cluster_f32(cluster_map(mu + 4 * r, c)) - mm);
-      const float4 y = ld_cluster_f32x4(cluster_map(pu + (uint32_t)(r * HD + col) * 4, c));
+      const float4 y = ld_cluster_f32x4(cluster_map(pu + (uint32_t)(r * L::ld + col) * 4, c));
       ll += ld_cluster_f32(cluster_map(lu + 4 * r, c)) * f;
       x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
     }
@@ -495,30 +571,37 @@ __global__ void __launch_bounds__(kPaThreads, 2) pattn_kernel(const __grid_const
   cluster_arrive_wait();   // a block's memory stays until its peers have read it
 }
 
-template <int HD, bool F8, int MT>
-cudaError_t launch_pa(const PAttn& a, int num_sms, cudaStream_t st) {
-  constexpr int smem = pa_smem<HD, F8, MT>();
-  auto kern = pattn_kernel<HD, F8, MT>;
-  // attributes are per device and cheap to set again
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int G = a.hq / a.hkv;
-  const int64_t rows = std::min<int64_t>((int64_t)std::min(a.max_q, a.tokens) * G, a.max_rows);
-  const int tpq = (int)((rows + MT * 16 - 1) / (MT * 16));
+template <int HD, bool F8, int NT>
+cudaError_t launch_pa(const PAttn& a, int64_t rows, int tpq, int num_sms, cudaStream_t st) {
+  using L = PaLayout<HD, F8, NT>;
+  auto kern = pattn_kernel<HD, F8, NT>;
   const int64_t items = (int64_t)a.seqs * tpq;
   // blocks of a cluster: until every SM has about one and a half, with at
   // least 64 keys (four steps a block, one per warp) of the longest context each
-  const int64_t max_keys = a.paged ? (int64_t)a.max_pages << a.page_shift : rows / G;
+  const int64_t max_keys = a.paged ? (int64_t)a.max_pages << a.page_shift : rows / (a.hq / a.hkv);
   int C = 1;
   while (C < 8 && items * a.hkv * C * 2 < 3LL * num_sms && max_keys >= 128 * C) C *= 2;
   if (items * C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_rows(kern, dim3((unsigned)(items * C), a.hkv), dim3(kPaThreads), smem, C, st, a, tpq, C);
+  return launch_rows_smem(std::integral_constant<int, NT * 1000 + HD * 2 + F8>(), kern, dim3((unsigned)(items * C), a.hkv),
+                          dim3(kPaThreads), L::smem, C, st, a, tpq, C);
+}
+template <int HD, bool F8>
+cudaError_t launch_pa_nt(const PAttn& a, int num_sms, cudaStream_t st) {
+  // tiles of at most 32 rows, as even as column tiles of 8 allow
+  const int64_t rows = std::min<int64_t>((int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), a.max_rows);
+  const int64_t least = (rows + 31) / 32;
+  const int nt = (int)std::min<int64_t>(4, ((rows + least - 1) / least + 7) / 8);
+  const int tpq = (int)((rows + nt * 8 - 1) / (nt * 8));
+  switch (nt) {
+    case 1: return launch_pa<HD, F8, 1>(a, rows, tpq, num_sms, st);
+    case 2: return launch_pa<HD, F8, 2>(a, rows, tpq, num_sms, st);
+    case 3: return launch_pa<HD, F8, 3>(a, rows, tpq, num_sms, st);
+    default: return launch_pa<HD, F8, 4>(a, rows, tpq, num_sms, st);
+  }
 }
 template <int HD>
 cudaError_t launch_pa_hd(const PAttn& a, int num_sms, cudaStream_t st) {
-  const int64_t rows = std::min<int64_t>((int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), a.max_rows);
-  if (rows <= 16) return a.f8 ? launch_pa<HD, true, 1>(a, num_sms, st) : launch_pa<HD, false, 1>(a, num_sms, st);
-  return a.f8 ? launch_pa<HD, true, 2>(a, num_sms, st) : launch_pa<HD, false, 2>(a, num_sms, st);
+  return a.f8 ? launch_pa_nt<HD, true>(a, num_sms, st) : launch_pa_nt<HD, false>(a, num_sms, st);
 }
 
 int fail(int code, const std::string& msg) {

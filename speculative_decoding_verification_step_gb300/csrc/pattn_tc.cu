@@ -18,7 +18,7 @@
 //                   O is rescaled in tensor memory;
 //   warp 8          producer: page ids and tensor copies (K_0 V_0 K_1 V_1 ..);
 //                   it zeroes V's rows past the length in the last step;
-//   warp 9          one thread issues the products, per step and tile
+//   warp 9          issues the products, per step and tile
 //                   O += P V (P from tensor memory, V as it lies, keys along
 //                   K), then S = Q K^T of the next step over the same columns
 //                   that P occupied: the tensor pipe runs in issue order;
@@ -81,6 +81,11 @@ SV_DEV void ta_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                ::"r"(smem_u32(bar)) : "memory");
 }
+SV_DEV bool ta_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
 SV_DEV void ta_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 SV_DEV void ta_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 SV_DEV void ta_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -97,6 +102,13 @@ SV_DEV void ta_ld32(uint32_t t, float* v) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t));
 }
+SV_DEV void ta_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 SV_DEV void ta_st32(uint32_t t, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -111,6 +123,28 @@ SV_DEV float ta_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+SV_DEV uint64_t ta_pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+SV_DEV void ta_split(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+SV_DEV uint64_t ta_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+SV_DEV uint64_t ta_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SV_DEV float ta_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 SV_DEV uint32_t ta_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -140,12 +174,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
   constexpr int kHalf = HD / 64;                       // 64-dim halves of a row
   constexpr uint32_t kTile = kTaKeys * HD * 2;         // bytes of a Q, K or V tile
   extern __shared__ __align__(1024) unsigned char tsm[];
-  __shared__ uint64_t q_full, kv_full[kTaStages], kv_empty[kTaStages], s_full[2], p_full[2], pv_done[2], v_fixed, drained;
+  __shared__ uint64_t q_full, kv_full[kTaStages], kv_empty[kTaStages], s_full[2], p_half[2], p_full[2], pv_done[2], v_fixed, drained;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_filled;
   const PAttn& a = ta.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int kvh = blockIdx.x % a.hkv, b = blockIdx.x / a.hkv, pair = (int)(gridDim.y - 1 - blockIdx.y);
   const int G = a.hq / a.hkv, tpt = ta.tpt;
 
@@ -186,7 +220,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);        // one arrival per softmax warp
+      mbar_init(&p_half[t], 4);        // one arrival per softmax warp
+      mbar_init(&p_full[t], 4);
       mbar_init(&pv_done[t], 1);
     }
     s_abort = 0;
@@ -200,8 +235,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
   ta_fence_before();
   __syncthreads();
   ta_fence_after();
-  const uint32_t tmem = s_tmem, o_at = 256;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  constexpr uint32_t o_at = 256;
 
+  // registers: the softmax warps hold a row's 128 scores (2 x 216 + 56 <= 3 x 168)
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 8) {
     // ---- producer ----
     if (lane == 0 && nst > 0) {
@@ -266,58 +305,74 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
     }
   } else if (warp == 9) {
     // ---- products ----
-    if (lane == 0 && nst > 0) {
+    // The whole warp runs the control flow, so that descriptors and addresses
+    // stay in uniform registers; one elected lane issues.
+    if (nst > 0) {
       constexpr uint32_t id_s = ta_idesc(kTaKeys, 0), id_o = ta_idesc(HD, 1);
-      bool ok = ta_wait(&q_full, 0, &s_abort);
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        const bool got = __all_sync(0xffffffffu, ta_wait(bar, parity, &s_abort));
+        ta_fence_after();
+        return got;
+      };
       // S_t = Q_t K^T of step j from ring entry 2 j
       auto score = [&](int t, int j) {
-        const uint32_t k_at = kv_at + (uint32_t)((2 * j) % kTaStages) * kTile;
+        const uint64_t qd = ta_desc(q_at + t * kTile, 1), kd = ta_desc(kv_at + (uint32_t)((2 * j) % kTaStages) * kTile, 1);
+        if (ta_elect()) {
 #pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          const uint32_t off = (ks / 4) * (kTile / kHalf) + (ks % 4) * 32;
-          ta_mma_ss(tmem + t * 128, ta_desc(q_at + t * kTile + off, 1), ta_desc(k_at + off, 1), id_s, ks > 0);
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            constexpr uint32_t half = kTile / kHalf / 16;
+            const uint32_t off = (ks / 4) * half + (ks % 4) * 2;   // 16-byte units
+            ta_mma_ss(tmem + t * 128, qd + off, kd + off, id_s, ks > 0);
+          }
+          ta_commit(&s_full[t]);
         }
-        ta_commit(&s_full[t]);
+        __syncwarp();
+      };
+      // O_t += P_t V over half of step j's keys
+      auto gather = [&](int t, int j, int half) {
+        const uint64_t vd = ta_desc(kv_at + (uint32_t)((2 * j + 1) % kTaStages) * kTile, (kTile / kHalf) >> 4);
+        if (ta_elect()) {
+#pragma unroll
+          for (int k4 = 0; k4 < kTaKeys / 32; ++k4) {
+            const int ks = half * (kTaKeys / 32) + k4;
+            ta_mma_ts(tmem + o_at + t * HD, tmem + t * 128 + ks * 8, vd + ks * 128, id_o, j > 0 || ks > 0);
+          }
+          if (half) ta_commit(&pv_done[t]);
+        }
+        __syncwarp();
       };
       // frees ring entry i once the products issued so far are done, where a later fill waits for it
       auto release = [&](int i) {
-        if (i + kTaStages < 2 * nst) ta_commit(&kv_empty[i % kTaStages]);
+        if (i + kTaStages < 2 * nst && ta_elect()) ta_commit(&kv_empty[i % kTaStages]);
+        __syncwarp();
       };
-      ok = ok && ta_wait(&kv_full[0], 0, &s_abort);
+      bool ok = wait(&q_full, 0) && wait(&kv_full[0], 0);
       if (ok) {
-        ta_fence_after();
-        for (int t = 0; t < ntile; ++t)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
           if (steps[t] > 0) score(t, 0);
         release(0);
       }
       for (int j = 0; ok && j < nst; ++j) {
         const int iv = 2 * j + 1, ik = 2 * j + 2;
-        bool have_v = false, have_k = false;
-        for (int t = 0; ok && t < ntile; ++t) {
-          if (j < steps[t]) {
-            ok = ta_wait(&p_full[t], (unsigned)(j & 1), &s_abort);
-            if (ok && !have_v) {
-              ok = ta_wait(&kv_full[iv % kTaStages], (unsigned)((iv / kTaStages) & 1), &s_abort);
-              if (ok && j == nst - 1 && last_rows < kTaKeys) ok = ta_wait(&v_fixed, 0, &s_abort);
-              have_v = true;
-            }
-            if (!ok) break;
-            ta_fence_after();
-            const uint32_t v_at = kv_at + (uint32_t)(iv % kTaStages) * kTile;
+        ok = wait(&kv_full[iv % kTaStages], (unsigned)((iv / kTaStages) & 1));
+        if (ok && j == nst - 1 && last_rows < kTaKeys) ok = wait(&v_fixed, 0);
+        bool have_k = false;
 #pragma unroll
-            for (int ks = 0; ks < kTaKeys / 16; ++ks)
-              ta_mma_ts(tmem + o_at + t * HD, tmem + t * 128 + ks * 8, ta_desc(v_at + ks * 2048, (kTile / kHalf) >> 4), id_o,
-                        (j > 0 || ks > 0));
-            ta_commit(&pv_done[t]);
-          }
-          if (j + 1 < steps[t]) {
-            if (!have_k) {
-              ok = ta_wait(&kv_full[ik % kTaStages], (unsigned)((ik / kTaStages) & 1), &s_abort);
-              have_k = true;
+        for (int t = 0; t < 2; ++t) {
+          // the first 64 keys' products run while the other exponentials are taken
+          if (ok && j < steps[t]) {
+            ok = wait(&p_half[t], (unsigned)(j & 1));
+            if (ok) {
+              gather(t, j, 0);
+              ok = wait(&p_full[t], (unsigned)(j & 1));
+              if (ok) gather(t, j, 1);
             }
-            if (!ok) break;
-            ta_fence_after();
-            score(t, j + 1);
+          }
+          if (ok && j + 1 < steps[t]) {
+            if (!have_k) ok = wait(&kv_full[ik % kTaStages], (unsigned)((ik / kTaStages) & 1));
+            have_k = true;
+            if (ok) score(t, j + 1);
           }
         }
         if (!ok) break;
@@ -325,13 +380,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
         release(ik);
       }
       if (!ok) {   // the products issued so far end before the space goes
-        ta_commit(&drained);
+        if (ta_elect()) ta_commit(&drained);
+        __syncwarp();
         long long spins = 0;
         while (!mbar_test(&drained, 0) && ++spins < (1LL << 20)) {
         }
       }
     }
-  } else if (warp < 8) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax of tile t: one row per thread ----
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const int ti = r / G, tok = tok0 + t * tpt + ti;
@@ -360,13 +418,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
         for (int c = 0; c < 128; ++c)
           if (c >= lim) s[c] = neg_inf();
       }
-      float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
+      float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
-      for (int c = 4; c < 128; c += 4) {
-        t0 = fmaxf(t0, fmaxf(s[c], s[c + 1]));
-        t1 = fmaxf(t1, fmaxf(s[c + 2], s[c + 3]));
+      for (int c = 4; c < 124; c += 8) {
+        t0 = ta_max3(t0, s[c], s[c + 1]);
+        t1 = ta_max3(t1, s[c + 2], s[c + 3]);
+        t2 = ta_max3(t2, s[c + 4], s[c + 5]);
+        t3 = ta_max3(t3, s[c + 6], s[c + 7]);
       }
-      const float top = fmaxf(t0, t1) * scale;
+      t0 = ta_max3(t0, s[124], s[125]);
+      t1 = ta_max3(t1, s[126], s[127]);
+      const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
       const bool move = top > m + kTaLazy;
       if (__any_sync(0xffffffffu, move)) {
         const float to = move ? top : m, f = ta_exp2(m - to);
@@ -388,24 +450,34 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
           }
         }
       }
-      const float neg = -m;
-      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-      uint32_t p[64];
+      const uint64_t neg2 = ta_pair(-m, -m), scale2 = ta_pair(scale, scale);
+      uint64_t sum0 = ta_pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-      for (int c = 0; c < 128; c += 4) {
-        const float x0 = ta_exp2(fmaf(s[c], scale, neg)), x1 = ta_exp2(fmaf(s[c + 1], scale, neg));
-        const float x2 = ta_exp2(fmaf(s[c + 2], scale, neg)), x3 = ta_exp2(fmaf(s[c + 3], scale, neg));
-        a0 += x0; a1 += x1; a2 += x2; a3 += x3;
-        p[c / 2] = ta_pack(x0, x1);
-        p[c / 2 + 1] = ta_pack(x2, x3);
+      for (int q = 0; q < 4; ++q) {          // 32 keys at a time: scores out, probabilities in
+        uint32_t p[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const int i = 32 * q + c;
+          float x0, x1, x2, x3;
+          ta_split(ta_fma2(ta_pair(s[i], s[i + 1]), scale2, neg2), x0, x1);
+          ta_split(ta_fma2(ta_pair(s[i + 2], s[i + 3]), scale2, neg2), x2, x3);
+          x0 = ta_exp2(x0); x1 = ta_exp2(x1); x2 = ta_exp2(x2); x3 = ta_exp2(x3);
+          sum0 = ta_add2(sum0, ta_pair(x0, x1));
+          sum1 = ta_add2(sum1, ta_pair(x2, x3));
+          p[c / 2] = ta_pack(x0, x1);
+          p[c / 2 + 1] = ta_pack(x2, x3);
+        }
+        ta_st16(s_at + 16 * q, p);
+        if (q & 1) {
+          ta_wait_st();
+          ta_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q == 1 ? &p_half[t] : &p_full[t]);
+        }
       }
-      l += (a0 + a1) + (a2 + a3);
-      ta_st32(s_at, p);
-      ta_st32(s_at + 32, p + 32);
-      ta_wait_st();
-      ta_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
+      float a0, a1;
+      ta_split(ta_add2(sum0, sum1), a0, a1);
+      l += a0 + a1;
     }
     if (ok && my > 0) {
       ok = ta_wait(&pv_done[t], (unsigned)((my - 1) & 1), &s_abort);
@@ -489,13 +561,12 @@ bool ta_map(TensorMap128& m, const void* base, int hd, int64_t d1, int64_t d2, i
 template <int HD>
 cudaError_t launch_ta(const TaArgs& ta, cudaStream_t st) {
   auto kern = pattn_tc_kernel<HD>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ta_smem<HD>());
-  if (e != cudaSuccess) return e;
   const PAttn& a = ta.a;
   const int toks = std::min(a.max_q, a.tokens);
   const int pairs = (toks + 2 * ta.tpt - 1) / (2 * ta.tpt);
   if ((int64_t)a.hkv * a.seqs > 0x7fffffffLL || pairs > 65535) return cudaErrorInvalidConfiguration;
-  return launch_rows(kern, dim3((unsigned)(a.hkv * a.seqs), (unsigned)pairs), dim3(kTaThreads), ta_smem<HD>(), 1, st, ta);
+  return launch_rows_smem(std::integral_constant<int, HD>(), kern, dim3((unsigned)(a.hkv * a.seqs), (unsigned)pairs),
+                          dim3(kTaThreads), ta_smem<HD>(), 1, st, ta);
 }
 
 }  // namespace
