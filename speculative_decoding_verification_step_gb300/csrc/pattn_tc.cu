@@ -24,8 +24,10 @@
 //                   that P occupied: the tensor pipe runs in issue order;
 //   warp 11         allocates and frees tensor memory.
 // Tensor memory, 512 columns: S/P 2 x 128, O 2 x head_dim.
-// Blocks are launched from each sequence's last rows to its first, so the
-// causal triangle's long rows start first.
+// Rows leave through the shared memory of their Q tile: a thread's row is
+// staged there and the warp writes whole rows (a thread writing its own row,
+// 16 bytes in each of 32 lines at a time, took 6000 clocks a tile, a fifth of
+// a block's time at 4096 tokens).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -52,6 +54,9 @@ struct TaArgs {
   TensorMap128 qm, km, vm;
   PAttn a;
   int tpt;          // tokens of a tile: 128 / G
+  uint32_t g_mul;   // ceil(2^16 / G): r * g_mul >> 16 = r / G for r < 128
+  int pairs;        // row pairs of the longest sequence
+  int chunk;        // (sequence, KV head) pairs in flight at a time
   int box_rows;     // key rows of a K / V box
 };
 
@@ -146,6 +151,12 @@ SV_DEV float ta_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Keeps what uses v[0 .. N-1] from being scheduled above this point.
+template <int N>
+SV_DEV void ta_pin(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
 SV_DEV uint32_t ta_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -167,8 +178,9 @@ SV_DEV bool ta_wait(uint64_t* bar, unsigned parity, volatile int* abort) {
   return true;
 }
 
-// Block (x, y): KV head x % hkv of sequence x / hkv, its row pair
-// gridDim.y - 1 - y.
+// Block i: chunks of `chunk` (sequence, KV head) pairs one after the other; in
+// a chunk the row pairs from each sequence's last to its first, all its heads
+// side by side.
 template <int HD>
 __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
   constexpr int kHalf = HD / 64;                       // 64-dim halves of a row
@@ -180,7 +192,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
   __shared__ int s_filled;
   const PAttn& a = ta.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x % a.hkv, b = blockIdx.x / a.hkv, pair = (int)(gridDim.y - 1 - blockIdx.y);
+  const int per_chunk = ta.chunk * ta.pairs, chunk = (int)blockIdx.x / per_chunk, in_chunk = (int)blockIdx.x % per_chunk;
+  const int width = min(ta.chunk, a.hkv * a.seqs - chunk * ta.chunk);
+  const int item = chunk * ta.chunk + in_chunk % width, pair = ta.pairs - 1 - in_chunk / width;
+  const int kvh = item % a.hkv, b = item / a.hkv;
   const int G = a.hq / a.hkv, tpt = ta.tpt;
 
   const int r_first = __ldg(a.cu + b);
@@ -210,7 +225,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
 
   const uint32_t base = (smem_u32(tsm) + 1023u) & ~1023u;
   const uint32_t q_at = base, kv_at = base + 2 * kTile;
-  if (threadIdx.x == 0) {
+  if (warp == 8 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ta.qm)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ta.km)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ta.vm)) : "memory");
     mbar_init(&q_full, 1);
     mbar_init(&v_fixed, 1);
     mbar_init(&drained, 1);
@@ -227,6 +245,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
     s_abort = 0;
     s_filled = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (nst > 0) {   // Q is on its way while tensor memory is allocated
+      mbar_arrive_expect_tx(&q_full, (unsigned)(ntile * kHalf * 128 * G * tpt));
+      for (int t = 0; t < ntile; ++t)
+        for (int h = 0; h < kHalf; ++h)
+          ta_tma_3d(q_at + t * kTile + h * (kTile / kHalf), &ta.qm, h * 64, kvh * G, r_first + tok0 + t * tpt, &q_full);
+    }
   }
   if (warp == 11) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
@@ -243,12 +268,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
   asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 8) {
     // ---- producer ----
-    if (lane == 0 && nst > 0) {
-      mbar_arrive_expect_tx(&q_full, (unsigned)(ntile * kHalf * 128 * G * tpt));
-      for (int t = 0; t < ntile; ++t)
-        for (int h = 0; h < kHalf; ++h)
-          ta_tma_3d(q_at + t * kTile + h * (kTile / kHalf), &ta.qm, h * 64, kvh * G, r_first + tok0 + t * tpt, &q_full);
-    }
     const int per = a.paged ? kTaKeys / ta.box_rows : 1;     // boxes of a step
     const int32_t* table = a.paged ? a.table + b * a.table_stride : nullptr;
     const int npages = a.paged ? (int)(((int64_t)keys + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
@@ -428,6 +447,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
       }
       t0 = ta_max3(t0, s[124], s[125]);
       t1 = ta_max3(t1, s[126], s[127]);
+      ta_pin<128>(s);                        // the maximum first, then the exponentials
       const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
       const bool move = top > m + kTaLazy;
       if (__any_sync(0xffffffffu, move)) {
@@ -473,6 +493,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
           ta_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(q == 1 ? &p_half[t] : &p_full[t]);
+          // the second half's exponentials stay behind the first's arrival
+          // (moved up among them they hold it back: 2440 clocks a step for 1770)
+          if (q == 1) ta_pin<64>(s + 64);
         }
       }
       float a0, a1;
@@ -488,25 +511,42 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
     const float inv = !ok ? __uint_as_float(0x7fffffffu) : l == 0.f ? 0.f : 1.f / l;
     const int64_t at = r_first + tok;
     const int h = kvh * G + r - ti * G;
-    bf16* d = (bf16*)a.out + at * a.o_ts + (int64_t)h * a.o_hs;
-#pragma unroll 1
-    for (int c = 0; c < HD; c += 32) {
-      float o[32];
+    constexpr int kChunks = HD / 8;                      // 16-byte chunks of a row
+    const uint32_t stage = q_at + t * kTile + (uint32_t)((warp & 3) * 32 * HD * 2);
+    if (t < ntile) {
+      float o[HD];
       if (ok && my > 0) {
-        ta_ld32(out_at + c, o);
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) ta_ld32(out_at + c, o + c);
         ta_wait_ld();
+      } else {
+#pragma unroll
+        for (int c = 0; c < HD; ++c) o[c] = 0.f;
       }
-      if (row_ok) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t w[4];
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = seen > 0 || !ok ? o[e + 2 * i] * inv : 0.f, y = seen > 0 || !ok ? o[e + 2 * i + 1] * inv : 0.f;
-            w[i] = ok ? ta_pack(x, y) : 0x7fff7fffu;
-          }
-          *reinterpret_cast<uint4*>(d + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) {
+          w[i] = ta_pack(o[8 * c + 2 * i] * inv, o[8 * c + 2 * i + 1] * inv);
         }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(stage + (uint32_t)(lane * HD * 2 + ((c ^ (lane & 7)) << 4))), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+      }
+      __syncwarp();
+      constexpr int kStep = 32 / kChunks;                // rows of one store
+      const int cc = lane % kChunks, r_at = (warp & 3) * 32 + lane / kChunks, t_at = tok0 + t * tpt;
+      bf16* const out0 = (bf16*)a.out + (int64_t)(r_first + t_at) * a.o_ts + (int64_t)(kvh * G) * a.o_hs + cc * 8;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += kStep) {
+        const int r2 = r_at + i, t2 = (int)((uint32_t)r2 * ta.g_mul >> 16);   // r2 / G
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(stage + (uint32_t)((r2 & 31) * HD * 2 + ((cc ^ (r2 & 7)) << 4))) : "memory");
+        if (t2 < tpt && t_at + t2 < toks)
+          *reinterpret_cast<uint4*>(out0 + t2 * a.o_ts + (r2 - t2 * G) * a.o_hs) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     if (row_ok && a.lse)
@@ -561,12 +601,10 @@ bool ta_map(TensorMap128& m, const void* base, int hd, int64_t d1, int64_t d2, i
 template <int HD>
 cudaError_t launch_ta(const TaArgs& ta, cudaStream_t st) {
   auto kern = pattn_tc_kernel<HD>;
-  const PAttn& a = ta.a;
-  const int toks = std::min(a.max_q, a.tokens);
-  const int pairs = (toks + 2 * ta.tpt - 1) / (2 * ta.tpt);
-  if ((int64_t)a.hkv * a.seqs > 0x7fffffffLL || pairs > 65535) return cudaErrorInvalidConfiguration;
-  return launch_rows_smem(std::integral_constant<int, HD>(), kern, dim3((unsigned)(a.hkv * a.seqs), (unsigned)pairs),
-                          dim3(kTaThreads), ta_smem<HD>(), 1, st, ta);
+  const int64_t blocks = (int64_t)ta.a.hkv * ta.a.seqs * ta.pairs;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_rows_smem(std::integral_constant<int, HD>(), kern, dim3((unsigned)blocks), dim3(kTaThreads), ta_smem<HD>(), 1,
+                          st, ta);
 }
 
 }  // namespace
@@ -583,11 +621,16 @@ bool pattn_tc_supported(const PAttn& a) {
 }
 
 cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
   TaArgs ta{};
   ta.a = a;
   const int G = a.hq / a.hkv;
   ta.tpt = kTaRows / G;
+  ta.g_mul = (65536u + G - 1) / G;
+  ta.pairs = (std::min(a.max_q, a.tokens) + 2 * ta.tpt - 1) / (2 * ta.tpt);
+  // A block reads all the keys that its rows see, so blocks of one KV head
+  // run together and share them in L2: as many heads at a time as give the
+  // SMs four rounds of blocks (enough for their unequal lengths to even out).
+  ta.chunk = std::max(1, std::min(a.hkv * a.seqs, (4 * num_sms + ta.pairs - 1) / ta.pairs));
   const int ps = a.paged ? 1 << a.page_shift : kTaKeys;
   ta.box_rows = std::min(ps, kTaKeys);
   bool ok = ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt);
