@@ -7,27 +7,40 @@
 // The kernel keeps the tensor pipe fed while the softmax of one tile runs
 // behind the products of the other.
 //
-// Block = two tiles of 128 rows (tokens x the G query heads of one KV head)
-// against the keys in steps of 128, over a ring of shared-memory tiles filled
-// by tensor copies, one box per page (128-byte swizzle, two 64-dim halves).
+// A block walks work items: two tiles of 128 rows (tokens x the G query heads
+// of one KV head) against the keys in steps of 128, over a ring of
+// shared-memory tiles filled by tensor copies, one box per page (128-byte
+// swizzle, 64-dim halves).
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row.  It reads its
 //                   128 scores from tensor memory, takes the maximum without
 //                   any exchange, writes p as bf16 over the scores and keeps
 //                   the row sum in fp32.  The exponent reference is lazy: it
 //                   moves only when a score exceeds it by 2^8, and only then
-//                   O is rescaled in tensor memory;
+//                   O is rescaled in tensor memory.  Rows leave through 4 KB
+//                   of shared memory a warp, as whole lines (a thread storing
+//                   its own row took 6000 clocks a tile);
 //   warp 8          producer: page ids and tensor copies (K_0 V_0 K_1 V_1 ..);
-//                   it zeroes V's rows past the length in the last step;
-//   warp 9          issues the products, per step and tile
-//                   O += P V (P from tensor memory, V as it lies, keys along
-//                   K), then S = Q K^T of the next step over the same columns
-//                   that P occupied: the tensor pipe runs in issue order;
-//   warp 11         allocates and frees tensor memory.
+//   warp 9          issues the products, per step and tile O += P V (P from
+//                   tensor memory, V as it lies, keys along K; the first 64
+//                   keys while the other exponentials are taken), then
+//                   S = Q K^T of the next step over the same columns that P
+//                   occupied: the tensor pipe runs in issue order.  The warp
+//                   stays converged and one elected lane issues: from a single
+//                   thread's control flow an MMA took 100 clocks to issue;
+//   warp 11         allocates and frees tensor memory;
+//   warps 12-15     8-bit keys only: a thread turns one row of codes into bf16
+//                   (code * 2^e is exact there), from the copies' ring into
+//                   the products'.  Rows past the length become zero.
 // Tensor memory, 512 columns: S/P 2 x 128, O 2 x head_dim.
-// Rows leave through the shared memory of their Q tile: a thread's row is
-// staged there and the warp writes whole rows (a thread writing its own row,
-// 16 bytes in each of 32 lines at a time, took 6000 clocks a tile, a fifth of
-// a block's time at 4096 tokens).
+// Blocks are persistent, one per SM, and the ring runs on across items: the
+// next item's Q, K and first scores are ready while the rows of this one
+// leave (a block per item spent 13 thousand clocks on start and end).  Items
+// come heads side by side within a chunk of heads, so that they share keys in
+// L2, and rows from each sequence's last to its first, so that the causal
+// triangle's long rows start first.
+// With few items (a chunk of one or two sequences) a cluster of two blocks
+// takes one item each half of the keys; block r finishes tile r with the
+// other's sums, read from its shared memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -44,8 +57,6 @@ namespace {
 
 constexpr int kTaRows = 128;        // rows of a tile (MMA M)
 constexpr int kTaKeys = 128;        // keys of a step
-constexpr int kTaThreads = 384;
-constexpr int kTaStages = 4;
 constexpr long long kTaWaitLimit = 1LL << 24;
 constexpr float kTaLazy = 8.f;
 constexpr float kTaNone = -1e30f;
@@ -57,11 +68,24 @@ struct TaArgs {
   uint32_t g_mul;   // ceil(2^16 / G): r * g_mul >> 16 = r / G for r < 128
   int pairs;        // row pairs of the longest sequence
   int chunk;        // (sequence, KV head) pairs in flight at a time
+  int items;        // (sequence, KV head, row pair): seqs * hkv * pairs
+  int split;        // 2: clusters of two blocks share an item's keys
   int box_rows;     // key rows of a K / V box
 };
 
-template <int HD>
-constexpr int ta_smem() { return 2 * kTaRows * HD * 2 + kTaStages * kTaKeys * HD * 2 + 1024; }
+template <int HD, bool F8>
+struct TaLayout {
+  static constexpr int threads = F8 ? 512 : 384;
+  static constexpr int stages = F8 ? 3 : 4;                // bf16 K / V tiles
+  static constexpr int raws = F8 ? 2 : 0;                  // tiles of codes
+  static constexpr uint32_t tile = kTaKeys * HD * 2;
+  static constexpr uint32_t raw = kTaKeys * HD;
+  static constexpr uint32_t q = 0, kv = 2 * tile, raw_at = kv + stages * tile, stage_at = raw_at + raws * raw;
+  static constexpr uint32_t stage = 32 * 128;              // a warp's rows on their way out, 64 dims at a time
+  static constexpr int smem = (int)(stage_at + 8 * stage) + 1024;
+  // registers (multiples of 8): softmax, others, 8-bit conversion; 2 x 216 + 56 <= 3 x 168, 2 x 184 + 56 + 88 <= 4 x 128
+  static constexpr int soft_regs = F8 ? 184 : 216, other_regs = 56;
+};
 
 SV_DEV uint64_t ta_desc(uint32_t addr, uint32_t lbo) {   // 128-byte swizzle, 8-row groups 1024 bytes apart
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)lbo << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
@@ -178,63 +202,127 @@ SV_DEV bool ta_wait(uint64_t* bar, unsigned parity, volatile int* abort) {
   return true;
 }
 
-// Block i: chunks of `chunk` (sequence, KV head) pairs one after the other; in
-// a chunk the row pairs from each sequence's last to its first, all its heads
-// side by side.
-template <int HD>
-__global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
+SV_DEV uint32_t ta_cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+SV_DEV uint32_t ta_map_peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+SV_DEV void ta_arrive_peer(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+SV_DEV float4 ta_ld_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+template <int N>
+SV_DEV void ta_regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+SV_DEV void ta_regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Two codes in the lower bytes of each half's upper byte -> bf16 pair times
+// two powers of two (2^100 and 2^(20 + e)): code * 2^e, exact.
+SV_DEV uint32_t ta_code_pair(uint32_t x, __nv_bfloat162 up, __nv_bfloat162 scale) {
+  uint32_t b = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);   // code * 2^-120
+  __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), up), scale);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// A work item as every warp sees it.
+struct TaItem {
+  int kvh, b, r_first, toks, keys, first_pos, tok0, ntile;
+  int beg, nst;       // this block's key steps beg .. beg + nst - 1
+  int steps[2];       // of those, each tile's (from beg)
+};
+
+template <int HD, bool F8>
+__global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
+  using L = TaLayout<HD, F8>;
   constexpr int kHalf = HD / 64;                       // 64-dim halves of a row
-  constexpr uint32_t kTile = kTaKeys * HD * 2;         // bytes of a Q, K or V tile
+  constexpr uint32_t kTile = L::tile;
+  constexpr int kS = L::stages, kR = F8 ? L::raws : 1;
   extern __shared__ __align__(1024) unsigned char tsm[];
-  __shared__ uint64_t q_full, kv_full[kTaStages], kv_empty[kTaStages], s_full[2], p_half[2], p_full[2], pv_done[2], v_fixed, drained;
+  __shared__ uint64_t q_full, q_free, kv_full[kS], kv_empty[kS], s_full[2], p_half[2], p_full[2], pv_done[2];
+  __shared__ uint64_t raw_full[kR], raw_empty[kR], drained, part_full;
+  __shared__ __align__(16) unsigned char s_scale[kR][kTaKeys];
+  __shared__ float s_part[2][kTaRows];                 // split: the other tile's references and sums
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_filled;
+  __shared__ int s_filled, s_qloads;
   const PAttn& a = ta.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int per_chunk = ta.chunk * ta.pairs, chunk = (int)blockIdx.x / per_chunk, in_chunk = (int)blockIdx.x % per_chunk;
-  const int width = min(ta.chunk, a.hkv * a.seqs - chunk * ta.chunk);
-  const int item = chunk * ta.chunk + in_chunk % width, pair = ta.pairs - 1 - in_chunk / width;
-  const int kvh = item % a.hkv, b = item / a.hkv;
   const int G = a.hq / a.hkv, tpt = ta.tpt;
+  const int rank = ta.split == 2 ? (int)ta_cluster_rank() : 0;
+  const int first = (int)blockIdx.x / ta.split, stride = (int)gridDim.x / ta.split;
 
-  const int r_first = __ldg(a.cu + b);
-  const int n = __ldg(a.cu + b + 1) - r_first;
-  if (r_first < 0 || n <= 0 || n > a.tokens - r_first || (int64_t)n * G <= a.max_rows) return;
-  const int toks = min(n, a.max_q);           // tokens that are computed
-  const int tok0 = pair * 2 * tpt;
-  if (tok0 >= toks) return;
-  int keys = n;
-  if (a.paged) {
-    keys = __ldg(a.lens + b);
-    const int64_t cap = (int64_t)a.max_pages << a.page_shift;
-    keys = keys < 0 ? 0 : (int)min((int64_t)keys, cap);
-  }
-  const int first_pos = keys - n;
-  const int ntile = tok0 + tpt < toks ? 2 : 1;
-  // key steps of each tile: what its last token sees
-  int steps[2];
+  // Item `idx` (its rows and lengths read from the index arrays); false when it holds no rows.
+  auto item_at = [&](int idx, TaItem& it) {
+    const int per_chunk = ta.chunk * ta.pairs, ch = idx / per_chunk, in = idx - ch * per_chunk;
+    const int width = min(ta.chunk, a.hkv * a.seqs - ch * ta.chunk);
+    const int up = in / width, head = ch * ta.chunk + in - up * width;
+    it.b = head / a.hkv;
+    it.kvh = head - it.b * a.hkv;
+    it.tok0 = (ta.pairs - 1 - up) * 2 * tpt;
+    it.r_first = __ldg(a.cu + it.b);
+    const int n = __ldg(a.cu + it.b + 1) - it.r_first;
+    int keys = a.paged ? __ldg(a.lens + it.b) : n;
+    if (it.r_first < 0 || n <= 0 || n > a.tokens - it.r_first || (int64_t)n * G <= a.max_rows) return false;
+    it.toks = min(n, a.max_q);                // tokens that are computed
+    if (it.tok0 >= it.toks) return false;
+    if (a.paged) keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
+    it.keys = keys;
+    it.first_pos = keys - n;
+    it.ntile = it.tok0 + tpt < it.toks ? 2 : 1;
+    int all[2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int last = min(toks, tok0 + (t + 1) * tpt) - 1;
-    const int see = min(keys, max(0, first_pos + last + 1));
-    steps[t] = t < ntile ? (see + kTaKeys - 1) / kTaKeys : 0;
-  }
-  const int nst = max(steps[0], steps[1]);
-  const int last_rows = keys - (nst - 1) * kTaKeys;    // valid keys of the last step (>= 128: all)
+    for (int t = 0; t < 2; ++t) {             // key steps of each tile: what its last token sees
+      const int last = min(it.toks, it.tok0 + (t + 1) * tpt) - 1;
+      const int see = min(keys, max(0, it.first_pos + last + 1));
+      all[t] = t < it.ntile ? (see + kTaKeys - 1) / kTaKeys : 0;
+    }
+    const int total = max(all[0], all[1]), mid = (total + 1) / 2;
+    it.beg = rank ? mid : 0;
+    it.nst = (ta.split == 2 ? (rank ? total : mid) : total) - it.beg;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) it.steps[t] = max(0, min(all[t] - it.beg, it.nst));
+    return true;
+  };
+  // First item of this block from idx on that holds rows (32 candidates at a time), or -1.
+  auto next_item = [&](int idx) {
+    for (; idx < ta.items; idx += 32 * stride) {
+      TaItem it;
+      const int64_t i = (int64_t)idx + (int64_t)lane * stride;
+      const unsigned some = __ballot_sync(0xffffffffu, i < ta.items && item_at((int)i, it));
+      if (some) return idx + (__ffs(some) - 1) * stride;
+      if ((int64_t)idx + 32LL * stride >= ta.items) break;
+    }
+    return -1;
+  };
+
+  if (next_item(first) < 0) return;           // no rows: both blocks of a cluster find so
 
   const uint32_t base = (smem_u32(tsm) + 1023u) & ~1023u;
-  const uint32_t q_at = base, kv_at = base + 2 * kTile;
+  const uint32_t q_at = base + L::q, kv_at = base + L::kv, raw_at = base + L::raw_at;
   if (warp == 8 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ta.qm)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ta.km)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ta.vm)) : "memory");
     mbar_init(&q_full, 1);
-    mbar_init(&v_fixed, 1);
+    mbar_init(&q_free, 1);
     mbar_init(&drained, 1);
-    for (int s = 0; s < kTaStages; ++s) {
-      mbar_init(&kv_full[s], 1);
+    mbar_init(&part_full, 4);
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(&kv_full[s], F8 ? 4 : 1);    // converted by four warps, or copied
       mbar_init(&kv_empty[s], 1);
+    }
+    for (int s = 0; s < kR; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -243,15 +331,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
       mbar_init(&pv_done[t], 1);
     }
     s_abort = 0;
-    s_filled = 0;
+    s_filled = s_qloads = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (nst > 0) {   // Q is on its way while tensor memory is allocated
-      mbar_arrive_expect_tx(&q_full, (unsigned)(ntile * kHalf * 128 * G * tpt));
-      for (int t = 0; t < ntile; ++t)
-        for (int h = 0; h < kHalf; ++h)
-          ta_tma_3d(q_at + t * kTile + h * (kTile / kHalf), &ta.qm, h * 64, kvh * G, r_first + tok0 + t * tpt, &q_full);
-    }
   }
   if (warp == 11) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
@@ -259,83 +340,166 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
   }
   ta_fence_before();
   __syncthreads();
+  // a peer's barrier exists before anything arrives there
+  if (ta.split == 2)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   ta_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   constexpr uint32_t o_at = 256;
 
-  // registers: the softmax warps hold a row's 128 scores (2 x 216 + 56 <= 3 x 168)
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 8) {
-    // ---- producer ----
-    const int per = a.paged ? kTaKeys / ta.box_rows : 1;     // boxes of a step
-    const int32_t* table = a.paged ? a.table + b * a.table_stride : nullptr;
-    const int npages = a.paged ? (int)(((int64_t)keys + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
-    auto page_of = [&](int j) {   // lane i: page of box i of step j; -1 (zero rows) past the length
-      const int64_t key = (int64_t)j * kTaKeys + lane * ta.box_rows;
-      const int pg = (int)(key >> a.page_shift);
-      return lane < per && j < nst && pg < npages ? __ldg(table + pg) : -1;
-    };
-    int next = a.paged ? page_of(0) : 0;
-    bool live = true;
-    for (int j = 0; j < nst && live; ++j) {
-      const int page = next;
-      if (a.paged) next = page_of(j + 1);
+  if (warp >= 12) {
+    if constexpr (F8) {
+      // ---- 8-bit rows to bf16: thread = key row ----
+      ta_regs_less<88>();
+      const int r = threadIdx.x - 384;
+      const __nv_bfloat162 up = __floats2bfloat162_rn(1.2676506002282294e30f, 1.2676506002282294e30f);   // 2^100
+      int i = 0;                               // tile: K and V of the steps of all items in turn
+      bool ok = true;
+      for (int idx = next_item(first); idx >= 0 && ok; idx = next_item(idx + stride)) {
+        TaItem it;
+        item_at(idx, it);
+        for (int j = 0; ok && j < 2 * it.nst; ++j, ++i) {
+          const int rs = i % kR, s = i % kS;
+          ok = ta_wait(&raw_full[rs], (unsigned)((i / kR) & 1), &s_abort);
+          if (ok && i >= kS) ok = ta_wait(&kv_empty[s], (unsigned)((i / kS - 1) & 1), &s_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t code = s_scale[rs][r];
+          const bool live = (it.beg + j / 2) * kTaKeys + r < it.keys;
+          // 2^(20 + e) with e = code - 127, a NaN row NaN, a row past the length zero
+          const uint32_t sb = !live ? 0u : code == 255u ? 0x7fffu : (min(max(code + 20u, 1u), 254u) << 7);
+          const uint32_t s2 = sb | (sb << 16);
+          const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+          const uint32_t src = raw_at + rs * L::raw + r * HD, dst = kv_at + s * kTile + r * 128;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int i = 2 * j + kv, s = i % kTaStages;
-        if (i >= kTaStages) live = live && ta_wait(&kv_empty[s], (unsigned)((i / kTaStages - 1) & 1), &s_abort);
-        live = __all_sync(0xffffffffu, live);
-        if (!live) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&kv_full[s], kTile);
-          s_filled = i + 1;
-        }
-        __syncwarp();
-        const void* map = kv ? &ta.vm : &ta.km;
-        const uint32_t dst = kv_at + s * kTile;
-        if (lane < per) {
-          for (int h = 0; h < kHalf; ++h) {
-            const uint32_t d = dst + h * (kTile / kHalf) + lane * ta.box_rows * 128;
-            if (a.paged)
-              ta_tma_3d(d, map, h * 64,
-                        (kvh << a.page_shift) + (int)(((int64_t)j * kTaKeys + lane * ta.box_rows) & ((1 << a.page_shift) - 1)),
-                        page, &kv_full[s]);
-            else
-              ta_tma_3d(d, map, h * 64, kvh, r_first + j * kTaKeys, &kv_full[s]);
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t w[4], o[8];
+            const int sw = HD == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src + (sw << 4)) : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = ta_code_pair(__byte_perm(w[k], 0, 0x1404), up, scale);
+              o[2 * k + 1] = ta_code_pair(__byte_perm(w[k], 0, 0x3424), up, scale);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int cc = 2 * c + h, col = cc & 7;
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = live ? o[4 * h + k] : 0u;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                           ::"r"(dst + (cc >> 3) * (kTile / kHalf) + ((col ^ (r & 7)) << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[rs]);
+            mbar_arrive(&kv_full[s]);
           }
         }
       }
     }
-    if (live && nst > 0 && last_rows < kTaKeys) {
-      // V's rows past the length: p is zero there, but the slots may hold
-      // anything.  (This warp has seen the entry's earlier fills consumed, so
-      // its parity is the last fill's.)
-      const int iv = 2 * nst - 1, s = iv % kTaStages;
-      if (__all_sync(0xffffffffu, ta_wait(&kv_full[s], (unsigned)((iv / kTaStages) & 1), &s_abort))) {
-        for (int h = 0; h < kHalf; ++h)
-          for (int e = last_rows * 8 + lane; e < kTaKeys * 8; e += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                         ::"r"(kv_at + s * kTile + h * (kTile / kHalf) + e * 16), "r"(0) : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_fixed);
+  } else if (warp >= 8) {
+    ta_regs_less<L::other_regs>();
+    if (warp == 8) {
+      // ---- producer ----
+      const int per = a.paged ? kTaKeys / ta.box_rows : 1;     // boxes of a step
+      constexpr int kRing = F8 ? L::raws : kS;
+      uint64_t* const full = F8 ? raw_full : kv_full;
+      uint64_t* const empty = F8 ? raw_empty : kv_empty;
+      int i = 0, loads = 0;                                    // ring fills, Q loads
+      bool live = true;
+      for (int idx = next_item(first); idx >= 0 && live; idx = next_item(idx + stride)) {
+        TaItem it;
+        item_at(idx, it);
+        if (it.nst == 0) continue;
+        if (loads > 0) live = __all_sync(0xffffffffu, ta_wait(&q_free, (unsigned)((loads - 1) & 1), &s_abort));
+        if (!live) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full, (unsigned)(it.ntile * kHalf * 128 * G * tpt));
+          s_qloads = loads + 1;
+          for (int t = 0; t < it.ntile; ++t)
+            for (int h = 0; h < kHalf; ++h)
+              ta_tma_3d(q_at + t * kTile + h * (kTile / kHalf), &ta.qm, h * 64, it.kvh * G, it.r_first + it.tok0 + t * tpt,
+                        &q_full);
+        }
+        ++loads;
+        const int32_t* table = a.paged ? a.table + it.b * a.table_stride : nullptr;
+        const int npages = a.paged ? (int)(((int64_t)it.keys + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
+        auto page_of = [&](int j) {   // lane b: page of box b of step j; -1 (zero rows) past the length or outside the pool
+          const int64_t key = (int64_t)(it.beg + j) * kTaKeys + lane * ta.box_rows;
+          const int pg = (int)(key >> a.page_shift);
+          const int page = lane < per && j < it.nst && pg < npages ? __ldg(table + pg) : -1;
+          return page >= a.pages ? -1 : page;
+        };
+        int next = a.paged ? page_of(0) : 0;
+        for (int j = 0; j < it.nst && live; ++j) {
+          const int page = next;
+          if (a.paged) next = page_of(j + 1);
+          const int64_t key = (int64_t)(it.beg + j) * kTaKeys + (a.paged ? lane * ta.box_rows : 0);
+          const int row = a.paged ? (it.kvh << a.page_shift) + (int)(key & ((1 << a.page_shift) - 1)) : it.kvh;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++i) {
+            const int s = i % kRing;
+            if (i >= kRing) live = live && ta_wait(&empty[s], (unsigned)((i / kRing - 1) & 1), &s_abort);
+            live = __all_sync(0xffffffffu, live);
+            if (!live) break;
+            const void* map = kv ? &ta.vm : &ta.km;
+            if constexpr (F8) {
+              const bool in = lane < per && page >= 0;
+              const unsigned some = __ballot_sync(0xffffffffu, in);
+              if (lane < per && !in)
+                for (int e = 0; e < ta.box_rows; e += 4) *reinterpret_cast<uint32_t*>(&s_scale[s][lane * ta.box_rows + e]) = 0x7f7f7f7fu;
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&full[s], L::raw + __popc(some) * ta.box_rows);
+                s_filled = i + 1;
+              }
+              __syncwarp();
+              if (lane < per) {
+                ta_tma_3d(raw_at + s * L::raw + lane * ta.box_rows * HD, map, 0, row, page, &full[s]);
+                if (in) bulk_g2s(&s_scale[s][lane * ta.box_rows], (kv ? a.vs : a.ks) + (int64_t)page * a.scale_stride + row,
+                                 ta.box_rows, &full[s]);
+              }
+            } else {
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&full[s], kTile);
+                s_filled = i + 1;
+              }
+              __syncwarp();
+              if (lane < per) {
+                for (int h = 0; h < kHalf; ++h)
+                  ta_tma_3d(kv_at + s * kTile + h * (kTile / kHalf) + lane * ta.box_rows * 128, map, h * 64, row,
+                            a.paged ? page : it.r_first + (int)key, &full[s]);
+              }
+            }
+          }
+        }
       }
-    }
-  } else if (warp == 9) {
-    // ---- products ----
-    // The whole warp runs the control flow, so that descriptors and addresses
-    // stay in uniform registers; one elected lane issues.
-    if (nst > 0) {
+      // the last fills are used, and the products' signals have landed, before the block ends
+      for (int k = max(0, i - kRing); live && k < i; ++k)
+        live = __all_sync(0xffffffffu, ta_wait(&empty[k % kRing], (unsigned)((k / kRing) & 1), &s_abort));
+      if (live && loads > 0) ta_wait(&q_free, (unsigned)((loads - 1) & 1), &s_abort);
+      if constexpr (F8) {
+        for (int k = max(0, i - kS); live && k < i; ++k)
+          live = __all_sync(0xffffffffu, ta_wait(&kv_empty[k % kS], (unsigned)((k / kS) & 1), &s_abort));
+      }
+    } else if (warp == 9) {
+      // ---- products ----
+      // The whole warp runs the control flow, so that descriptors and addresses
+      // stay in uniform registers; one elected lane issues.
       constexpr uint32_t id_s = ta_idesc(kTaKeys, 0), id_o = ta_idesc(HD, 1);
       auto wait = [&](uint64_t* bar, unsigned parity) {
         const bool got = __all_sync(0xffffffffu, ta_wait(bar, parity, &s_abort));
         ta_fence_after();
         return got;
       };
-      // S_t = Q_t K^T of step j from ring entry 2 j
-      auto score = [&](int t, int j) {
-        const uint64_t qd = ta_desc(q_at + t * kTile, 1), kd = ta_desc(kv_at + (uint32_t)((2 * j) % kTaStages) * kTile, 1);
+      // S_t = Q_t K^T from ring fill i
+      auto score = [&](int t, int i) {
+        const uint64_t qd = ta_desc(q_at + t * kTile, 1), kd = ta_desc(kv_at + (uint32_t)(i % kS) * kTile, 1);
         if (ta_elect()) {
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks) {
@@ -347,221 +511,296 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
         }
         __syncwarp();
       };
-      // O_t += P_t V over half of step j's keys
-      auto gather = [&](int t, int j, int half) {
-        const uint64_t vd = ta_desc(kv_at + (uint32_t)((2 * j + 1) % kTaStages) * kTile, (kTile / kHalf) >> 4);
+      // O_t += P_t V over half of a step's keys, V from ring fill i
+      auto gather = [&](int t, int i, int half, bool fresh) {
+        const uint64_t vd = ta_desc(kv_at + (uint32_t)(i % kS) * kTile, (kTile / kHalf) >> 4);
         if (ta_elect()) {
 #pragma unroll
           for (int k4 = 0; k4 < kTaKeys / 32; ++k4) {
             const int ks = half * (kTaKeys / 32) + k4;
-            ta_mma_ts(tmem + o_at + t * HD, tmem + t * 128 + ks * 8, vd + ks * 128, id_o, j > 0 || ks > 0);
+            ta_mma_ts(tmem + o_at + t * HD, tmem + t * 128 + ks * 8, vd + ks * 128, id_o, !fresh || ks > 0);
           }
           if (half) ta_commit(&pv_done[t]);
         }
         __syncwarp();
       };
-      // frees ring entry i once the products issued so far are done, where a later fill waits for it
-      auto release = [&](int i) {
-        if (i + kTaStages < 2 * nst && ta_elect()) ta_commit(&kv_empty[i % kTaStages]);
+      // signals bar once the products issued so far are done
+      auto signal = [&](uint64_t* bar) {
+        if (ta_elect()) ta_commit(bar);
         __syncwarp();
       };
-      bool ok = wait(&q_full, 0) && wait(&kv_full[0], 0);
-      if (ok) {
+      int i0 = 0, loads = 0;                  // ring fill of the item's first K, Q loads
+      unsigned np[2] = {0, 0};                // steps of each tile over all items
+      bool ok = true;
+      int idx = next_item(first);
+      while (idx >= 0 && ok) {
+        TaItem it;
+        item_at(idx, it);
+        // (the same in every lane; said so for uniform registers)
+        it.beg = __shfl_sync(0xffffffffu, it.beg, 0);
+        it.nst = __shfl_sync(0xffffffffu, it.nst, 0);
+        it.keys = __shfl_sync(0xffffffffu, it.keys, 0);
+        it.steps[0] = __shfl_sync(0xffffffffu, it.steps[0], 0);
+        it.steps[1] = __shfl_sync(0xffffffffu, it.steps[1], 0);
+        if (it.nst == 0) {
+          idx = next_item(idx + stride);
+          continue;
+        }
+        ok = wait(&q_full, (unsigned)(loads & 1)) && wait(&kv_full[i0 % kS], (unsigned)((i0 / kS) & 1));
+        if (!ok) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (steps[t] > 0) score(t, 0);
-        release(0);
-      }
-      for (int j = 0; ok && j < nst; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
-        ok = wait(&kv_full[iv % kTaStages], (unsigned)((iv / kTaStages) & 1));
-        if (ok && j == nst - 1 && last_rows < kTaKeys) ok = wait(&v_fixed, 0);
-        bool have_k = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          // the first 64 keys' products run while the other exponentials are taken
-          if (ok && j < steps[t]) {
-            ok = wait(&p_half[t], (unsigned)(j & 1));
-            if (ok) {
-              gather(t, j, 0);
-              ok = wait(&p_full[t], (unsigned)(j & 1));
-              if (ok) gather(t, j, 1);
+          if (it.steps[t] > 0) score(t, i0);
+        signal(&kv_empty[i0 % kS]);
+        if (it.nst == 1) signal(&q_free);
+        idx = next_item(idx + stride);        // looked up while the first scores are on their way
+        for (int j = 0; ok && j < it.nst; ++j) {
+          const int iv = i0 + 2 * j + 1, ik = iv + 1;
+          ok = wait(&kv_full[iv % kS], (unsigned)((iv / kS) & 1));
+          if constexpr (!F8) {
+            // V's rows past the length: p is zero there, but the slots may hold anything
+            const int rows = it.keys - (it.beg + j) * kTaKeys;
+            if (ok && rows < kTaKeys) {
+              for (int h = 0; h < kHalf; ++h)
+                for (int e = rows * 8 + lane; e < kTaKeys * 8; e += 32)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                               ::"r"(kv_at + (iv % kS) * kTile + h * (kTile / kHalf) + e * 16), "r"(0) : "memory");
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
             }
           }
-          if (ok && j + 1 < steps[t]) {
-            if (!have_k) ok = wait(&kv_full[ik % kTaStages], (unsigned)((ik / kTaStages) & 1));
-            have_k = true;
-            if (ok) score(t, j + 1);
+          bool have_k = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            // the first 64 keys' products run while the other exponentials are taken
+            if (ok && j < it.steps[t]) {
+              ok = wait(&p_half[t], np[t] & 1);
+              if (ok) {
+                gather(t, iv, 0, j == 0);
+                ok = wait(&p_full[t], np[t] & 1);
+                if (ok) gather(t, iv, 1, j == 0);
+              }
+              ++np[t];
+            }
+            if (ok && j + 1 < it.steps[t]) {
+              if (!have_k) ok = wait(&kv_full[ik % kS], (unsigned)((ik / kS) & 1));
+              have_k = true;
+              if (ok) score(t, ik);
+            }
           }
+          if (!ok) break;
+          signal(&kv_empty[iv % kS]);
+          if (j + 1 < it.nst) signal(&kv_empty[ik % kS]);
+          if (j + 2 == it.nst) signal(&q_free);   // the last scores are issued
         }
-        if (!ok) break;
-        release(iv);
-        release(ik);
+        i0 += 2 * it.nst;
+        ++loads;
       }
       if (!ok) {   // the products issued so far end before the space goes
-        if (ta_elect()) ta_commit(&drained);
-        __syncwarp();
+        signal(&drained);
         long long spins = 0;
         while (!mbar_test(&drained, 0) && ++spins < (1LL << 20)) {
         }
       }
     }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    ta_regs_more<L::soft_regs>();
     // ---- softmax of tile t: one row per thread ----
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
-    const int ti = r / G, tok = tok0 + t * tpt + ti;
-    const bool row_ok = t < ntile && ti < tpt && tok < toks;
-    const int seen = row_ok ? min(keys, max(0, first_pos + tok + 1)) : 0;
-    const int tile_all = min(keys, max(0, first_pos + tok0 + t * tpt + 1));   // keys that every row sees
+    const int ti = (int)((uint32_t)r * ta.g_mul >> 16);      // r / G
     const uint32_t row = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + row + t * 128, out_at = tmem + row + o_at + t * HD;
+    const uint32_t stage = base + L::stage_at + warp * L::stage;
     const float scale = a.scale_log2;
-    float m = kTaNone, l = 0.f;
+    unsigned np = 0;                           // steps of this tile over all items
     bool ok = true;
-    const int my = t < ntile ? steps[t] : 0;
-    for (int j = 0; j < my; ++j) {
-      ok = ta_wait(&s_full[t], (unsigned)(j & 1), &s_abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      ta_fence_after();
-      float s[128];
+    for (int idx = next_item(first); idx >= 0; idx = next_item(idx + stride)) {
+      TaItem it;
+      item_at(idx, it);
+      const int t_at = it.tok0 + t * tpt, tok = t_at + ti;
+      const bool row_ok = t < it.ntile && ti < tpt && tok < it.toks;
+      const int seen = row_ok ? min(it.keys, max(0, it.first_pos + tok + 1)) : 0;
+      const int tile_all = min(it.keys, max(0, it.first_pos + t_at + 1));   // keys that every row sees
+      float m = kTaNone, l = 0.f;
+      const int my = it.steps[t];
+      for (int j = 0; ok && j < my; ++j, ++np) {
+        ok = ta_wait(&s_full[t], np & 1, &s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ta_fence_after();
+        float s[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) ta_ld32(s_at + 32 * c, s + 32 * c);
-      ta_wait_ld();
-      const int key0 = j * kTaKeys;
-      if (key0 + kTaKeys > tile_all) {
-        const int lim = seen - key0;
+        for (int c = 0; c < 4; ++c) ta_ld32(s_at + 32 * c, s + 32 * c);
+        ta_wait_ld();
+        const int key0 = (it.beg + j) * kTaKeys;
+        if (key0 + kTaKeys > tile_all) {
+          const int lim = seen - key0;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= lim) s[c] = neg_inf();
-      }
-      float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) s[c] = neg_inf();
+        }
+        float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
-      for (int c = 4; c < 124; c += 8) {
-        t0 = ta_max3(t0, s[c], s[c + 1]);
-        t1 = ta_max3(t1, s[c + 2], s[c + 3]);
-        t2 = ta_max3(t2, s[c + 4], s[c + 5]);
-        t3 = ta_max3(t3, s[c + 6], s[c + 7]);
-      }
-      t0 = ta_max3(t0, s[124], s[125]);
-      t1 = ta_max3(t1, s[126], s[127]);
-      ta_pin<128>(s);                        // the maximum first, then the exponentials
-      const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
-      const bool move = top > m + kTaLazy;
-      if (__any_sync(0xffffffffu, move)) {
-        const float to = move ? top : m, f = ta_exp2(m - to);
-        m = to;
-        l *= f;
-        if (j > 0) {
-          ok = ta_wait(&pv_done[t], (unsigned)((j - 1) & 1), &s_abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ta_fence_after();
+        for (int c = 4; c < 124; c += 8) {
+          t0 = ta_max3(t0, s[c], s[c + 1]);
+          t1 = ta_max3(t1, s[c + 2], s[c + 3]);
+          t2 = ta_max3(t2, s[c + 4], s[c + 5]);
+          t3 = ta_max3(t3, s[c + 6], s[c + 7]);
+        }
+        t0 = ta_max3(t0, s[124], s[125]);
+        t1 = ta_max3(t1, s[126], s[127]);
+        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
+        const bool move = top > m + kTaLazy;
+        if (__any_sync(0xffffffffu, move)) {
+          const float to = move ? top : m, f = ta_exp2(m - to);
+          m = to;
+          l *= f;
+          if (j > 0) {
+            ok = ta_wait(&pv_done[t], (np - 1) & 1, &s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ta_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            ta_ld32(out_at + c, o);
-            ta_wait_ld();
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              ta_ld32(out_at + c, o);
+              ta_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            ta_st32(out_at + c, reinterpret_cast<uint32_t*>(o));
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              ta_st32(out_at + c, reinterpret_cast<uint32_t*>(o));
+            }
           }
         }
-      }
-      const uint64_t neg2 = ta_pair(-m, -m), scale2 = ta_pair(scale, scale);
-      uint64_t sum0 = ta_pair(0.f, 0.f), sum1 = sum0;
+        const uint64_t neg2 = ta_pair(-m, -m), scale2 = ta_pair(scale, scale);
+        uint64_t sum0 = ta_pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {          // 32 keys at a time: scores out, probabilities in
-        uint32_t p[16];
+        for (int q = 0; q < 4; ++q) {          // 32 keys at a time: scores out, probabilities in
+          uint32_t p[16];
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const int i = 32 * q + c;
-          float x0, x1, x2, x3;
-          ta_split(ta_fma2(ta_pair(s[i], s[i + 1]), scale2, neg2), x0, x1);
-          ta_split(ta_fma2(ta_pair(s[i + 2], s[i + 3]), scale2, neg2), x2, x3);
-          x0 = ta_exp2(x0); x1 = ta_exp2(x1); x2 = ta_exp2(x2); x3 = ta_exp2(x3);
-          sum0 = ta_add2(sum0, ta_pair(x0, x1));
-          sum1 = ta_add2(sum1, ta_pair(x2, x3));
-          p[c / 2] = ta_pack(x0, x1);
-          p[c / 2 + 1] = ta_pack(x2, x3);
+          for (int c = 0; c < 32; c += 4) {
+            const int i = 32 * q + c;
+            float x0, x1, x2, x3;
+            ta_split(ta_fma2(ta_pair(s[i], s[i + 1]), scale2, neg2), x0, x1);
+            ta_split(ta_fma2(ta_pair(s[i + 2], s[i + 3]), scale2, neg2), x2, x3);
+            x0 = ta_exp2(x0); x1 = ta_exp2(x1); x2 = ta_exp2(x2); x3 = ta_exp2(x3);
+            sum0 = ta_add2(sum0, ta_pair(x0, x1));
+            sum1 = ta_add2(sum1, ta_pair(x2, x3));
+            p[c / 2] = ta_pack(x0, x1);
+            p[c / 2 + 1] = ta_pack(x2, x3);
+          }
+          ta_st16(s_at + 16 * q, p);
+          if (q & 1) {
+            ta_wait_st();
+            ta_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q == 1 ? &p_half[t] : &p_full[t]);
+          }
         }
-        ta_st16(s_at + 16 * q, p);
-        if (q & 1) {
-          ta_wait_st();
-          ta_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q == 1 ? &p_half[t] : &p_full[t]);
-          // the second half's exponentials stay behind the first's arrival
-          // (moved up among them they hold it back: 2440 clocks a step for 1770)
-          if (q == 1) ta_pin<64>(s + 64);
-        }
+        float a0, a1;
+        ta_split(ta_add2(sum0, sum1), a0, a1);
+        l += a0 + a1;
       }
-      float a0, a1;
-      ta_split(ta_add2(sum0, sum1), a0, a1);
-      l += a0 + a1;
-    }
-    if (ok && my > 0) {
-      ok = ta_wait(&pv_done[t], (unsigned)((my - 1) & 1), &s_abort);
-      ok = __all_sync(0xffffffffu, ok);
-      ta_fence_after();
-    }
-    // rows out; a wait that gave up leaves NaN, not a wrong number
-    const float inv = !ok ? __uint_as_float(0x7fffffffu) : l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = r_first + tok;
-    const int h = kvh * G + r - ti * G;
-    constexpr int kChunks = HD / 8;                      // 16-byte chunks of a row
-    const uint32_t stage = q_at + t * kTile + (uint32_t)((warp & 3) * 32 * HD * 2);
-    if (t < ntile) {
+      if (ok && my > 0) {
+        ok = ta_wait(&pv_done[t], (np - 1) & 1, &s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        ta_fence_after();
+      }
+      if (t >= it.ntile) continue;
       float o[HD];
       if (ok && my > 0) {
 #pragma unroll
         for (int c = 0; c < HD; c += 32) ta_ld32(out_at + c, o + c);
         ta_wait_ld();
+        ta_fence_before();
       } else {
 #pragma unroll
         for (int c = 0; c < HD; ++c) o[c] = 0.f;
       }
+      if (ta.split == 2) {
+        // one item a block: the ring is free once both tiles' products are done
+        const int other = it.steps[1 - t];
+        if (ok && other > 0) ok = __all_sync(0xffffffffu, ta_wait(&pv_done[1 - t], (unsigned)((other - 1) & 1), &s_abort));
+        if (t != rank) {                       // for the peer: sums column by column, then references
+          if (!ok) l = __uint_as_float(0x7fffffffu);
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = ta_pack(o[8 * c + 2 * i] * inv, o[8 * c + 2 * i + 1] * inv);
+          for (int c = 0; c < HD / 4; ++c)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(kv_at + (uint32_t)(c * kTaRows + r) * 16), "f"(o[4 * c]), "f"(o[4 * c + 1]), "f"(o[4 * c + 2]),
+                           "f"(o[4 * c + 3]) : "memory");
+          s_part[0][r] = m;
+          s_part[1][r] = l;
+          __syncwarp();
+          if (lane == 0) ta_arrive_peer(ta_map_peer(smem_u32(&part_full), (uint32_t)(1 - rank)));
+          continue;
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     ::"r"(stage + (uint32_t)(lane * HD * 2 + ((c ^ (lane & 7)) << 4))), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                     : "memory");
+        bool got = ta_wait(&part_full, 0, &s_abort);
+        got = __all_sync(0xffffffffu, got);
+        ok = ok && got;
+        if (ok) {
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          const uint32_t pm = ta_map_peer(smem_u32(&s_part[0][r]), (uint32_t)(1 - rank));
+          const uint32_t pl = ta_map_peer(smem_u32(&s_part[1][r]), (uint32_t)(1 - rank));
+          float m2, l2;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m2) : "r"(pm) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l2) : "r"(pl) : "memory");
+          const float to = fmaxf(m, m2), f1 = ta_exp2(m - to), f2 = ta_exp2(m2 - to);
+          const uint32_t po = ta_map_peer(kv_at + (uint32_t)r * 16, (uint32_t)(1 - rank));
+#pragma unroll
+          for (int c = 0; c < HD / 4; ++c) {
+            const float4 y = ta_ld_peer(po + (uint32_t)(c * kTaRows) * 16);
+            o[4 * c] = o[4 * c] * f1 + y.x * f2;
+            o[4 * c + 1] = o[4 * c + 1] * f1 + y.y * f2;
+            o[4 * c + 2] = o[4 * c + 2] * f1 + y.z * f2;
+            o[4 * c + 3] = o[4 * c + 3] * f1 + y.w * f2;
+          }
+          m = to;
+          l = l * f1 + l2 * f2;
+        }
       }
-      __syncwarp();
-      constexpr int kStep = 32 / kChunks;                // rows of one store
-      const int cc = lane % kChunks, r_at = (warp & 3) * 32 + lane / kChunks, t_at = tok0 + t * tpt;
-      bf16* const out0 = (bf16*)a.out + (int64_t)(r_first + t_at) * a.o_ts + (int64_t)(kvh * G) * a.o_hs + cc * 8;
-#pragma unroll 4
-      for (int i = 0; i < 32; i += kStep) {
-        const int r2 = r_at + i, t2 = (int)((uint32_t)r2 * ta.g_mul >> 16);   // r2 / G
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(stage + (uint32_t)((r2 & 31) * HD * 2 + ((cc ^ (r2 & 7)) << 4))) : "memory");
-        if (t2 < tpt && t_at + t2 < toks)
-          *reinterpret_cast<uint4*>(out0 + t2 * a.o_ts + (r2 - t2 * G) * a.o_hs) = make_uint4(w[0], w[1], w[2], w[3]);
+      // rows out; a wait that gave up leaves NaN, not a wrong number
+      const float inv = !ok ? __uint_as_float(0x7fffffffu) : l == 0.f ? 0.f : 1.f / l;
+      const int cc = lane & 7, r_at = (warp & 3) * 32 + (lane >> 3);
+      bf16* const out0 = (bf16*)a.out + (int64_t)(it.r_first + t_at) * a.o_ts + (int64_t)(it.kvh * G) * a.o_hs + cc * 8;
+#pragma unroll
+      for (int h = 0; h < kHalf; ++h) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = ta_pack(o[64 * h + 8 * c + 2 * i] * inv, o[64 * h + 8 * c + 2 * i + 1] * inv);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       ::"r"(stage + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) << 4))), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {      // four rows a store
+          const int r2 = r_at + i, t2 = (int)((uint32_t)r2 * ta.g_mul >> 16);   // r2 / G
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(stage + (uint32_t)((r2 & 31) * 128 + ((cc ^ (r2 & 7)) << 4))) : "memory");
+          if (t2 < tpt && t_at + t2 < it.toks)
+            *reinterpret_cast<uint4*>(out0 + 64 * h + t2 * a.o_ts + (r2 - t2 * G) * a.o_hs) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
       }
+      if (row_ok && a.lse)
+        a.lse[(int64_t)(it.r_first + tok) * a.hq + it.kvh * G + r - ti * G] =
+            !ok ? __uint_as_float(0x7fffffffu) : l == 0.f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
     }
-    if (row_ok && a.lse)
-      a.lse[at * a.hq + h] = !ok ? __uint_as_float(0x7fffffffu) : l == 0.f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
   }
   __syncthreads();
   if (s_abort && threadIdx.x == 0) {
     // a wait gave up: copies in flight land (bounded) before the space goes
-    for (int i = max(0, s_filled - kTaStages); i < s_filled; ++i) {
+    constexpr int kRing = F8 ? L::raws : kS;
+    for (int i = max(0, s_filled - kRing); i < s_filled; ++i) {
       long long spins = 0;
-      while (!mbar_test(&kv_full[i % kTaStages], (unsigned)((i / kTaStages) & 1)) && ++spins < (1LL << 20)) {
+      while (!mbar_test(F8 ? &raw_full[i % kR] : &kv_full[i % kS], (unsigned)((i / kRing) & 1)) && ++spins < (1LL << 20)) {
       }
     }
     long long spins = 0;
-    while (nst > 0 && !mbar_test(&q_full, 0) && ++spins < (1LL << 20)) {
+    while (s_qloads > 0 && !mbar_test(&q_full, (unsigned)((s_qloads - 1) & 1)) && ++spins < (1LL << 20)) {
     }
   }
   __syncthreads();
@@ -569,6 +808,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) pattn_tc_kernel(const __grid_co
     ta_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+  // a block's sums stay until its peer has read them
+  if (ta.split == 2)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 ta_encoder() {
@@ -582,36 +824,40 @@ PFN_cuTensorMapEncodeTiled_v12000 ta_encoder() {
   }();
   return fn;
 }
-// [d2][d1][hd] bf16 with strides s1, s2 (elements), boxes of 64 x b1 x b2.
-bool ta_map(TensorMap128& m, const void* base, int hd, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1, int b2) {
+// [d2][d1][hd] with strides s1, s2 (elements): bf16 in boxes of 64 x b1 x b2,
+// or bytes in boxes of whole rows.
+bool ta_map(TensorMap128& m, const void* base, int hd, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1, int b2,
+            bool bytes = false) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = ta_encoder();
   if (!enc) return false;
   // the stride of a dimension of one element is never used, but has to be valid
   if (d1 == 1) s1 = hd;
   if (d2 == 1) s2 = hd;
+  const int es = bytes ? 1 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)d1, (cuuint64_t)d2};
-  cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(reinterpret_cast<CUtensorMap*>(&m), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  cuuint64_t strides[2] = {(cuuint64_t)s1 * es, (cuuint64_t)s2 * es};
+  cuuint32_t box[3] = {(cuuint32_t)(bytes ? hd : 64), (cuuint32_t)b1, (cuuint32_t)b2};
+  cuuint32_t step[3] = {1, 1, 1};
+  return enc(reinterpret_cast<CUtensorMap*>(&m), bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             bytes && hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD>
-cudaError_t launch_ta(const TaArgs& ta, cudaStream_t st) {
-  auto kern = pattn_tc_kernel<HD>;
-  const int64_t blocks = (int64_t)ta.a.hkv * ta.a.seqs * ta.pairs;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_rows_smem(std::integral_constant<int, HD>(), kern, dim3((unsigned)blocks), dim3(kTaThreads), ta_smem<HD>(), 1,
-                          st, ta);
+template <int HD, bool F8>
+cudaError_t launch_ta(const TaArgs& ta, int num_sms, cudaStream_t st) {
+  using L = TaLayout<HD, F8>;
+  auto kern = pattn_tc_kernel<HD, F8>;
+  const int blocks = ta.split == 2 ? 2 * ta.items : std::min(ta.items, num_sms);
+  return launch_rows_smem(std::integral_constant<int, HD * 2 + F8>(), kern, dim3((unsigned)blocks), dim3(L::threads), L::smem,
+                          ta.split, st, ta);
 }
 
 }  // namespace
 
 bool pattn_tc_supported(const PAttn& a) {
   const int G = a.hq / a.hkv;
-  if ((a.hd != 64 && a.hd != 128) || a.f8 || G > kTaRows) return false;
+  if ((a.hd != 64 && a.hd != 128) || G > kTaRows) return false;
   // tensor maps take positive strides only (a broadcast head has stride 0)
   auto pos = [](int64_t s, int64_t d) { return d == 1 || (s > 0 && s < (1LL << 38)); };
   if (!pos(a.q_ts, a.tokens) || !pos(a.q_hs, a.hq)) return false;
@@ -629,20 +875,27 @@ cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st) {
   ta.pairs = (std::min(a.max_q, a.tokens) + 2 * ta.tpt - 1) / (2 * ta.tpt);
   // A block reads all the keys that its rows see, so blocks of one KV head
   // run together and share them in L2: as many heads at a time as give the
-  // SMs four rounds of blocks (enough for their unequal lengths to even out).
+  // SMs four rounds of items.
   ta.chunk = std::max(1, std::min(a.hkv * a.seqs, (4 * num_sms + ta.pairs - 1) / ta.pairs));
+  const int64_t items = (int64_t)a.hkv * a.seqs * ta.pairs;
+  if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+  ta.items = (int)items;
+  // items that can hold rows: no more than the tokens fill, and one ragged pair a sequence
+  const int64_t most = a.hkv * std::min<int64_t>((int64_t)a.seqs * ta.pairs, a.tokens / (2 * ta.tpt) + a.seqs);
+  ta.split = most <= num_sms ? 2 : 1;
   const int ps = a.paged ? 1 << a.page_shift : kTaKeys;
   ta.box_rows = std::min(ps, kTaKeys);
   bool ok = ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt);
   if (a.paged) {
-    ok = ok && ta_map(ta.km, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, ta.box_rows, 1) &&
-         ta_map(ta.vm, a.v, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, ta.box_rows, 1);
+    ok = ok && ta_map(ta.km, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, ta.box_rows, 1, a.f8) &&
+         ta_map(ta.vm, a.v, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, ta.box_rows, 1, a.f8);
   } else {
     ok = ok && ta_map(ta.km, a.k, a.hd, a.hkv, a.tokens, a.k_hs, a.k_ts, 1, kTaKeys) &&
          ta_map(ta.vm, a.v, a.hd, a.hkv, a.tokens, a.v_hs, a.v_ts, 1, kTaKeys);
   }
   if (!ok) return cudaErrorInvalidValue;
-  return a.hd == 64 ? launch_ta<64>(ta, st) : launch_ta<128>(ta, st);
+  if (a.f8) return a.hd == 64 ? launch_ta<64, true>(ta, num_sms, st) : launch_ta<128, true>(ta, num_sms, st);
+  return a.hd == 64 ? launch_ta<64, false>(ta, num_sms, st) : launch_ta<128, false>(ta, num_sms, st);
 }
 
 }  // namespace sv
