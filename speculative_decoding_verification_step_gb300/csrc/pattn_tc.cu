@@ -27,17 +27,21 @@
 //                   occupied: the tensor pipe runs in issue order.  The warp
 //                   stays converged and one elected lane issues: from a single
 //                   thread's control flow an MMA took 100 clocks to issue;
+//   warp 10         scheduler: hands the work items to the others through a
+//                   queue in shared memory, two ahead;
 //   warp 11         allocates and frees tensor memory;
 //   warps 12-15     8-bit keys only: a thread turns one row of codes into bf16
 //                   (code * 2^e is exact there), from the copies' ring into
 //                   the products'.  Rows past the length become zero.
 // Tensor memory, 512 columns: S/P 2 x 128, O 2 x head_dim.
-// Blocks are persistent, one per SM, and the ring runs on across items: the
-// next item's Q, K and first scores are ready while the rows of this one
-// leave (a block per item spent 13 thousand clocks on start and end).  Items
-// come heads side by side within a chunk of heads, so that they share keys in
-// L2, and rows from each sequence's last to its first, so that the causal
-// triangle's long rows start first.
+// A block goes on to further items by taking over blocks of the grid that
+// have not started (cluster launch control), and the ring runs on across
+// items: the next item's Q, K and first scores are ready while the rows of
+// this one leave (a block per item spent 13 thousand clocks on start and
+// end, and a fixed share of the items per block left some 9% longer at
+// work).  Items come heads side by side within a chunk of heads, so that they
+// share keys in L2, and rows from each sequence's last to its first, so that
+// the causal triangle's long rows start first.
 // With few items (a chunk of one or two sequences) a cluster of two blocks
 // takes one item each half of the keys; block r finishes tile r with the
 // other's sums, read from its shared memory.
@@ -46,6 +50,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -170,6 +175,11 @@ SV_DEV uint64_t ta_add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+SV_DEV uint64_t ta_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 SV_DEV float ta_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -233,8 +243,24 @@ SV_DEV uint32_t ta_code_pair(uint32_t x, __nv_bfloat162 up, __nv_bfloat162 scale
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// The response of a take-over: the index of the block taken, or -1.
+SV_DEV int ta_taken(const uint4* at) {
+  uint32_t x = 0, got;
+  asm volatile(
+      "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %1, 1, 0, p;\n"
+      " mov.u32 %0, 0;\n @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n}"
+      : "=r"(x), "=r"(got) : "r"(smem_u32(at)) : "memory");
+  return got ? (int)x : -1;
+}
+SV_DEV void ta_take(uint4* at, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(smem_u32(at)), "r"(smem_u32(bar)) : "memory");
+}
+
 // A work item as every warp sees it.
 struct TaItem {
+  int valid;          // 0: no more items
   int kvh, b, r_first, toks, keys, first_pos, tok0, ntile;
   int beg, nst;       // this block's key steps beg .. beg + nst - 1
   int steps[2];       // of those, each tile's (from beg)
@@ -248,7 +274,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   constexpr int kS = L::stages, kR = F8 ? L::raws : 1;
   extern __shared__ __align__(1024) unsigned char tsm[];
   __shared__ uint64_t q_full, q_free, kv_full[kS], kv_empty[kS], s_full[2], p_half[2], p_full[2], pv_done[2];
-  __shared__ uint64_t raw_full[kR], raw_empty[kR], drained, part_full;
+  __shared__ uint64_t raw_full[kR], raw_empty[kR], drained, part_full, item_full[2], item_empty[2], taken;
+  __shared__ __align__(16) uint4 s_taken;
+  __shared__ TaItem s_item[2];
   __shared__ __align__(16) unsigned char s_scale[kR][kTaKeys];
   __shared__ float s_part[2][kTaRows];                 // split: the other tile's references and sums
   __shared__ uint32_t s_tmem;
@@ -258,8 +286,6 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.hq / a.hkv, tpt = ta.tpt;
   const int rank = ta.split == 2 ? (int)ta_cluster_rank() : 0;
-  const int first = (int)blockIdx.x / ta.split, stride = (int)gridDim.x / ta.split;
-
   // Item `idx` (its rows and lengths read from the index arrays); false when it holds no rows.
   auto item_at = [&](int idx, TaItem& it) {
     const int per_chunk = ta.chunk * ta.pairs, ch = idx / per_chunk, in = idx - ch * per_chunk;
@@ -292,19 +318,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     for (int t = 0; t < 2; ++t) it.steps[t] = max(0, min(all[t] - it.beg, it.nst));
     return true;
   };
-  // First item of this block from idx on that holds rows (32 candidates at a time), or -1.
-  auto next_item = [&](int idx) {
-    for (; idx < ta.items; idx += 32 * stride) {
-      TaItem it;
-      const int64_t i = (int64_t)idx + (int64_t)lane * stride;
-      const unsigned some = __ballot_sync(0xffffffffu, i < ta.items && item_at((int)i, it));
-      if (some) return idx + (__ffs(some) - 1) * stride;
-      if ((int64_t)idx + 32LL * stride >= ta.items) break;
-    }
-    return -1;
-  };
-
-  if (next_item(first) < 0) return;           // no rows: both blocks of a cluster find so
+  TaItem mine;
+  mine.valid = item_at((int)blockIdx.x / ta.split, mine);
+  if (!mine.valid) return;                    // (both blocks of a cluster)
 
   const uint32_t base = (smem_u32(tsm) + 1023u) & ~1023u;
   const uint32_t q_at = base + L::q, kv_at = base + L::kv, raw_at = base + L::raw_at;
@@ -316,6 +332,11 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     mbar_init(&q_free, 1);
     mbar_init(&drained, 1);
     mbar_init(&part_full, 4);
+    mbar_init(&taken, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], F8 ? 14 : 10);   // one arrival per warp that works on items
+    }
     for (int s = 0; s < kS; ++s) {
       mbar_init(&kv_full[s], F8 ? 4 : 1);    // converted by four warps, or copied
       mbar_init(&kv_empty[s], 1);
@@ -347,6 +368,15 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   constexpr uint32_t o_at = 256;
 
+  // Next item of the queue (the k-th of this block); false at the end or when a wait gave up.
+  auto get_item = [&](int k, TaItem& it) {
+    const bool got = __all_sync(0xffffffffu, ta_wait(&item_full[k & 1], (unsigned)((k >> 1) & 1), &s_abort));
+    it = s_item[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+    return got && it.valid;
+  };
+
   if (warp >= 12) {
     if constexpr (F8) {
       // ---- 8-bit rows to bf16: thread = key row ----
@@ -355,9 +385,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       const __nv_bfloat162 up = __floats2bfloat162_rn(1.2676506002282294e30f, 1.2676506002282294e30f);   // 2^100
       int i = 0;                               // tile: K and V of the steps of all items in turn
       bool ok = true;
-      for (int idx = next_item(first); idx >= 0 && ok; idx = next_item(idx + stride)) {
-        TaItem it;
-        item_at(idx, it);
+      TaItem it;
+      for (int k = 0; ok && get_item(k, it); ++k) {
         for (int j = 0; ok && j < 2 * it.nst; ++j, ++i) {
           const int rs = i % kR, s = i % kS;
           ok = ta_wait(&raw_full[rs], (unsigned)((i / kR) & 1), &s_abort);
@@ -412,9 +441,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       uint64_t* const empty = F8 ? raw_empty : kv_empty;
       int i = 0, loads = 0;                                    // ring fills, Q loads
       bool live = true;
-      for (int idx = next_item(first); idx >= 0 && live; idx = next_item(idx + stride)) {
-        TaItem it;
-        item_at(idx, it);
+      TaItem it;
+      for (int k = 0; live && get_item(k, it); ++k) {
         if (it.nst == 0) continue;
         if (loads > 0) live = __all_sync(0xffffffffu, ta_wait(&q_free, (unsigned)((loads - 1) & 1), &s_abort));
         if (!live) break;
@@ -532,20 +560,15 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       int i0 = 0, loads = 0;                  // ring fill of the item's first K, Q loads
       unsigned np[2] = {0, 0};                // steps of each tile over all items
       bool ok = true;
-      int idx = next_item(first);
-      while (idx >= 0 && ok) {
-        TaItem it;
-        item_at(idx, it);
+      TaItem it;
+      for (int k = 0; ok && get_item(k, it); ++k) {
         // (the same in every lane; said so for uniform registers)
         it.beg = __shfl_sync(0xffffffffu, it.beg, 0);
         it.nst = __shfl_sync(0xffffffffu, it.nst, 0);
         it.keys = __shfl_sync(0xffffffffu, it.keys, 0);
         it.steps[0] = __shfl_sync(0xffffffffu, it.steps[0], 0);
         it.steps[1] = __shfl_sync(0xffffffffu, it.steps[1], 0);
-        if (it.nst == 0) {
-          idx = next_item(idx + stride);
-          continue;
-        }
+        if (it.nst == 0) continue;
         ok = wait(&q_full, (unsigned)(loads & 1)) && wait(&kv_full[i0 % kS], (unsigned)((i0 / kS) & 1));
         if (!ok) break;
 #pragma unroll
@@ -553,7 +576,6 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           if (it.steps[t] > 0) score(t, i0);
         signal(&kv_empty[i0 % kS]);
         if (it.nst == 1) signal(&q_free);
-        idx = next_item(idx + stride);        // looked up while the first scores are on their way
         for (int j = 0; ok && j < it.nst; ++j) {
           const int iv = i0 + 2 * j + 1, ik = iv + 1;
           ok = wait(&kv_full[iv % kS], (unsigned)((iv / kS) & 1));
@@ -602,6 +624,42 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         while (!mbar_test(&drained, 0) && ++spins < (1LL << 20)) {
         }
       }
+    } else if (warp == 10) {
+      // ---- scheduler ----
+      TaItem it = mine;
+      bool ok = true;
+      unsigned takes = 0;
+      for (int k = 0;; ++k) {
+        if (lane == 0) {
+          s_item[k & 1] = it;
+          mbar_arrive(&item_full[k & 1]);
+        }
+        __syncwarp();
+        if (!it.valid) break;
+        // one item ahead: the next is taken when all have begun this one
+        ok = __all_sync(0xffffffffu, ta_wait(&item_empty[k & 1], (unsigned)((k >> 1) & 1), &s_abort));
+        it.valid = 0;
+        while (ok && ta.split == 1) {          // a block of the grid that has not started and holds rows
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&taken, 16);
+            ta_take(&s_taken, &taken);
+          }
+          ok = __all_sync(0xffffffffu, ta_wait(&taken, takes & 1, &s_abort));
+          ++takes;
+          if (!ok) break;
+          const int idx = ta_taken(&s_taken);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // read before the next response lands there
+          __syncwarp();
+          if (idx < 0) break;
+          it.valid = item_at(idx, it);
+          if (it.valid) break;
+        }
+        if (!ok) break;
+      }
+      // a response on its way lands (bounded) before the space goes
+      long long spins = 0;
+      while (!ok && takes > 0 && !mbar_test(&taken, (takes - 1) & 1) && ++spins < (1LL << 20)) {
+      }
     }
   } else {
     ta_regs_more<L::soft_regs>();
@@ -614,9 +672,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     const float scale = a.scale_log2;
     unsigned np = 0;                           // steps of this tile over all items
     bool ok = true;
-    for (int idx = next_item(first); idx >= 0; idx = next_item(idx + stride)) {
-      TaItem it;
-      item_at(idx, it);
+    TaItem it;
+    for (int k = 0; get_item(k, it); ++k) {   // (after a wait gave up: what was handed out still gets its NaN)
       const int t_at = it.tok0 + t * tpt, tok = t_at + ti;
       const bool row_ok = t < it.ntile && ti < tpt && tok < it.toks;
       const int seen = row_ok ? min(it.keys, max(0, it.first_pos + tok + 1)) : 0;
@@ -760,6 +817,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       // rows out; a wait that gave up leaves NaN, not a wrong number
       const float inv = !ok ? __uint_as_float(0x7fffffffu) : l == 0.f ? 0.f : 1.f / l;
       const int cc = lane & 7, r_at = (warp & 3) * 32 + (lane >> 3);
+      const int o_ts = (int)a.o_ts, o_hs = (int)a.o_hs;    // 128 tokens' rows lie within 2^31 elements
+      const uint64_t inv2 = ta_pair(inv, inv);
       bf16* const out0 = (bf16*)a.out + (int64_t)(it.r_first + t_at) * a.o_ts + (int64_t)(it.kvh * G) * a.o_hs + cc * 8;
 #pragma unroll
       for (int h = 0; h < kHalf; ++h) {
@@ -767,7 +826,11 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         for (int c = 0; c < 8; ++c) {
           uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = ta_pack(o[64 * h + 8 * c + 2 * i] * inv, o[64 * h + 8 * c + 2 * i + 1] * inv);
+          for (int i = 0; i < 4; ++i) {
+            float x, y;
+            ta_split(ta_mul2(ta_pair(o[64 * h + 8 * c + 2 * i], o[64 * h + 8 * c + 2 * i + 1]), inv2), x, y);
+            w[i] = ta_pack(x, y);
+          }
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                        ::"r"(stage + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) << 4))), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                        : "memory");
@@ -781,7 +844,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                        : "r"(stage + (uint32_t)((r2 & 31) * 128 + ((cc ^ (r2 & 7)) << 4))) : "memory");
           if (t2 < tpt && t_at + t2 < it.toks)
-            *reinterpret_cast<uint4*>(out0 + 64 * h + t2 * a.o_ts + (r2 - t2 * G) * a.o_hs) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out0 + 64 * h + (t2 * o_ts + (r2 - t2 * G) * o_hs)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
       }
@@ -845,11 +908,10 @@ bool ta_map(TensorMap128& m, const void* base, int hd, int64_t d1, int64_t d2, i
 }
 
 template <int HD, bool F8>
-cudaError_t launch_ta(const TaArgs& ta, int num_sms, cudaStream_t st) {
+cudaError_t launch_ta(const TaArgs& ta, cudaStream_t st) {
   using L = TaLayout<HD, F8>;
   auto kern = pattn_tc_kernel<HD, F8>;
-  const int blocks = ta.split == 2 ? 2 * ta.items : std::min(ta.items, num_sms);
-  return launch_rows_smem(std::integral_constant<int, HD * 2 + F8>(), kern, dim3((unsigned)blocks), dim3(L::threads), L::smem,
+  return launch_rows_smem(std::integral_constant<int, HD * 2 + F8>(), kern, dim3((unsigned)(ta.split * ta.items)), dim3(L::threads), L::smem,
                           ta.split, st, ta);
 }
 
@@ -861,6 +923,7 @@ bool pattn_tc_supported(const PAttn& a) {
   // tensor maps take positive strides only (a broadcast head has stride 0)
   auto pos = [](int64_t s, int64_t d) { return d == 1 || (s > 0 && s < (1LL << 38)); };
   if (!pos(a.q_ts, a.tokens) || !pos(a.q_hs, a.hq)) return false;
+  if (std::abs(a.o_ts) >= 1 << 23 || std::abs(a.o_hs) >= 1 << 23) return false;   // 32-bit offsets within a tile
   if (!a.paged)
     return pos(a.k_ts, a.tokens) && pos(a.k_hs, a.hkv) && pos(a.v_ts, a.tokens) && pos(a.v_hs, a.hkv);
   return pos(a.page_stride, a.pages) && (int64_t)a.hkv << a.page_shift <= 0x7fffffffLL;
@@ -894,8 +957,8 @@ cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st) {
          ta_map(ta.vm, a.v, a.hd, a.hkv, a.tokens, a.v_hs, a.v_ts, 1, kTaKeys);
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (a.f8) return a.hd == 64 ? launch_ta<64, true>(ta, num_sms, st) : launch_ta<128, true>(ta, num_sms, st);
-  return a.hd == 64 ? launch_ta<64, false>(ta, num_sms, st) : launch_ta<128, false>(ta, num_sms, st);
+  if (a.f8) return a.hd == 64 ? launch_ta<64, true>(ta, st) : launch_ta<128, true>(ta, st);
+  return a.hd == 64 ? launch_ta<64, false>(ta, st) : launch_ta<128, false>(ta, st);
 }
 
 }  // namespace sv
