@@ -85,12 +85,9 @@ struct PAttn {
   const int32_t* table;
   int64_t table_stride;
   int pages, page_shift, max_pages;
-  // sequences with more than max_rows rows (tokens * G) are left to the
-  // tensor-memory kernel, which takes those only
-  int max_rows;
 };
-// Rows per KV head up to which the register-tile kernel takes a sequence
-// when both kernels can.
+// Rows per KV head of the longest sequence up to which the register-tile
+// kernel takes a call that both can.
 constexpr int kPaMaxRows = 64;
 cudaError_t launch_pattn(const PAttn& a, int num_sms, cudaStream_t st);
 // Tensor-memory kernel: bf16 or e4m3 keys, head dim 64 or 128.

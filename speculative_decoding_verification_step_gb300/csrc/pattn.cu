@@ -41,7 +41,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
 #include <string>
 
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
   const int r_first = __ldg(a.cu + b);
   const int n = __ldg(a.cu + b + 1) - r_first;
   int keys = a.paged ? __ldg(a.lens + b) : n;
-  if (r_first < 0 || n <= 0 || n > a.tokens - r_first || (int64_t)n * G > a.max_rows) return;
+  if (r_first < 0 || n <= 0 || n > a.tokens - r_first) return;
   if (a.paged) keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
   const int rows = min(n, a.max_q) * G;       // rows that are computed
   const int row0 = tile * kRows;
@@ -588,7 +587,7 @@ cudaError_t launch_pa(const PAttn& a, int64_t rows, int tpq, int num_sms, cudaSt
 template <int HD, bool F8>
 cudaError_t launch_pa_nt(const PAttn& a, int num_sms, cudaStream_t st) {
   // tiles of at most 32 rows, as even as column tiles of 8 allow
-  const int64_t rows = std::min<int64_t>((int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), a.max_rows);
+  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv);
   const int64_t least = (rows + 31) / 32;
   const int nt = (int)std::min<int64_t>(4, ((rows + least - 1) / least + 7) / 8);
   const int tpq = (int)((rows + nt * 8 - 1) / (nt * 8));
@@ -632,17 +631,13 @@ int run_attention(PAttn& a, const char* who, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
-  // Sequences of at most kPaMaxRows rows per KV head go to the register-tile
-  // kernel, longer chunks to the tensor-memory one where it applies; a batch
-  // that may hold both kinds launches both, each skipping the other's.
+  // Up to kPaMaxRows rows per KV head the register-tile kernel, beyond the
+  // tensor-memory one where it applies.  A batch with both kinds goes to the
+  // latter whole: a short sequence costs it one tile's walk over the keys
+  // beside the long ones, less than a second launch behind them.
   const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv);
-  a.max_rows = INT_MAX;
-  if (rows > kPaMaxRows && pattn_tc_supported(a)) {
-    a.max_rows = kPaMaxRows;
-    e = launch_pattn_tc(a, sms, st);
-    if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
-  }
-  e = a.hd == 32 ? launch_pa_hd<32>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64>(a, sms, st) : launch_pa_hd<128>(a, sms, st);
+  if (rows > kPaMaxRows && pattn_tc_supported(a)) e = launch_pattn_tc(a, sms, st);
+  else e = a.hd == 32 ? launch_pa_hd<32>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64>(a, sms, st) : launch_pa_hd<128>(a, sms, st);
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
 }
 

@@ -42,9 +42,9 @@
 // work).  Items come heads side by side within a chunk of heads, so that they
 // share keys in L2, and rows from each sequence's last to its first, so that
 // the causal triangle's long rows start first.
-// With few items (a chunk of one or two sequences) a cluster of two blocks
-// takes one item each half of the keys; block r finishes tile r with the
-// other's sums, read from its shared memory.
+// With few items (chunks of a few sequences) a cluster of two blocks shares an
+// item's keys; block t finishes tile t with the other's sums, read from its
+// shared memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -75,6 +75,7 @@ struct TaArgs {
   int chunk;        // (sequence, KV head) pairs in flight at a time
   int items;        // (sequence, KV head, row pair): seqs * hkv * pairs
   int split;        // 2: clusters of two blocks share an item's keys
+  int by_length;    // sequences in order of their lengths (paged, at most 32)
   int box_rows;     // key rows of a K / V box
 };
 
@@ -88,6 +89,7 @@ struct TaLayout {
   static constexpr uint32_t q = 0, kv = 2 * tile, raw_at = kv + stages * tile, stage_at = raw_at + raws * raw;
   static constexpr uint32_t stage = 32 * 128;              // a warp's rows on their way out, 64 dims at a time
   static constexpr int smem = (int)(stage_at + 8 * stage) + 1024;
+  static_assert(smem <= 227 * 1024 - 1536, "with the barriers and queues, one block's shared memory");
   // registers (multiples of 8): softmax, others, 8-bit conversion; 2 x 216 + 56 <= 3 x 168, 2 x 184 + 56 + 88 <= 4 x 128
   static constexpr int soft_regs = F8 ? 184 : 216, other_regs = 56;
 };
@@ -278,26 +280,39 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   __shared__ __align__(16) uint4 s_taken;
   __shared__ TaItem s_item[2];
   __shared__ __align__(16) unsigned char s_scale[kR][kTaKeys];
-  __shared__ float s_part[2][kTaRows];                 // split: the other tile's references and sums
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_filled, s_qloads;
   const PAttn& a = ta.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.hq / a.hkv, tpt = ta.tpt;
-  const int rank = ta.split == 2 ? (int)ta_cluster_rank() : 0;
-  // Item `idx` (its rows and lengths read from the index arrays); false when it holds no rows.
+  const int rank = ta.split > 1 ? (int)ta_cluster_rank() : 0;
+  // Item `idx` (its rows and lengths read from the index arrays); false when
+  // it holds no rows.  Called by whole warps.
   auto item_at = [&](int idx, TaItem& it) {
-    const int per_chunk = ta.chunk * ta.pairs, ch = idx / per_chunk, in = idx - ch * per_chunk;
-    const int width = min(ta.chunk, a.hkv * a.seqs - ch * ta.chunk);
-    const int up = in / width, head = ch * ta.chunk + in - up * width;
-    it.b = head / a.hkv;
-    it.kvh = head - it.b * a.hkv;
-    it.tok0 = (ta.pairs - 1 - up) * 2 * tpt;
+    if (ta.by_length) {                        // the warp's lanes rank the sequences, longest first
+      const int per_seq = a.hkv * ta.pairs, k = idx / per_seq, in = idx - k * per_seq, up = in / a.hkv;
+      const int len = lane < a.seqs ? __ldg(a.lens + lane) : -0x7fffffff - 1;
+      int before = 0;
+      for (int j = 0; j < a.seqs; ++j) {
+        const int other = __shfl_sync(0xffffffffu, len, j);
+        before += other > len || (other == len && j < lane);
+      }
+      it.b = __ffs(__ballot_sync(0xffffffffu, lane < a.seqs && before == k)) - 1;
+      it.kvh = in - up * a.hkv;
+      it.tok0 = (ta.pairs - 1 - up) * 2 * tpt;
+    } else {
+      const int per_chunk = ta.chunk * ta.pairs, ch = idx / per_chunk, in = idx - ch * per_chunk;
+      const int width = min(ta.chunk, a.hkv * a.seqs - ch * ta.chunk);
+      const int up = in / width, head = ch * ta.chunk + in - up * width;
+      it.b = head / a.hkv;
+      it.kvh = head - it.b * a.hkv;
+      it.tok0 = (ta.pairs - 1 - up) * 2 * tpt;
+    }
     it.r_first = __ldg(a.cu + it.b);
     const int n = __ldg(a.cu + it.b + 1) - it.r_first;
     int keys = a.paged ? __ldg(a.lens + it.b) : n;
-    if (it.r_first < 0 || n <= 0 || n > a.tokens - it.r_first || (int64_t)n * G <= a.max_rows) return false;
+    if (it.r_first < 0 || n <= 0 || n > a.tokens - it.r_first) return false;
     it.toks = min(n, a.max_q);                // tokens that are computed
     if (it.tok0 >= it.toks) return false;
     if (a.paged) keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
@@ -311,16 +326,16 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       const int see = min(keys, max(0, it.first_pos + last + 1));
       all[t] = t < it.ntile ? (see + kTaKeys - 1) / kTaKeys : 0;
     }
-    const int total = max(all[0], all[1]), mid = (total + 1) / 2;
-    it.beg = rank ? mid : 0;
-    it.nst = (ta.split == 2 ? (rank ? total : mid) : total) - it.beg;
+    const int total = max(all[0], all[1]);
+    it.beg = total * rank / ta.split;
+    it.nst = total * (rank + 1) / ta.split - it.beg;
 #pragma unroll
     for (int t = 0; t < 2; ++t) it.steps[t] = max(0, min(all[t] - it.beg, it.nst));
     return true;
   };
   TaItem mine;
   mine.valid = item_at((int)blockIdx.x / ta.split, mine);
-  if (!mine.valid) return;                    // (both blocks of a cluster)
+  if (!mine.valid) return;                    // (all blocks of a cluster)
 
   const uint32_t base = (smem_u32(tsm) + 1023u) & ~1023u;
   const uint32_t q_at = base + L::q, kv_at = base + L::kv, raw_at = base + L::raw_at;
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     mbar_init(&q_full, 1);
     mbar_init(&q_free, 1);
     mbar_init(&drained, 1);
-    mbar_init(&part_full, 4);
+    mbar_init(&part_full, 4 * max(1, ta.split - 1));   // four warps of every other block
     mbar_init(&taken, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&item_full[s], 1);
@@ -362,7 +377,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   ta_fence_before();
   __syncthreads();
   // a peer's barrier exists before anything arrives there
-  if (ta.split == 2)
+  if (ta.split > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   ta_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
@@ -773,21 +788,22 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
 #pragma unroll
         for (int c = 0; c < HD; ++c) o[c] = 0.f;
       }
-      if (ta.split == 2) {
+      if (ta.split > 1) {
         // one item a block: the ring is free once both tiles' products are done
         const int other = it.steps[1 - t];
         if (ok && other > 0) ok = __all_sync(0xffffffffu, ta_wait(&pv_done[1 - t], (unsigned)((other - 1) & 1), &s_abort));
-        if (t != rank) {                       // for the peer: sums column by column, then references
+        const uint32_t part = kv_at + t * 2 * kTile;       // [dims / 4][row] of four sums
+        if (t != rank) {                       // for the tile's finisher
           if (!ok) l = __uint_as_float(0x7fffffffu);
 #pragma unroll
           for (int c = 0; c < HD / 4; ++c)
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
-                         ::"r"(kv_at + (uint32_t)(c * kTaRows + r) * 16), "f"(o[4 * c]), "f"(o[4 * c + 1]), "f"(o[4 * c + 2]),
+                         ::"r"(part + (uint32_t)(c * kTaRows + r) * 16), "f"(o[4 * c]), "f"(o[4 * c + 1]), "f"(o[4 * c + 2]),
                            "f"(o[4 * c + 3]) : "memory");
-          s_part[0][r] = m;
-          s_part[1][r] = l;
+          // and its reference and sum, in the warp's room for rows
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(m), "f"(l) : "memory");
           __syncwarp();
-          if (lane == 0) ta_arrive_peer(ta_map_peer(smem_u32(&part_full), (uint32_t)(1 - rank)));
+          if (lane == 0) ta_arrive_peer(ta_map_peer(smem_u32(&part_full), (uint32_t)t));
           continue;
         }
         bool got = ta_wait(&part_full, 0, &s_abort);
@@ -795,23 +811,24 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         ok = ok && got;
         if (ok) {
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
-          const uint32_t pm = ta_map_peer(smem_u32(&s_part[0][r]), (uint32_t)(1 - rank));
-          const uint32_t pl = ta_map_peer(smem_u32(&s_part[1][r]), (uint32_t)(1 - rank));
-          float m2, l2;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m2) : "r"(pm) : "memory");
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l2) : "r"(pl) : "memory");
-          const float to = fmaxf(m, m2), f1 = ta_exp2(m - to), f2 = ta_exp2(m2 - to);
-          const uint32_t po = ta_map_peer(kv_at + (uint32_t)r * 16, (uint32_t)(1 - rank));
+          for (int peer = 0; peer < ta.split; ++peer) {
+            if (peer == rank) continue;
+            float m2, l2;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(m2), "=f"(l2) : "r"(ta_map_peer(stage + lane * 8, (uint32_t)peer)) : "memory");
+            const float to = fmaxf(m, m2), f1 = ta_exp2(m - to), f2 = ta_exp2(m2 - to);
+            const uint32_t po = ta_map_peer(part + (uint32_t)r * 16, (uint32_t)peer);
 #pragma unroll
-          for (int c = 0; c < HD / 4; ++c) {
-            const float4 y = ta_ld_peer(po + (uint32_t)(c * kTaRows) * 16);
-            o[4 * c] = o[4 * c] * f1 + y.x * f2;
-            o[4 * c + 1] = o[4 * c + 1] * f1 + y.y * f2;
-            o[4 * c + 2] = o[4 * c + 2] * f1 + y.z * f2;
-            o[4 * c + 3] = o[4 * c + 3] * f1 + y.w * f2;
+            for (int c = 0; c < HD / 4; ++c) {
+              const float4 y = ta_ld_peer(po + (uint32_t)(c * kTaRows) * 16);
+              o[4 * c] = o[4 * c] * f1 + y.x * f2;
+              o[4 * c + 1] = o[4 * c + 1] * f1 + y.y * f2;
+              o[4 * c + 2] = o[4 * c + 2] * f1 + y.z * f2;
+              o[4 * c + 3] = o[4 * c + 3] * f1 + y.w * f2;
+            }
+            m = to;
+            l = l * f1 + l2 * f2;
           }
-          m = to;
-          l = l * f1 + l2 * f2;
         }
       }
       // rows out; a wait that gave up leaves NaN, not a wrong number
@@ -872,7 +889,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
   // a block's sums stay until its peer has read them
-  if (ta.split == 2)
+  if (ta.split > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -941,11 +958,18 @@ cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st) {
   // SMs four rounds of items.
   ta.chunk = std::max(1, std::min(a.hkv * a.seqs, (4 * num_sms + ta.pairs - 1) / ta.pairs));
   const int64_t items = (int64_t)a.hkv * a.seqs * ta.pairs;
-  if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+  if (items > 0x1fffffffLL) return cudaErrorInvalidConfiguration;
   ta.items = (int)items;
   // items that can hold rows: no more than the tokens fill, and one ragged pair a sequence
   const int64_t most = a.hkv * std::min<int64_t>((int64_t)a.seqs * ta.pairs, a.tokens / (2 * ta.tpt) + a.seqs);
-  ta.split = most <= num_sms ? 2 : 1;
+  // Two blocks an item where items leave half of the SMs idle, or where they
+  // fill them less than once with walks of very different lengths (64 items of
+  // 128 steps: 178 -> 99 us; 128 equal items of 32 steps: 53 us, and 67 split).
+  const int64_t max_keys = a.paged ? (int64_t)a.max_pages << a.page_shift : std::min(a.max_q, a.tokens);
+  const bool uneven = (int64_t)a.seqs * a.max_q * 2 > 3LL * a.tokens;
+  ta.split = most * (uneven ? 1 : 2) <= num_sms && max_keys >= 16 * kTaKeys ? 2 : 1;
+  // new tokens few beside their contexts: a walk's length is its sequence's
+  ta.by_length = a.paged && a.seqs <= 32 && max_keys >= 2LL * a.max_q ? 1 : 0;
   const int ps = a.paged ? 1 << a.page_shift : kTaKeys;
   ta.box_rows = std::min(ps, kTaKeys);
   bool ok = ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt);
