@@ -31,33 +31,76 @@ namespace sv {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 constexpr int kScaleMax = 60;     // |e| of an 8-bit row's power of two
+constexpr int kRowBatch = 2;      // rows of a thread in flight
 constexpr int kMaxTokBlock = 16;  // tokens of a block
 
-SV_DEV float2 turn_cos_sin(const spec_rope& r, int i, int pos, float sign) {
+SV_DEV void turn_cos_sin(const spec_rope& r, int i, int pos, float sign, float* cos_out, float* sin_out) {
   const uint64_t ph = r.turn[i] * (uint64_t)(int64_t)pos;
   float s, c;
   sincospif((float)(int32_t)(ph >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-  return make_float2(c * r.mscale, s * r.mscale * sign);
+  *cos_out = c * r.mscale;
+  *sin_out = s * r.mscale * sign;
+}
+// n / d for n * d < 2^32, by m = ceil(2^32 / d) (0 for d = 1).
+SV_DEV int quick_div(int n, uint32_t m) { return m ? (int)__umulhi((uint32_t)n, m) : n; }
+uint32_t div_magic(int64_t d) { return d <= 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); }
+
+// Two fp32 values in a register pair, one instruction for both.
+SV_DEV uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+SV_DEV void split2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+SV_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Largest magnitude; a NaN stays one.
+SV_DEV float abs_max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
 }
 
-// V adjacent elements as fp32.
+// V adjacent elements as they lie (held while their loads are in flight), and
+// as fp32.
 template <typename T, int V>
-SV_DEV void load_v(const T* p, float (&x)[V]) {
-  if constexpr (V == 8 && sizeof(T) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
-    x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
-  } else if constexpr (V == 8) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
+struct RawV {
+  static constexpr int n = V == 8 ? (int)sizeof(T) / 2 : 1;
+  uint4 w[V == 8 ? n : 1];
+  T x;
+  SV_DEV void load(const T* p) {
+    if constexpr (V == 8) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f32(p[i]);
+      for (int i = 0; i < n; ++i) w[i] = *(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+      x = *p;
+    }
   }
-}
+  SV_DEV void get(float (&y)[V]) const {
+    if constexpr (V == 8 && sizeof(T) == 2) {
+      y[0] = bf16lo(w[0].x); y[1] = bf16hi(w[0].x); y[2] = bf16lo(w[0].y); y[3] = bf16hi(w[0].y);
+      y[4] = bf16lo(w[0].z); y[5] = bf16hi(w[0].z); y[6] = bf16lo(w[0].w); y[7] = bf16hi(w[0].w);
+    } else if constexpr (V == 8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        y[4 * i] = __uint_as_float(w[i].x); y[4 * i + 1] = __uint_as_float(w[i].y);
+        y[4 * i + 2] = __uint_as_float(w[i].z); y[4 * i + 3] = __uint_as_float(w[i].w);
+      }
+    } else {
+      y[0] = to_f32(x);
+    }
+  }
+};
 SV_DEV uint32_t pack2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -90,36 +133,45 @@ SV_DEV void unit_chunks(int u, int rot, int inter, int* a, int* b) {
     *b = 2 * u + 1;
   }
 }
-// Rotates the two chunks of unit u (xa, xb) by the token's cos / sin table.
+// Rotates the two chunks of unit u (xa, xb) by the token's cosines and sines.
 template <int V>
-SV_DEV void unit_rotate(float (&xa)[V], float (&xb)[V], int u, int rot, int inter, const float2* cs) {
-  if (!inter) {
-    if (u >= rot / (2 * V)) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 w = cs[u * V + i];
-      const float p = xa[i], q = xb[i];
-      xa[i] = p * w.x - q * w.y;
-      xb[i] = q * w.x + p * w.y;
-    }
-  } else if constexpr (V == 1) {
+SV_DEV void unit_rotate(float (&xa)[V], float (&xb)[V], int u, int rot, int inter, const float* co, const float* si) {
+  if constexpr (V == 1) {
     if (u >= rot / 2) return;
-    const float2 w = cs[u];
-    const float p = xa[0], q = xb[0];
-    xa[0] = p * w.x - q * w.y;
-    xb[0] = q * w.x + p * w.y;
+    const float c = co[u], n = si[u], p = xa[0], q = xb[0];
+    xa[0] = p * c - q * n;
+    xb[0] = q * c + p * n;
   } else {
+    // the unit's eight angles: of elements V u .. (halves), or of pairs 8 u .. (interleaved)
+    if (u * 2 * V >= rot) return;
+    float c[8], n[8];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int c = 2 * u + half;
-      if (c * V >= rot) return;
+    for (int i = 0; i < 8; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(co + u * 8 + i), y = *reinterpret_cast<const float4*>(si + u * 8 + i);
+      c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
+      n[i] = y.x; n[i + 1] = y.y; n[i + 2] = y.z; n[i + 3] = y.w;
+    }
+    if (!inter) {
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const float2 w = cs[(c * V + i) / 2];
-        float* x = half ? xb : xa;
-        const float p = x[i], q = x[i + 1];
-        x[i] = p * w.x - q * w.y;
-        x[i + 1] = q * w.x + p * w.y;
+      for (int i = 0; i < 8; i += 2) {
+        const uint64_t p = pair2(xa[i], xa[i + 1]), q = pair2(xb[i], xb[i + 1]);
+        const uint64_t cc = pair2(c[i], c[i + 1]), nn = pair2(n[i], n[i + 1]), mn = pair2(-n[i], -n[i + 1]);
+        split2(fma2(q, mn, mul2(p, cc)), xa[i], xa[i + 1]);
+        split2(fma2(p, nn, mul2(q, cc)), xb[i], xb[i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint64_t x = pair2(xa[i], xa[i + 1]), y = pair2(xa[i + 1], xa[i]);
+        split2(fma2(y, pair2(-n[i / 2], n[i / 2]), mul2(x, pair2(c[i / 2], c[i / 2]))), xa[i], xa[i + 1]);
+      }
+      if ((2 * u + 1) * V < rot) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const uint64_t x = pair2(xb[i], xb[i + 1]), y = pair2(xb[i + 1], xb[i]);
+          const float cc = c[4 + i / 2], nn = n[4 + i / 2];
+          split2(fma2(y, pair2(-nn, nn), mul2(x, pair2(cc, cc))), xb[i], xb[i + 1]);
+        }
       }
     }
   }
@@ -132,6 +184,7 @@ struct RopeArgs {
   int64_t xt, xh, yt, yh;
   const int32_t* pos;
   int tokens, heads, hd, tpb, hpb;
+  uint32_t m_per, m_unit;   // quick_div of a block's units by those of a token, of a head
   float sign;
   spec_rope r;
 };
@@ -140,34 +193,47 @@ struct RopeArgs {
 // two chunks (V = 8: 16-byte accesses; V = 1 for odd sizes and alignments).
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  extern __shared__ float2 cs[];
-  const int rot = a.r.rot_dim, np = rot / 2;
+  extern __shared__ __align__(16) float cs[];   // cosines [tpb][pad], sines [tpb][pad]
+  const int rot = a.r.rot_dim, np = rot / 2, pad = (np + 7) & ~7;
   const int t0 = blockIdx.x * a.tpb, nt = min(a.tpb, a.tokens - t0);
   const int h0 = blockIdx.y * a.hpb, nh = min(a.hpb, a.heads - h0);
-  for (int e = threadIdx.x; e < nt * np; e += blockDim.x)
-    cs[e] = turn_cos_sin(a.r, e % np, __ldg(a.pos + t0 + e / np), a.sign);
-  __syncthreads();
-  const int U = a.hd / (2 * V), per = nh * U;
-#pragma unroll 2
-  for (int e = threadIdx.x; e < nt * per; e += blockDim.x) {
-    const int t = e / per, w = e - t * per, h = w / U, u = w - h * U;
-    int ca, cb;
+  float* const si = cs + a.tpb * pad;
+  // (a block's last heads may be fewer: units past them are skipped)
+  const int U = a.hd / (2 * V), per = a.hpb * U, total = nt * per;
+  for (int e = threadIdx.x, pass = 0; pass == 0 || e < total; e += blockDim.x, ++pass) {
+    const int t = quick_div(e, a.m_per), w = e - t * per, h = quick_div(w, a.m_unit), u = w - h * U;
+    const bool live = e < total && h < nh;
+    int ca = 0, cb = 0;
     unit_chunks<V>(u, rot, a.r.interleaved, &ca, &cb);
-    const TI* x = (const TI*)a.x + (t0 + t) * a.xt + (h0 + h) * a.xh;
-    TO* y = (TO*)a.y + (t0 + t) * a.yt + (h0 + h) * a.yh;
-    float xa[V], xb[V];
-    load_v<TI, V>(x + ca * V, xa);
-    load_v<TI, V>(x + cb * V, xb);
-    unit_rotate<V>(xa, xb, u, rot, a.r.interleaved, cs + t * np);
-    store_v<TO, V>(y + ca * V, xa);
-    store_v<TO, V>(y + cb * V, xb);
+    RawV<TI, V> ra, rb;
+    if (live) {
+      const TI* x = (const TI*)a.x + (t0 + t) * a.xt + (h0 + h) * a.xh;
+      ra.load(x + ca * V);
+      rb.load(x + cb * V);
+    }
+    if (pass == 0) {   // the first loads are on their way while the angles are worked out
+      for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
+        const int tt = i / np, k = i - tt * np;
+        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), a.sign, cs + tt * pad + k, si + tt * pad + k);
+      }
+      __syncthreads();
+    }
+    if (live) {
+      TO* y = (TO*)a.y + (t0 + t) * a.yt + (h0 + h) * a.yh;
+      float xa[V], xb[V];
+      ra.get(xa);
+      rb.get(xb);
+      unit_rotate<V>(xa, xb, u, rot, a.r.interleaved, cs + t * pad, si + t * pad);
+      store_v<TO, V>(y + ca * V, xa);
+      store_v<TO, V>(y + cb * V, xb);
+    }
   }
 }
 
 template <typename TI, typename TO>
 cudaError_t launch_rope(const RopeArgs& a, bool vec, cudaStream_t st) {
   const dim3 grid((a.tokens + a.tpb - 1) / a.tpb, (a.heads + a.hpb - 1) / a.hpb);
-  const size_t smem = (size_t)a.tpb * (a.r.rot_dim / 2) * sizeof(float2);
+  const size_t smem = (size_t)a.tpb * ((a.r.rot_dim / 2 + 7) & ~7) * 2 * sizeof(float);
   return vec ? launch_rows(rope_kernel<TI, TO, 8>, grid, dim3(kRowThreads), smem, 1, st, a)
              : launch_rows(rope_kernel<TI, TO, 1>, grid, dim3(kRowThreads), smem, 1, st, a);
 }
@@ -213,50 +279,70 @@ struct AppendArgs {
   const int32_t* seq;
   const int32_t* pos;
   int tokens, tpb;
+  uint32_t m_heads;  // quick_div by the KV heads
   spec_rope r;       // rot_dim 0: no rotation
 };
 
-// A row (token, head, k or v) is held by HD / (2 V UPL) adjacent lanes, UPL
+// Blocks of K and of V (z) differ in the rotation only.  A row (token, head) is held by HD / (2 V UPL) adjacent lanes, UPL
 // units of two chunks each: the row's largest magnitude is a shuffle away and
 // the row is read and written once.  V = 1 serves rotated parts that are no
 // multiple of 16 and unaligned inputs.
 template <typename T, int HD, int V, bool F8>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kUnits = HD / (2 * V), kLanes = kUnits < 32 ? kUnits : 32, kUpl = kUnits / kLanes;
-  extern __shared__ float2 cs[];
+  constexpr int kBatch = V == 8 ? kRowBatch : 1;
+  extern __shared__ __align__(16) float cs[];   // cosines [tpb][pad], sines [tpb][pad]
   __shared__ int2 slot[kMaxTokBlock];
-  const int rot = a.r.rot_dim, np = rot / 2;
+  const int isv = blockIdx.z;
+  const int rot = isv ? 0 : a.r.rot_dim, np = rot / 2, pad = (np + 7) & ~7;
   const int t0 = blockIdx.x * a.tpb, nt = min(a.tpb, a.tokens - t0);
-  if ((int)threadIdx.x < nt)
-    slot[threadIdx.x] = cache_slot(a.c, __ldg(a.seq + t0 + threadIdx.x), __ldg(a.pos + t0 + threadIdx.x));
-  for (int e = threadIdx.x; e < nt * np; e += blockDim.x)
-    cs[e] = turn_cos_sin(a.r, e % np, __ldg(a.pos + t0 + e / np), 1.f);
-  __syncthreads();
+  float* const si = cs + a.tpb * pad;
+  const T* const src = (const T*)(isv ? a.v : a.k) + t0 * (isv ? a.vt : a.kt);
+  const int64_t ts = isv ? a.vt : a.kt, hs = isv ? a.vh : a.kh;
   // in small calls grid.y blocks share a token's rows
-  const int rows = nt * a.c.hkv * 2;
+  const int rows = nt * a.c.hkv;
   const int stride = (int)(blockDim.x * gridDim.y) / kLanes;
   const int lane = threadIdx.x % kLanes;
-  for (int r0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) / kLanes; ; r0 += stride) {
-    // whole warps stay together for the shuffles
-    if (!__any_sync(0xffffffffu, r0 < rows)) break;
-    const bool live = r0 < rows;
-    const int row = live ? r0 : rows - 1;
-    const int isv = row & 1, h = (row >> 1) % a.c.hkv, t = (row >> 1) / a.c.hkv;
-    const T* x = isv ? (const T*)a.v + (t0 + t) * a.vt + h * a.vh : (const T*)a.k + (t0 + t) * a.kt + h * a.kh;
-    const int2 s = slot[t];
-    const int rr = isv ? 0 : rot;
-    float xa[kUpl][V], xb[kUpl][V];
-    int ca[kUpl], cb[kUpl];
+  int ca[kUpl], cb[kUpl];
 #pragma unroll
-    for (int j = 0; j < kUpl; ++j) {
-      const int u = j * kLanes + lane;
-      unit_chunks<V>(u, rr, a.r.interleaved, &ca[j], &cb[j]);
-      load_v<T, V>(x + ca[j] * V, xa[j]);
-      load_v<T, V>(x + cb[j] * V, xb[j]);
+  for (int j = 0; j < kUpl; ++j) unit_chunks<V>(j * kLanes + lane, rot, a.r.interleaved, &ca[j], &cb[j]);
+  for (int r0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) / kLanes, pass = 0;; r0 += kBatch * stride, ++pass) {
+    // whole warps stay together for the shuffles
+    if (pass && !__any_sync(0xffffffffu, r0 < rows)) break;
+    RawV<T, V> ra[kBatch][kUpl], rb[kBatch][kUpl];   // rows in flight
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int row = min(r0 + q * stride, rows - 1);
+      const int t = quick_div(row, a.m_heads), h = row - t * a.c.hkv;
+      const T* x = src + t * ts + h * hs;
+#pragma unroll
+      for (int j = 0; j < kUpl; ++j) {
+        ra[q][j].load(x + ca[j] * V);
+        rb[q][j].load(x + cb[j] * V);
+      }
+    }
+    if (pass == 0) {   // the first rows are on their way while slots and angles are worked out
+      if ((int)threadIdx.x < nt)
+        slot[threadIdx.x] = cache_slot(a.c, __ldg(a.seq + t0 + threadIdx.x), __ldg(a.pos + t0 + threadIdx.x));
+      for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
+        const int tt = i / np, k = i - tt * np;
+        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), 1.f, cs + tt * pad + k, si + tt * pad + k);
+      }
+      __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < kUpl; ++j)
-      if (rr) unit_rotate<V>(xa[j], xb[j], j * kLanes + lane, rr, a.r.interleaved, cs + t * np);
+    for (int q = 0; q < kBatch; ++q) {
+    const bool live = r0 + q * stride < rows;
+    const int row = min(r0 + q * stride, rows - 1);
+    const int t = quick_div(row, a.m_heads), h = row - t * a.c.hkv;
+    const int2 s = slot[t];
+    float xa[kUpl][V], xb[kUpl][V];
+#pragma unroll
+    for (int j = 0; j < kUpl; ++j) {
+      ra[q][j].get(xa[j]);
+      rb[q][j].get(xb[j]);
+      if (rot) unit_rotate<V>(xa[j], xb[j], j * kLanes + lane, rot, a.r.interleaved, cs + t * pad, si + t * pad);
+    }
     const size_t base = (size_t)(h << a.c.shift) + s.y;
     if constexpr (!F8) {
       if (live && s.x >= 0) {
@@ -268,12 +354,12 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
         }
       }
     } else {
-      uint32_t m = 0;   // largest magnitude as bits: infinities and NaN sort above every number
+      float top = 0.f;   // largest magnitude; as bits, infinities and NaN sort above every number
 #pragma unroll
       for (int j = 0; j < kUpl; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          m = max(m, max(__float_as_uint(xa[j][i]) & 0x7fffffffu, __float_as_uint(xb[j][i]) & 0x7fffffffu));
+        for (int i = 0; i < V; ++i) top = abs_max3(top, xa[j][i], xb[j][i]);
+      uint32_t m = __float_as_uint(top);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       // 448 = 1.75 * 2^8: smallest e with magnitude <= 448 * 2^e
@@ -290,14 +376,16 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
             const float* y = half ? xb[j] : xa[j];
             uint8_t* p = d + (half ? cb[j] : ca[j]) * V;
             if constexpr (V == 8) {
+              const uint64_t ff = pair2(f, f);
               uint32_t w[2];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * q] * f, y[4 * q + 1] * f),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * q + 2] * f, y[4 * q + 3] * f),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                w[q] = bad ? 0u : lo | (hi << 16);
+              for (int w4 = 0; w4 < 2; ++w4) {
+                float2 lo, hi;
+                split2(mul2(pair2(y[4 * w4], y[4 * w4 + 1]), ff), lo.x, lo.y);
+                split2(mul2(pair2(y[4 * w4 + 2], y[4 * w4 + 3]), ff), hi.x, hi.y);
+                w[w4] = __nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                        ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
+                if (bad) w[w4] = 0u;
               }
               *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
             } else {
@@ -310,13 +398,14 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
         }
       }
     }
+    }
   }
 }
 
 template <typename T, int HD, int V>
 cudaError_t launch_append(const AppendArgs& a, bool f8, int ysplit, cudaStream_t st) {
-  const dim3 grid((a.tokens + a.tpb - 1) / a.tpb, ysplit);
-  const size_t smem = (size_t)a.tpb * (a.r.rot_dim / 2) * sizeof(float2);
+  const dim3 grid((a.tokens + a.tpb - 1) / a.tpb, ysplit, 2);   // z: K, V
+  const size_t smem = (size_t)a.tpb * ((a.r.rot_dim / 2 + 7) & ~7) * 2 * sizeof(float);
   return f8 ? launch_rows(append_kernel<T, HD, V, true>, grid, dim3(kRowThreads), smem, 1, st, a)
             : launch_rows(append_kernel<T, HD, V, false>, grid, dim3(kRowThreads), smem, 1, st, a);
 }
@@ -337,6 +426,7 @@ struct GatherArgs {
   void* k;
   void* v;
   int tokens, tpb;
+  uint32_t m_per;    // quick_div of a block's chunks by those of a token
 };
 
 // A thread takes 16 bytes of a row (8 bf16 values or 16 codes).
@@ -355,7 +445,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const __grid_consta
   const int nc = a.c.hd / kVals, cshift = 31 - __clz(nc), per = a.c.hkv << cshift;
 #pragma unroll 4
   for (int e = threadIdx.x; e < nt * per; e += blockDim.x) {
-    const int t = e / per, w = e - t * per, h = w >> cshift, c = w & (nc - 1);
+    const int t = quick_div(e, a.m_per), w = e - t * per, h = w >> cshift, c = w & (nc - 1);
     const int2 s = slot[t];
     const size_t row = (size_t)(h << a.c.shift) + s.y;
     uint4 x = make_uint4(0, 0, 0, 0);
@@ -516,12 +606,14 @@ int spec_rope_rows(const void* x, int x_dtype, int64_t x_tok_stride, int64_t x_h
   // about a thousand units a block where there are many tokens; for few, the
   // heads of a token are spread over blocks of one unit a thread
   const int upt = head_dim / (vec ? 16 : 2);
-  a.hpb = heads;
-  a.tpb = std::max(1, std::min(kMaxTokBlock, 4 * kRowThreads / std::max(1, heads * upt)));
-  if ((int64_t)tokens * heads * upt < 600LL * kRowThreads) {
+  a.hpb = std::min(heads, std::max(1, 8192 / upt));
+  a.tpb = std::max(1, std::min(kMaxTokBlock, 4 * kRowThreads / (a.hpb * upt)));
+  if ((int64_t)tokens * heads * upt < 1200LL * kRowThreads) {
     a.tpb = 1;
-    a.hpb = std::max(1, std::min(heads, kRowThreads / upt));
+    a.hpb = std::max(1, std::min(a.hpb, kRowThreads / upt));
   }
+  a.m_per = div_magic((int64_t)a.hpb * upt);
+  a.m_unit = div_magic(upt);
   cudaStream_t st = (cudaStream_t)stream;
   const bool xi = x_dtype == SPEC_DTYPE_F32, yi = y_dtype == SPEC_DTYPE_F32;
   cudaError_t e;
@@ -548,10 +640,11 @@ int spec_kv_append(const spec_kv_cache* cache, const void* k, int64_t k_tok_stri
   if (plan) a.r = *plan;
   const bool vec = vec_ok(k, k_tok_stride, k_head_stride, dtype) && vec_ok(v, v_tok_stride, v_head_stride, dtype) &&
                    (!plan || plan->rot_dim % (plan->interleaved ? 8 : 16) == 0);
-  const int64_t per = (int64_t)cache->n_kv_heads * 2 * (cache->head_dim / (vec ? 16 : 2));   // threads a token
+  const int64_t per = (int64_t)cache->n_kv_heads * (cache->head_dim / (vec ? 16 : 2));   // threads a token's K or V
   a.tpb = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokBlock, 4 * kRowThreads / per));
+  a.m_heads = div_magic(cache->n_kv_heads);
   int ysplit = 1;
-  if (tokens * per < 600LL * kRowThreads) {
+  if (tokens * per < 1200LL * kRowThreads) {
     a.tpb = 1;
     ysplit = (int)std::max<int64_t>(1, std::min<int64_t>(8, per / kRowThreads));
   }
@@ -577,7 +670,8 @@ int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, const int32_t
   const bool f8 = cache->dtype == SPEC_DTYPE_E4M3;
   const int64_t per = (int64_t)cache->n_kv_heads * (cache->head_dim / (f8 ? 16 : 8));
   a.tpb = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokBlock, 4 * kRowThreads / per));
-  if (tokens * per < 600LL * kRowThreads) a.tpb = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokBlock, kRowThreads / per));
+  if (tokens * per < 1200LL * kRowThreads) a.tpb = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokBlock, kRowThreads / per));
+  a.m_per = div_magic(per);
   const dim3 grid((tokens + a.tpb - 1) / a.tpb, k_out && v_out ? 2 : 1);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
