@@ -89,7 +89,6 @@ struct PAttn {
 // Rows per KV head of the longest sequence up to which the register-tile
 // kernel takes a call that both can.
 constexpr int kPaMaxRows = 64;
-cudaError_t launch_pattn(const PAttn& a, int num_sms, cudaStream_t st);
 // Tensor-memory kernel: bf16 or e4m3 keys, head dim 64 or 128.
 bool pattn_tc_supported(const PAttn& a);
 cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st);

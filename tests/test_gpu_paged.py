@@ -495,6 +495,107 @@ def test_attn_paged_repeats_streams_and_graphs(dtype, n):
     assert torch.equal(outs[0], sv.attn_paged(q, c, cu, lens, max_q=n)[0])
 
 
+LONG = [  # few rows per KV head over contexts that fill the GPU: hq, hk, hd, page, new tokens, contexts
+    (32, 8, 128, 16, [6], [20000]),
+    (32, 8, 128, 16, [6] * 5, [3001, 129, 9000, 0, 128]),
+    (32, 8, 128, 64, [1, 1, 1], [4096, 7000, 3]),
+    (16, 2, 64, 16, [5, 4, 5], [16384, 20001, 1]),    # 40 rows: two tiles of 20
+    (32, 8, 64, 256, [1, 4], [6000, 5000]),
+    (7, 1, 128, 32, [3, 5], [40000, 5]),              # seven heads on one
+    (32, 8, 128, 32, [16, 0, 3], [5000, 10, 7000]),   # 64 rows, a sequence without new tokens
+    (4, 4, 128, 16, [4] * 40, [3, 2, 0, 1000] + [130 * b for b in range(36)]),
+    (64, 1, 128, 16, [1], [50000]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hk,hd,ps,ns,ctx", LONG)
+def test_attn_paged_long(hq, hk, hd, ps, ns, ctx, dtype):
+    c, q, cu, lens = _paged_case(sum(ctx) + hd, hq, hk, hd, ps, dtype, ns, ctx, pad=2)
+    out = _paged_check(c, q, cu, lens, ns, ctx, max_q=max(ns))
+    assert torch.equal(out, _paged_check(c, q, cu, lens, ns, ctx, max_q=max(ns)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attn_paged_long_sharp_scores(hd, dtype):
+    c, q, cu, lens = _paged_case(6, 16, 4, hd, 16, dtype, [3, 5], [12000, 900], sharp=30.0)
+    _paged_check(c, q, cu, lens, [3, 5], [12000, 900], max_q=5)
+    _paged_check(c, q, cu, lens, [3, 5], [12000, 900], max_q=5, scale=0.01)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attn_paged_long_wide_queries(hd):
+    """Queries of many sizes beside one large element."""
+    hq, hk, ctx = 8, 2, 30000
+    c, q, cu, lens = _paged_case(8, hq, hk, hd, 16, "e4m3", [4], [ctx])
+    g = _gen(3)
+    q = (q.float() * 2.0 ** -torch.randint(0, 10, q.shape, generator=g, device="cuda")).bfloat16()
+    q[..., 0] = 448.0
+    q = torch.where(q.abs() < 448 * 2.0 ** -13, 0, q)
+    _paged_check(c, q, cu, lens, [4], [ctx])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_paged_long_special_values(dtype):
+    """A NaN query row is NaN alone; a NaN key reaches the rows that see it; pages
+    outside the pool read as zero rows."""
+    hq, hk, hd, ctx = 8, 2, 128, 25000
+    c, q, cu, lens = _paged_case(9, hq, hk, hd, 16, dtype, [4], [ctx])
+    clean, _ = sv.attn_paged(q, c, cu, lens)
+    q2 = q.clone()
+    q2[1, 5, 7] = math.nan
+    out, _ = sv.attn_paged(q2, c, cu, lens)
+    assert torch.isnan(out[1, 5]).all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, 5] = False
+    assert torch.equal(out[keep], clean[keep])
+    table = c.table.clone()
+    t2 = table.clone()
+    t2[0, 700] = 2 ** 30
+    t2[0, 3] = -1
+    c.table.copy_(t2)
+    out, lse = sv.attn_paged(q, c, cu, lens)
+    c.table.copy_(table)
+    pos = torch.arange(ctx, device="cuda").int()
+    k, v = _read(c, _values(c), torch.zeros_like(pos), pos)
+    for p in (3, 700):
+        k[16 * p:16 * p + 16], v[16 * p:16 * p + 16] = 0, 0
+    _check_rows(out, lse, _attend_ref(q, k, v, 4, hd ** -0.5), ctx, hd)
+    bad = torch.full((1, hk, hd), math.nan, device="cuda")
+    sv.kv_append(c, bad, bad, _i32([0]), _i32([ctx - 2]))   # tokens 2 and 3 see it
+    out, _ = sv.attn_paged(q, c, cu, lens)
+    assert torch.isnan(out[2:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_paged_long_overlaps_and_graphs(dtype):
+    """Calls on two streams at once and replayed graphs give the bits of one call alone."""
+    ns, ctx = [4, 4, 4], [9000, 4000, 17000]
+    c, q, cu, lens = _paged_case(12, 32, 8, 128, 16, dtype, ns, ctx)
+    q2 = q.flip(0).contiguous()
+    ref, ref2 = (sv.attn_paged(x, c, cu, lens, max_q=4)[0] for x in (q, q2))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, got2 = [], []
+    for _ in range(4):
+        with torch.cuda.stream(a):
+            got.append(sv.attn_paged(q, c, cu, lens, max_q=4)[0])
+        with torch.cuda.stream(b):
+            got2.append(sv.attn_paged(q2, c, cu, lens, max_q=4)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, ref) for x in got) and all(torch.equal(x, ref2) for x in got2)
+    gr, o = torch.cuda.CUDAGraph(), torch.zeros_like(ref)
+    with torch.cuda.graph(gr):
+        sv.attn_paged(q, c, cu, lens, max_q=4, out=o)
+    for new in (ctx, [1, 17000, 4], [0, 0, 0], [17000, 17000, 17000]):
+        lens.copy_(_i32(new))
+        gr.replay()
+        torch.cuda.synchronize()
+        # (as bits: the longer lengths reach slots that hold NaN)
+        assert torch.equal(o.view(torch.int16), sv.attn_paged(q, c, cu, lens, max_q=4)[0].view(torch.int16))
+
+
 PROMPT = [  # hq, hk, hd, lengths
     (8, 2, 64, [130, 1, 77]),
     (32, 8, 128, [17]),
