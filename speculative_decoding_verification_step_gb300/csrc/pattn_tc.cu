@@ -789,9 +789,10 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         for (int c = 0; c < HD; ++c) o[c] = 0.f;
       }
       if (ta.split > 1) {
-        // one item a block: the ring is free once both tiles' products are done
-        const int other = it.steps[1 - t];
-        if (ok && other > 0) ok = __all_sync(0xffffffffu, ta_wait(&pv_done[1 - t], (unsigned)((other - 1) & 1), &s_abort));
+        // One item a block: the ring is free once both tiles' products are done.
+        // (Each tile's warps have waited for their own, step by step; a wait for the
+        // other tile's last one by its parity could pass two steps early.)
+        if (it.ntile == 2) named_sync(1, 256);
         const uint32_t part = kv_at + t * 2 * kTile;       // [dims / 4][row] of four sums
         if (t != rank) {                       // for the tile's finisher
           if (!ok) l = __uint_as_float(0x7fffffffu);

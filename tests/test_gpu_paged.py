@@ -505,6 +505,8 @@ LONG = [  # few rows per KV head over contexts that fill the GPU: hq, hk, hd, pa
     (32, 8, 128, 32, [16, 0, 3], [5000, 10, 7000]),   # 64 rows, a sequence without new tokens
     (4, 4, 128, 16, [4] * 40, [3, 2, 0, 1000] + [130 * b for b in range(36)]),
     (64, 1, 128, 16, [1], [50000]),
+    (32, 8, 128, 16, [9] * 16 + [1], [700, 9, 3, 1000] + [100 * b for b in range(13)]),   # 36 rows, items for all SMs
+    (32, 8, 64, 64, [13, 16, 2] * 6, [90 * b for b in range(18)]),
 ]
 
 
@@ -627,6 +629,25 @@ def test_attn_prompt(hq, hk, hd, ns):
             if n:
                 _check_rows(out[r], lse[r], _attend_ref(q[r], k[r], v[r], n, hd ** -0.5), n, hd)
         assert (out[total:] == 7.0).all() and (lse[total:] == 9.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attn_paged_chunks_repeat(hd, dtype):
+    """Chunks over contexts of many lengths, few enough for two blocks an item: the
+    same bits every time, beside other work, and right."""
+    ns, ctx = [256, 130, 64, 1], [5000, 3333, 6001, 700]
+    c, q, cu, lens = _paged_case(21, 16, 4, hd, 64, dtype, ns, ctx)
+    ref = _paged_check(c, q, cu, lens, ns, ctx, max_q=256)
+    side, noise = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for i in range(60):
+        with torch.cuda.stream(side):
+            noise.add_(1.0)
+        got.append(sv.attn_paged(q, c, cu, lens, max_q=256)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, ref) for x in got)
 
 
 def test_prompt_neighbours_do_not_leak():
