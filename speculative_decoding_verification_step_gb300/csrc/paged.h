@@ -86,8 +86,8 @@ struct PAttn {
   int64_t table_stride;
   int pages, page_shift, max_pages;
 };
-// Rows per KV head of the longest sequence up to which the register-tile
-// kernel takes a call that both can.
+// Rows per KV head of the longest sequence beyond which the tensor-memory
+// kernel takes every call that both can.
 constexpr int kPaMaxRows = 64;
 // Tensor-memory kernel: bf16 or e4m3 keys, head dim 64 or 128.
 bool pattn_tc_supported(const PAttn& a);

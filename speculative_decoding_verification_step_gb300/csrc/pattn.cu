@@ -631,12 +631,22 @@ int run_attention(PAttn& a, const char* who, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
-  // Up to kPaMaxRows rows per KV head the register-tile kernel, beyond the
-  // tensor-memory one where it applies.  A batch with both kinds goes to the
-  // latter whole: a short sequence costs it one tile's walk over the keys
-  // beside the long ones, less than a second launch behind them.
-  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv);
-  if (rows > kPaMaxRows && pattn_tc_supported(a)) e = launch_pattn_tc(a, sms, st);
+  // Up to 32 rows per KV head the register-tile kernel, beyond kPaMaxRows the
+  // tensor-memory one where it applies.  Between them the first walks the keys
+  // once per 32 rows but cuts them between up to eight blocks, the second walks
+  // them once for all rows: it is taken where (sequence, KV head) pairs keep its
+  // blocks busy, at head dim 64 only from 49 rows and 16-bit keys on.  Measured,
+  // tensor memory against register tiles, 4096 keys, 8 KV heads, head dim 128:
+  // 64 rows of 16 sequences 60 / 74 us (8-bit keys 83 / 89), of 8 sequences
+  // 39 / 47 (49 / 54), of 4 36 / 30; 36 rows of 16 sequences 60 / 77 (83 / 92),
+  // of 12 60 / 52.  Head dim 64: 64 rows of 16 sequences 44 / 57 (70 / 70), of
+  // 12 44 / 39; 36 rows of 64 sequences 121 / 113 (197 / 156).  A batch with
+  // both kinds goes whole: a short sequence costs the tensor-memory kernel one
+  // tile's walk over the keys beside the long ones, less than a second launch
+  // behind them.
+  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), pairs = (int64_t)a.seqs * a.hkv;
+  const bool many = rows > 48, busy = a.hd == 128 ? pairs * (many ? 8 : 4) >= 3 * sms : many && !a.f8 && pairs * 4 >= 3 * sms;
+  if ((rows > kPaMaxRows || (rows > 32 && busy)) && pattn_tc_supported(a)) e = launch_pattn_tc(a, sms, st);
   else e = a.hd == 32 ? launch_pa_hd<32>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64>(a, sms, st) : launch_pa_hd<128>(a, sms, st);
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
 }
