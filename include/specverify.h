@@ -433,15 +433,24 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * the grid), are left as they were.  A length past the table's positions is cut
  * there; a table entry that is not a page of the pool reads as zero rows.
  * scale >= 0; 0: 1/sqrt(head_dim).  Scores, softmax statistics and sums are fp32,
- * probabilities bf16 in the product with v.  Cache slots past a sequence's
+ * probabilities bf16 in the product with v; over an e4m3 cache elements of q
+ * below 2^-10 of their row's largest may be rounded by up to 2^-17 of that.
+ * Cache slots past a sequence's
  * length are never used, whatever they hold; a value row that is not finite
  * within the length reaches the outputs of the whole chunk.
+ * workspace: device memory, 16-byte aligned, of workspace_bytes (what it holds
+ * before and after means nothing; calls that may overlap need their own), or
+ * NULL: with fewer bytes than spec_attn_paged_workspace says the call is
+ * computed another way, a few roundings apart and slower.
  * Checked: n_heads a multiple of n_kv_heads; 16-byte aligned q and out with
  * strides multiples of 8. */
 SPEC_API int spec_attn_paged(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
                     const int32_t* cu_q, const int32_t* kv_lens, int tokens, int max_q, int n_heads,
                     float scale, void* out, int64_t out_tok_stride, int64_t out_head_stride, float* lse,
-                    void* stream);
+                    void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes of workspace that spec_attn_paged wants for a call of these sizes; 0
+ * where it has no use for one. */
+SPEC_API int64_t spec_attn_paged_workspace(const spec_kv_cache* cache, int tokens, int max_q, int n_heads);
 
 /* Causal attention within packed sequences: rows cu[b] .. cu[b+1] - 1 of q
  * [tokens][n_heads][head_dim] and of k and v [tokens][n_kv_heads][head_dim]

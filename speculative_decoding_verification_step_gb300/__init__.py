@@ -148,7 +148,8 @@ SIGNATURES = {
     "spec_kv_append": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _INT, _VP, _VP, _INT, _VP, _VP]),
     "spec_kv_gather": (ctypes.c_int, [_VP, _VP, _VP, _INT, _VP, _VP, _INT, _VP]),
     "spec_attn_paged": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _VP, _INT, _INT, _INT, ctypes.c_float,
-                                       _VP, _I64, _I64, _VP, _VP]),
+                                       _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
+    "spec_attn_paged_workspace": (ctypes.c_int64, [_VP, _INT, _INT, _INT]),
     "spec_attn_prompt": (ctypes.c_int, [_VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _INT, _INT,
                                         _INT, _INT, _INT, _INT, ctypes.c_float, _VP, _I64, _I64, _VP, _VP]),
     "spec_profile": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.POINTER(Profile)]),
@@ -530,6 +531,7 @@ class KVCache:
                               pages, ps, heads, hd, k.stride(0), k_scale.stride(0) if f8 else 0,
                               table.data_ptr(), table.stride(0), self.seqs, self.max_pages)
         self._ref = ctypes.byref(self._c)
+        self._ws = {}                        # workspace bytes of attn_paged calls by their sizes
 
     @classmethod
     def empty(cls, pages, page_size, n_kv_heads, head_dim, table, dtype="bf16"):
@@ -647,9 +649,26 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
     _index("kv_lens", kv_lens, seqs, dev)
     out, lse = _attn_out(q, shape, dev, out, lse)
     os_ = _rows3("out", out)
+    if max_q is None:
+        max_q = n
+    key = n, max_q, h
+    need = cache._ws.get(key)                # a function of the sizes alone
+    if need is None:
+        with _t.cuda.device(dev):
+            need = lib().spec_attn_paged_workspace(cache._ref, n, max_q, h)
+        if len(cache._ws) > 4096:
+            cache._ws.clear()
+        cache._ws[key] = need
+    if not need:
+        ws = None
+    elif stream is None:
+        ws = _t.empty(need, dtype=_t.uint8, device=q.device)
+    else:                                    # memory that goes back to the stream that uses it
+        with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=q.device)):
+            ws = _t.empty(need, dtype=_t.uint8, device=q.device)
     _call(dev, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
-          kv_lens.data_ptr(), n, n if max_q is None else max_q, h, scale, out.data_ptr(), os_[0], os_[1],
-          lse.data_ptr() if lse is not False else None)
+          kv_lens.data_ptr(), n, max_q, h, scale, out.data_ptr(), os_[0], os_[1],
+          lse.data_ptr() if lse is not False else None, ws.data_ptr() if need else None, need)
     return out, (lse if lse is not False else None)
 
 

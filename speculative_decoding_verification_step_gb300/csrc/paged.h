@@ -85,6 +85,7 @@ struct PAttn {
   const int32_t* table;
   int64_t table_stride;
   int pages, page_shift, max_pages;
+  float* ws;                     // workspace of launch_pattn_td, or null
 };
 // Rows per KV head of the longest sequence beyond which the tensor-memory
 // kernel takes every call that both can.
@@ -92,5 +93,10 @@ constexpr int kPaMaxRows = 64;
 // Tensor-memory kernel: bf16 or e4m3 keys, head dim 64 or 128.
 bool pattn_tc_supported(const PAttn& a);
 cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st);
+// Few rows over paged 8-bit keys on tensor memory (head dim 64 or 128), with
+// a.ws of pattn_td_workspace bytes for `rows` rows per KV head.
+bool pattn_td_supported(const PAttn& a);
+size_t pattn_td_workspace(int64_t rows, int hd, int num_sms);
+cudaError_t launch_pattn_td(const PAttn& a, int num_sms, cudaStream_t st);
 
 }  // namespace sv

@@ -611,8 +611,28 @@ bool row_aligned(const void* p, int64_t ts, int64_t hs) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ts % 8 == 0 && hs % 8 == 0;
 }
 
+// Workspace of launch_pattn_td where it is taken, else 0.  It costs 5 us a tile
+// and 10 us for its start and join, and saves a third of a long context's time:
+// it is taken at head dim 128 for more than 8 rows (a decoded token's few leave
+// the register tiles bound by the copies: 64 x 4096 keys of 4 rows 97 / 115 us),
+// tables of 4096 positions or more and six units of 128 keys an SM; and for any
+// rows where (sequence, KV head, tile) items are so few that the register
+// tiles' clusters of eight blocks do not cover the SMs, from 16384 positions on.
+// The lengths being on the device, a table's width stands for them.  24 rows,
+// register tiles / this, us: 64 sequences x 4096 keys 152 / 126, x 2048 90 / 91,
+// x 512 40 / 54; 16 x 4096 54 / 52; 1 x 16384 46 / 31, 1 x 4096 18 / 25.  Head
+// dim 64: 64 x 4096 105 / 115, 1 x 16384 32 / 28, 1 x 65536 104 / 49.
+size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
+  if (!a.paged || rows < 1 || rows > kPaMaxRows || !pattn_td_supported(a)) return 0;
+  const int64_t keys = (int64_t)a.max_pages << a.page_shift, items = (int64_t)a.seqs * a.hkv * ((rows + 31) / 32);
+  const int64_t units = items * ((keys + 127) / 128);
+  if (units > 0x7fffffffLL) return 0;
+  const bool many = a.hd == 128 && rows > 8 && keys >= 4096 && units >= 6LL * sms, few = items * 8 <= sms && keys >= 16384;
+  return many || few ? pattn_td_workspace(rows, a.hd, sms) : 0;
+}
+
 // Both attention calls, after their own checks.
-int run_attention(PAttn& a, const char* who, cudaStream_t st) {
+int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
   const std::string w = std::string(who) + ": ";
   if (a.hq < 1 || a.hkv < 1 || a.hq % a.hkv || a.hq > 65535 || a.hkv > 1024)
     return fail(SPEC_E_SHAPE, w + "n_heads must be a multiple of n_kv_heads (at most 1024)");
@@ -647,8 +667,22 @@ int run_attention(PAttn& a, const char* who, cudaStream_t st) {
   const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), pairs = (int64_t)a.seqs * a.hkv;
   const bool many = rows > 48, busy = a.hd == 128 ? pairs * (many ? 8 : 4) >= 3 * sms : many && !a.f8 && pairs * 4 >= 3 * sms;
   if ((rows > kPaMaxRows || (rows > 32 && busy)) && pattn_tc_supported(a)) e = launch_pattn_tc(a, sms, st);
+  else if (const size_t need = td_bytes(a, rows, sms); need && a.ws && ws_bytes >= need) e = launch_pattn_td(a, sms, st);
   else e = a.hd == 32 ? launch_pa_hd<32>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64>(a, sms, st) : launch_pa_hd<128>(a, sms, st);
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
+}
+
+void cache_fields(PAttn& a, const spec_kv_cache* cache) {
+  a.seqs = cache->seqs; a.hkv = cache->n_kv_heads; a.hd = cache->head_dim;
+  a.paged = 1; a.f8 = cache->dtype == SPEC_DTYPE_E4M3;
+  a.k = cache->k; a.v = cache->v; a.ks = cache->k_scale; a.vs = cache->v_scale;
+  const int64_t row = (int64_t)cache->n_kv_heads * cache->page_size;
+  a.page_stride = cache->page_stride ? cache->page_stride : row * cache->head_dim;
+  a.scale_stride = cache->scale_page_stride ? cache->scale_page_stride : row;
+  a.table = cache->table;
+  a.table_stride = cache->table_stride ? cache->table_stride : cache->max_pages;
+  a.pages = cache->pages; a.max_pages = cache->max_pages;
+  while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
 }
 
 }  // namespace
@@ -661,26 +695,35 @@ extern "C" {
 
 int spec_attn_paged(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
                     const int32_t* cu_q, const int32_t* kv_lens, int tokens, int max_q, int n_heads, float scale,
-                    void* out, int64_t out_tok_stride, int64_t out_head_stride, float* lse, void* stream) {
+                    void* out, int64_t out_tok_stride, int64_t out_head_stride, float* lse, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
   const char* who = "spec_attn_paged";
   const int rc = check_cache(cache, who);
   if (rc) return rc;
   if (tokens > 0 && !kv_lens) return fail(SPEC_E_ARG, std::string(who) + ": null kv_lens");
+  if (workspace_bytes < 0 || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+    return fail(SPEC_E_ARG, std::string(who) + ": workspace must be 16-byte aligned");
   PAttn a{};
+  cache_fields(a, cache);
   a.q = q; a.q_ts = q_tok_stride; a.q_hs = q_head_stride;
-  a.cu = cu_q; a.lens = kv_lens; a.seqs = cache->seqs; a.tokens = tokens; a.max_q = max_q;
-  a.hq = n_heads; a.hkv = cache->n_kv_heads; a.hd = cache->head_dim; a.scale_log2 = scale;
+  a.cu = cu_q; a.lens = kv_lens; a.tokens = tokens; a.max_q = max_q;
+  a.hq = n_heads; a.scale_log2 = scale;
   a.out = out; a.o_ts = out_tok_stride; a.o_hs = out_head_stride; a.lse = lse;
-  a.paged = 1; a.f8 = cache->dtype == SPEC_DTYPE_E4M3;
-  a.k = cache->k; a.v = cache->v; a.ks = cache->k_scale; a.vs = cache->v_scale;
-  const int64_t row = (int64_t)cache->n_kv_heads * cache->page_size;
-  a.page_stride = cache->page_stride ? cache->page_stride : row * cache->head_dim;
-  a.scale_stride = cache->scale_page_stride ? cache->scale_page_stride : row;
-  a.table = cache->table;
-  a.table_stride = cache->table_stride ? cache->table_stride : cache->max_pages;
-  a.pages = cache->pages; a.max_pages = cache->max_pages;
-  while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
-  return run_attention(a, who, (cudaStream_t)stream);
+  a.ws = (float*)workspace;
+  return run_attention(a, workspace ? (size_t)workspace_bytes : 0, who, (cudaStream_t)stream);
+}
+
+int64_t spec_attn_paged_workspace(const spec_kv_cache* cache, int tokens, int max_q, int n_heads) {
+  if (check_cache(cache, "spec_attn_paged_workspace") || tokens < 1 || max_q < 1 || n_heads < 1 ||
+      n_heads % cache->n_kv_heads)
+    return 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  PAttn a{};
+  cache_fields(a, cache);
+  a.hq = n_heads;
+  return (int64_t)td_bytes(a, (int64_t)std::min(max_q, tokens) * (n_heads / a.hkv), sms);
 }
 
 int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* k, int64_t k_tok_stride,
@@ -700,7 +743,7 @@ int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
   a.hq = n_heads; a.hkv = n_kv_heads; a.hd = head_dim; a.scale_log2 = scale;
   a.out = out; a.o_ts = out_tok_stride; a.o_hs = out_head_stride; a.lse = lse;
   a.k = k; a.v = v; a.k_ts = k_tok_stride; a.k_hs = k_head_stride; a.v_ts = v_tok_stride; a.v_hs = v_head_stride;
-  return run_attention(a, who, (cudaStream_t)stream);
+  return run_attention(a, 0, who, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -507,6 +507,9 @@ LONG = [  # few rows per KV head over contexts that fill the GPU: hq, hk, hd, pa
     (64, 1, 128, 16, [1], [50000]),
     (32, 8, 128, 16, [9] * 16 + [1], [700, 9, 3, 1000] + [100 * b for b in range(13)]),   # 36 rows, items for all SMs
     (32, 8, 64, 64, [13, 16, 2] * 6, [90 * b for b in range(18)]),
+    (32, 8, 128, 16, [3] * 40, [5000, 1, 0, 2] + [97 * b for b in range(36)]),            # more sequences than lanes
+    (32, 8, 128, 128, [0, 6, 5, 0], [100, 4097, 8000, 0]),
+    (8, 1, 64, 16, [1, 3], [17000, 250]),
 ]
 
 
@@ -524,6 +527,8 @@ def test_attn_paged_long_sharp_scores(hd, dtype):
     c, q, cu, lens = _paged_case(6, 16, 4, hd, 16, dtype, [3, 5], [12000, 900], sharp=30.0)
     _paged_check(c, q, cu, lens, [3, 5], [12000, 900], max_q=5)
     _paged_check(c, q, cu, lens, [3, 5], [12000, 900], max_q=5, scale=0.01)
+    c, q, cu, lens = _paged_case(7, 32, 2, hd, 16, dtype, [2, 1], [17000, 129], sharp=30.0)
+    _paged_check(c, q, cu, lens, [2, 1], [17000, 129])
 
 
 @pytest.mark.parametrize("hd", [64, 128])
@@ -568,6 +573,36 @@ def test_attn_paged_long_special_values(dtype):
     sv.kv_append(c, bad, bad, _i32([0]), _i32([ctx - 2]))   # tokens 2 and 3 see it
     out, _ = sv.attn_paged(q, c, cu, lens)
     assert torch.isnan(out[2:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_paged_workspace(dtype):
+    """With and without a workspace, and with one too small: right either way, nothing past its end."""
+    ns, ctx, (hq, hk, hd) = [4, 3], [9000, 30000], (16, 4, 128)
+    c, q, cu, lens = _paged_case(14, hq, hk, hd, 32, dtype, ns, ctx)
+    L, n = sv.lib(), sum(ns)
+    need = L.spec_attn_paged_workspace(c._ref, n, 4, hq)
+    assert (need > 0) == (dtype == "e4m3")
+    ws = torch.full((need + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+    for size in (0, max(need - 16, 0), need):
+        out, lse = torch.zeros(n, hq, hd, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, hq, device="cuda")
+        assert L.spec_attn_paged(c._ref, q.data_ptr(), q.stride(0), q.stride(1), cu.data_ptr(), lens.data_ptr(), n, 4, hq, 0.0,
+                                 out.data_ptr(), hq * hd, hd, lse.data_ptr(), ws.data_ptr() if size else None, size,
+                                 torch.cuda.current_stream().cuda_stream) == 0
+        values, r = _values(c), 0
+        for b, (k, m) in enumerate(zip(ns, ctx)):
+            pos = torch.arange(m, device="cuda").int()
+            kk, vv = _read(c, values, torch.full_like(pos, b), pos)
+            _check_rows(out[r:r + k], lse[r:r + k], _attend_ref(q[r:r + k], kk, vv, k, hd ** -0.5), m, hd)
+            r += k
+        if size < need:
+            assert (ws == 0x5a).all()
+    assert (ws[need:] == 0x5a).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out2, _ = sv.attn_paged(q, c, cu, lens, max_q=4, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(out2, out)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])

@@ -40,14 +40,15 @@ def test_cache_refusals(L, change, code):
     c = ctypes.byref(_cache(**change))
     assert L.spec_kv_append(c, P, 128, 64, P, 128, 64, 1, P, P, 1, None, None) == code
     assert L.spec_kv_gather(c, P, P, 1, P, P, 1, None) == code
-    assert L.spec_attn_paged(c, P, 256, 64, P, P, 1, 1, 4, 0.0, P, 256, 64, None, None) == code
+    assert L.spec_attn_paged(c, P, 256, 64, P, P, 1, 1, 4, 0.0, P, 256, 64, None, None, 0, None) == code
     assert L.spec_last_error(None)
 
 
 def test_null_cache(L):
     assert L.spec_kv_append(None, P, 128, 64, P, 128, 64, 1, P, P, 1, None, None) == -1
     assert L.spec_kv_gather(None, P, P, 1, P, P, 1, None) == -1
-    assert L.spec_attn_paged(None, P, 256, 64, P, P, 1, 1, 4, 0.0, P, 256, 64, None, None) == -1
+    assert L.spec_attn_paged(None, P, 256, 64, P, P, 1, 1, 4, 0.0, P, 256, 64, None, None, 0, None) == -1
+    assert L.spec_attn_paged_workspace(None, 1, 1, 4) == 0
 
 
 def test_row_refusals(L):
@@ -78,9 +79,10 @@ def test_attention_refusals(L):
     c = ctypes.byref(_cache())
     att = lambda **k: L.spec_attn_paged(c, k.get("q", P), k.get("qs", 256), 64, k.get("cu", P), k.get("lens", P),
                                         k.get("n", 1), k.get("m", 1), k.get("h", 4), k.get("scale", 0.0),
-                                        k.get("out", P), 256, k.get("oh", 64), None, None)
+                                        k.get("out", P), 256, k.get("oh", 64), None, k.get("ws"), k.get("wb", 0), None)
     assert att(q=None) == att(cu=None) == att(lens=None) == att(out=None) == -1
     assert att(q=P + 2) == att(qs=260) == att(oh=4) == att(n=-1) == att(m=-1) == -1
+    assert att(ws=P + 4, wb=64) == att(ws=P, wb=-1) == -1
     assert att(scale=math.nan) == att(scale=math.inf) == att(scale=-1.0) == -1
     assert att(h=3) == att(h=0) == -3
     assert att(n=0) == att(m=0) == 0
@@ -95,7 +97,7 @@ def test_attention_refusals(L):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
 def test_no_cpu_fallback(L):
     c = ctypes.byref(_cache())
-    assert L.spec_attn_paged(c, P, 256, 64, P, P, 1, 1, 4, 0.0, P, 256, 64, None, None) == -5
+    assert L.spec_attn_paged(c, P, 256, 64, P, P, 1, 1, 4, 0.0, P, 256, 64, None, None, 0, None) == -5
     assert L.spec_kv_gather(c, P, P, 1, P, P, 1, None) == -5
 
 
