@@ -435,9 +435,9 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * scale >= 0; 0: 1/sqrt(head_dim).  Scores, softmax statistics and sums are fp32,
  * probabilities bf16 in the product with v; over an e4m3 cache elements of q
  * below 2^-10 of their row's largest may be rounded by up to 2^-17 of that.
- * Cache slots past a sequence's
- * length are never used, whatever they hold; a value row that is not finite
- * within the length reaches the outputs of the whole chunk.
+ * Cache slots past a sequence's length are never used, whatever they hold; a
+ * value row that is not finite within the length reaches the outputs of the
+ * whole chunk.
  * workspace: device memory, 16-byte aligned, of workspace_bytes (what it holds
  * before and after means nothing; calls that may overlap need their own), or
  * NULL: with fewer bytes than spec_attn_paged_workspace says the call is

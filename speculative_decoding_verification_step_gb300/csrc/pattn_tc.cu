@@ -45,6 +45,11 @@
 // With few items (chunks of a few sequences) a cluster of two blocks shares an
 // item's keys; block t finishes tile t with the other's sums, read from its
 // shared memory.
+// Bound by the tensor pipe, 64 rounds of exponentials next to it and the causal
+// triangle's ragged ends.  Measured at head dim 128, 32 heads on 8: six packed
+// prompts of 4096 276 us (1.31 PFLOP/s, 69% of the library product's rate), one
+// of 16384 1253 us (93%), 16 of 1024 142 us; four chunks of up to 512 tokens over
+// 16384 keys 164 us (1.1 PFLOP/s); head dim 64, four of 4096 297 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
