@@ -61,11 +61,14 @@ struct TdArgs {
   int runs;
 };
 
+// R rows of a tile are worked on (16, 24 or 32), cols columns of the products
+// are theirs: what lies in the rest is never read.
 template <int HD, int R>
 struct TdLayout {
+  static constexpr int cols = (R + 15) / 16 * 16;
   static constexpr int ks = 3, vs = 4, vb = 2;             // K and V tiles as copied, V tiles converted
   static constexpr uint32_t tile = kTdKeys * HD, vtile = kTdKeys * HD * 2;
-  static constexpr uint32_t q = R * HD * 2, p = kTdKeys * R * 2;   // (two terms of HD bytes)
+  static constexpr uint32_t q = cols * HD * 2, p = kTdKeys * cols * 2;   // (two terms of HD bytes)
   static constexpr uint32_t k_at = 0, v_at = ks * tile, vb_at = v_at + vs * tile, q_at = vb_at + vb * vtile,
                             p_at = q_at + 2 * q;
   static constexpr int smem = (int)(p_at + 2 * p) + 1024;
@@ -176,14 +179,14 @@ SV_DEV void td_next(const PAttn& a, int tile_rows, TdPart& p, int u, int u_end) 
 template <int HD, int R>
 __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_constant__ TdArgs ta) {
   using L = TdLayout<HD, R>;
-  constexpr int kHalf = HD / 64;
+  constexpr int C = L::cols, kHalf = HD / 64;
   constexpr int kSc = 8;                                   // K scales wait for the softmax, behind the ring
   extern __shared__ __align__(1024) unsigned char tsm[];
   __shared__ uint64_t k_full[L::ks], k_empty[L::ks], v_full[L::vs], v_empty[L::vs], b_full[2], b_empty[2];
   __shared__ uint64_t q_full[2], q_empty[2], s_full[4], p_full[4], pv_done[2], drained[2];
   __shared__ __align__(16) unsigned char s_ks[kSc][kTdKeys], s_vs[L::vs][kTdKeys];
-  __shared__ float s_qf[2][R], s_red[4][R], s_f[R];
-  __shared__ int64_t s_at[R];
+  __shared__ float s_qf[2][C], s_red[4][C], s_f[C];
+  __shared__ int64_t s_at[C];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_kfill, s_vfill;
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
   constexpr uint32_t kO = 128;               // columns: scores 0, 32, 64, 96; O^T 128
 
   // Q of tile k to its buffer: rows first, first + kStagers, ... of one warp
-  constexpr int kStagers = 8, kOwn = R / kStagers;
+  constexpr int kStagers = 8, kOwn = C / kStagers;
   auto stage = [&](const TdPart& w, int k, int first) {
     const int buf = k & 1;
     if (k >= 2 && !__all_sync(0xffffffffu, ta_wait(&q_empty[buf], (unsigned)((k / 2 - 1) & 1), &s_abort))) return false;
@@ -283,11 +286,11 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         lo |= (uint32_t)l << (16 * i);
       }
       if (bad) hi = 0x7f7f7f7fu, lo = 0;     // NaN codes: a masked score is still masked
-      // rows r (h) and R + r (l) of HD bytes
-      const int c = (kPer * lane) >> 4, sub = (kPer * lane) & 15;
+      // rows r (upper bits) and C + r (the rest) of HD bytes
+      const int chunk = (kPer * lane) >> 4, sub = (kPer * lane) & 15;
 #pragma unroll
       for (int term = 0; term < 2; ++term) {
-        const int rr = r + term * R, sw = HD == 128 ? c ^ (rr & 7) : c ^ ((rr >> 1) & 3);
+        const int rr = r + term * C, sw = HD == 128 ? chunk ^ (rr & 7) : chunk ^ ((rr >> 1) & 3);
         const uint32_t d = at + rr * HD + (sw << 4) + sub, v = term ? lo : hi;
         if constexpr (kPer == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d), "r"(v) : "memory");
         else asm volatile("st.shared.b16 [%0], %1;" ::"r"(d), "h"((uint16_t)v) : "memory");
@@ -419,8 +422,8 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
     } else {
       // ---- products: warp 5 the scores, warp 6 O^T (converged, one elected lane issues) ----
       constexpr uint32_t kId = (1u << 4) | ((uint32_t)(128 >> 4) << 24);
-      constexpr uint32_t id_s = kId | ((uint32_t)(R >> 3) << 17);
-      constexpr uint32_t id_o = ta_idesc(R, 1) | (1u << 15);     // both operands with keys along K, as they lie
+      constexpr uint32_t id_s = kId | ((uint32_t)(C >> 3) << 17);
+      constexpr uint32_t id_o = ta_idesc(C, 1) | (1u << 15);     // both operands with keys along K, as they lie
       auto wait = [&](uint64_t* bar, unsigned parity) {
         const bool got = __all_sync(0xffffffffu, ta_wait(bar, parity, &s_abort));
         ta_fence_after();
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
               for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int s = 0; s < HD / 32; ++s)
-                  ta_mma_f8(tmem + (i & 3) * 32, kd + 2 * s, qd + t * (R * HD / 16) + 2 * s, id_s, t + s > 0);
+                  ta_mma_f8(tmem + (i & 3) * 32, kd + 2 * s, qd + t * (C * HD / 16) + 2 * s, id_s, t + s > 0);
               ta_commit(&s_full[i & 3]);
               ta_commit(&k_empty[i % L::ks]);
             }
@@ -463,10 +466,10 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
             if (ta_elect()) {
               // head dim 64: the 128 lanes hold the dims twice
               const uint64_t vd = ta_desc(v_at, HD == 64 ? 0 : (L::vtile / kHalf) >> 4);
-              const uint64_t pd = ta_desc_narrow(base + L::p_at + (i & 1) * L::p, R / 8);
+              const uint64_t pd = ta_desc_narrow(base + L::p_at + (i & 1) * L::p, C / 8);
 #pragma unroll
               for (int ks = 0; ks < kTdKeys / 16; ++ks)
-                ta_mma_ss(tmem + kO, vd + ks * 128, pd + ks * (16 * R * 2 / 16), id_o, j > 0 || ks > 0);
+                ta_mma_ss(tmem + kO, vd + ks * 128, pd + ks * (16 * C * 2 / 16), id_o, j > 0 || ks > 0);
               ta_commit(&pv_done[i & 1]);
               ta_commit(&b_empty[s]);
             }
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         // scores, -inf where a row does not see the key
         auto scores = [&](float* s) {
 #pragma unroll
-          for (int c = 0; c < R; c += 16) ta_ld16(tmem + lanes + (i & 3) * 32 + c, s + c);
+          for (int c = 0; c < R; c += 8) ta_ld8(tmem + lanes + (i & 3) * 32 + c, s + c);
           ta_wait_ld();
           ta_pin<R>(s);
           const uint64_t kk = ta_pair(kf, kf);
@@ -569,15 +572,15 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
           ta_fence_after();
           named_sync(kTdBar, 128);
 #pragma unroll
-          for (int c = 0; c < R; c += 16) {
-            float o[16];
+          for (int c = 0; c < R; c += 8) {
+            float o[8];
             if (j > 0) {
-              ta_ld16(tmem + lanes + kO + c, o);
+              ta_ld8(tmem + lanes + kO + c, o);
               ta_wait_ld();
-              ta_pin<16>(o);
+              ta_pin<8>(o);
             }
 #pragma unroll
-            for (int r = c; r < c + 16; r += 2) {
+            for (int r = c; r < c + 8; r += 2) {
               float n0, n1, t[2];
               ta_split(nm[r / 2], n0, n1);
 #pragma unroll
@@ -590,12 +593,12 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
               o[r - c] *= f0;
               o[r - c + 1] *= f1;
             }
-            if (j > 0) ta_st16(tmem + lanes + kO + c, reinterpret_cast<uint32_t*>(o));
+            if (j > 0) ta_st8(tmem + lanes + kO + c, reinterpret_cast<uint32_t*>(o));
           }
           if (j > 0) ta_wait_st();
           named_sync(kTdBar, 128);              // s_red is read
         }
-        const uint32_t p_at = base + L::p_at + (i & 1) * L::p + tid * R * 2;
+        const uint32_t p_at = base + L::p_at + (i & 1) * L::p + tid * C * 2;
 #pragma unroll
         for (int r = 0; r < R; r += 8) {
           uint32_t v[4];
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
             l2[r / 2 + e] = ta_add2(l2[r / 2 + e], ta_pair(p0, p1));
             v[e] = ta_pack(p0, p1);
           }
-          const int c = r / 8, sw = R == 32 ? c ^ ((tid >> 1) & 3) : c ^ ((tid >> 2) & 1);
+          const int c = r / 8, sw = C == 32 ? c ^ ((tid >> 1) & 3) : c ^ ((tid >> 2) & 1);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                        ::"r"(p_at + (sw << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
         }
@@ -622,14 +625,14 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         ta_fence_after();
         ok = !any(!done || !got);
       }
-      float l[R];
+      float l[C] = {};
 #pragma unroll
       for (int r = 0; r < R; r += 2) ta_split(l2[r / 2], l[r], l[r + 1]);
       // sums over the lanes, halving the rows of a lane at each exchange
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const bool up = lane & o;
-        const int n = R * o / 32;
+        const int n = C * o / 32;
         if (n > 0) {
 #pragma unroll
           for (int r = 0; r < n; ++r) {
@@ -640,18 +643,18 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
           l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
         }
       }
-      s_red[warp][lane / (32 / R)] = l[0];
+      s_red[warp][lane / (32 / C)] = l[0];
       float o[R];
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < R; c += 16) ta_ld16(tmem + lanes + kO + c, o + c);
+        for (int c = 0; c < R; c += 8) ta_ld8(tmem + lanes + kO + c, o + c);
         ta_wait_ld();
         ta_pin<R>(o);
         ta_fence_before();
       }
       named_sync(kTdBar, 128);
       // row r's sum, reference and place on lane r
-      const int lr = lane % R, row = w.row0 + lr, t = row / G, h = w.kvh * G + row - t * G;
+      const int lr = lane % C, row = w.row0 + lr, t = row / G, h = w.kvh * G + row - t * G;
       const int live = last_row + 1 - w.row0;
       const float sum = !ok ? __uint_as_float(0x7fffffffu) : (s_red[0][lr] + s_red[1][lr]) + (s_red[2][lr] + s_red[3][lr]);
       float ref = 0.f;
@@ -778,10 +781,10 @@ cudaError_t launch_td(const TdArgs& ta, cudaStream_t st) {
                      ta.runs);
 }
 
-// Columns of a call's tiles and the rows they hold: even tiles of at most 32.
-int td_cols(int64_t rows) {
+// Rows that a call's tiles are worked on with: even tiles of at most 32.
+int td_rows(int64_t rows) {
   const int64_t tiles = (rows + 31) / 32;
-  return (rows + tiles - 1) / tiles <= 16 ? 16 : 32;
+  return std::max<int>(16, (int)((rows + tiles - 1) / tiles + 7) / 8 * 8);
 }
 
 }  // namespace
@@ -791,22 +794,22 @@ bool pattn_td_supported(const PAttn& a) {
          (int64_t)a.hkv << a.page_shift <= 0x7fffffffLL;
 }
 size_t pattn_td_workspace(int64_t rows, int hd, int num_sms) {
-  return (size_t)num_sms * 2 * td_cols(rows) * (hd + 2) * sizeof(float);
+  return (size_t)num_sms * 2 * td_rows(rows) * (hd + 2) * sizeof(float);
 }
 
 cudaError_t launch_pattn_td(const PAttn& a, int num_sms, cudaStream_t st) {
   TdArgs ta{};
   ta.a = a;
   const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), tiles = (rows + 31) / 32;
-  const int cols = td_cols(rows);
+  const int r = td_rows(rows);
   ta.rows = (int)((rows + tiles - 1) / tiles);
   ta.runs = num_sms;
   const int ps = 1 << a.page_shift, box = std::min(ps, kTdKeys);
   if (!ta_map(ta.km, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, box, 1, 1) ||
       !ta_map(ta.vm, a.v, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, box, 1, 1))
     return cudaErrorInvalidValue;
-  if (a.hd == 128) return cols == 16 ? launch_td<128, 16>(ta, st) : launch_td<128, 32>(ta, st);
-  return cols == 16 ? launch_td<64, 16>(ta, st) : launch_td<64, 32>(ta, st);
+  if (a.hd == 128) return r == 16 ? launch_td<128, 16>(ta, st) : r == 24 ? launch_td<128, 24>(ta, st) : launch_td<128, 32>(ta, st);
+  return r == 16 ? launch_td<64, 16>(ta, st) : r == 24 ? launch_td<64, 24>(ta, st) : launch_td<64, 32>(ta, st);
 }
 
 }  // namespace sv
