@@ -619,22 +619,26 @@ bool row_aligned(const void* p, int64_t ts, int64_t hs) {
 }
 
 // Workspace of launch_pattn_td where it is taken, else 0.  It costs 5 us a tile
-// and 10 us for its start and join, and saves a third of a long context's time:
-// it is taken at head dim 128 for more than 8 rows (a decoded token's few leave
-// the register tiles bound by the copies: 64 x 4096 keys of 4 rows 97 / 115 us),
-// tables of 4096 positions or more and six units of 128 keys an SM; and for any
-// rows where (sequence, KV head, tile) items are so few that the register
-// tiles' clusters of eight blocks do not cover the SMs, from 16384 positions on.
-// The lengths being on the device, a table's width stands for them.  24 rows,
-// register tiles / this, us: 64 sequences x 4096 keys 152 / 126, x 2048 90 / 91,
-// x 512 40 / 54; 16 x 4096 54 / 52; 1 x 16384 46 / 31, 1 x 4096 18 / 25.  Head
-// dim 64: 64 x 4096 105 / 115, 1 x 16384 32 / 28, 1 x 65536 104 / 49.
+// and 10 us for its start and join, and saves up to a third of a long context's
+// time.  It is taken at head dim 128 for more than 16 rows (with pages of 64,
+// whose copies are fewer, more than 8), tables of 2048 positions or more and ten
+// units of 128 keys an SM; and for any rows and dims where (sequence, KV head,
+// tile) items are so few that the register tiles' clusters of eight blocks do
+// not cover the SMs.  The lengths being on the device, a table's width stands for
+// them.  Register tiles / this, us, 8 KV heads.  24 rows, head dim 128: 64
+// sequences x 4096 keys 152 / 116, x 2048 90 / 80, x 1024 56 / 63; 16 x 4096
+// 54 / 43, x 2048 34 / 34; 4 x 8192 33 / 29, x 4096 21 / 24; 1 x 8192 27 / 25,
+// x 4096 18 / 24, x 65536 152 / 52.  16 rows, 64 x 4096: 108 / 111, with pages of
+// 64 109 / 93; 4 rows 97 / 113, 1 x 16384 28 / 25, 2 x 16384 30 / 30.  24 rows,
+// head dim 64: 64 x 4096 105 / 105, 4 x 8192 23 / 26, 1 x 16384 32 / 26.
 size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
   if (!a.paged || rows < 1 || rows > kPaMaxRows || !pattn_td_supported(a)) return 0;
   const int64_t keys = (int64_t)a.max_pages << a.page_shift, items = (int64_t)a.seqs * a.hkv * ((rows + 31) / 32);
   const int64_t units = items * ((keys + 127) / 128);
   if (units > 0x7fffffffLL) return 0;
-  const bool many = a.hd == 128 && rows > 8 && keys >= 4096 && units >= 6LL * sms, few = items * 8 <= sms && keys >= 16384;
+  const bool wide = rows > 16;
+  const bool many = a.hd == 128 && (wide || (rows > 8 && a.page_shift >= 6)) && keys >= 2048 && units >= 10LL * sms;
+  const bool few = items * (wide ? 8 : 16) <= sms && keys >= (wide && a.hd == 128 ? 8192 : 16384);
   return many || few ? pattn_td_workspace(rows, a.hd, sms) : 0;
 }
 

@@ -30,12 +30,12 @@
 // Every wait is for the phase after the last one that the same warp has seen (a
 // wait by parity passes early when a barrier is two phases behind), so the V
 // ring has an even number of stages: each belongs to one of the two groups.
-// Bound by the softmax warps' latencies, 1700 clocks a unit of 32 rows, and
-// 5 us a tile.  Measured (8 KV heads, head dim 128, 24 rows, 8-bit keys) against
-// the register-tile kernel: 64 x 4096 keys 126 / 152 us (3.2 TB/s), 16 x 16384
-// 124 / 169, 16 x 4096 52 / 54, 1 x 16384 31 / 46, 1 x 65536 58 / 152.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+// Bound by the softmax warps' latencies (1500 clocks a unit of 16 rows, 1800 of
+// 24, 2000 of 32; the next unit's scores loaded early cost registers and were 4%
+// slower, two units a pass 40%) and by 5 us at the ends of a tile.  Measured (8 KV
+// heads, head dim 128, 24 rows) against the register-tile kernel: 64 x 4096 keys
+// 116 / 152 us (3.5 TB/s), 16 x 16384 116 / 169, 16 x 4096 43 / 54, 1 x 16384
+// 28 / 46, 1 x 65536 52 / 152.
 #include <cuda_runtime.h>
 
 #include <algorithm>

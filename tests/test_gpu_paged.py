@@ -510,6 +510,9 @@ LONG = [  # few rows per KV head over contexts that fill the GPU: hq, hk, hd, pa
     (32, 8, 128, 16, [3] * 40, [5000, 1, 0, 2] + [97 * b for b in range(36)]),            # more sequences than lanes
     (32, 8, 128, 128, [0, 6, 5, 0], [100, 4097, 8000, 0]),
     (8, 1, 64, 16, [1, 3], [17000, 250]),
+    (32, 8, 128, 16, [6, 5] * 20, [5000, 1, 0, 5] + [97 * b for b in range(36)]),
+    (8, 8, 128, 64, [9, 1, 16], [6000, 3, 9001]),                                         # 16 columns, one head each
+    (32, 8, 128, 16, [6], [8192]),
 ]
 
 
@@ -576,6 +579,31 @@ def test_attn_paged_long_special_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attn_paged_long_bound_and_strides(hd, dtype):
+    """Rows past max_q stay; outputs between other columns, tables and pools with strides of their own, shared pages."""
+    hq, hk, ps, ctx, n = 16, 4, 32, 20000, 8
+    c, q, cu, lens = _paged_case(31, hq, hk, hd, ps, dtype, [n, n], [ctx, 40])
+    table = torch.full((2, c.max_pages + 5), -7, dtype=torch.int32, device="cuda")
+    table[:, :c.max_pages] = c.table[0]                   # both read the first sequence's pages
+    two = sv.KVCache(c.k, c.v, table[:, :c.max_pages], c.k_scale, c.v_scale)
+    wide = torch.full((2 * n, hq, hd + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2 * n, hq), 9.0, device="cuda")
+    lens = _i32([ctx, ctx - 3])
+    sv.attn_paged(q, two, cu, lens, max_q=6, out=wide[..., :hd], lse=lse)
+    assert (wide[..., hd:] == 5.0).all()
+    values = _values(c)
+    for b, m in enumerate([ctx, ctx - 3]):
+        pos = torch.arange(m, device="cuda").int()
+        k, v = _read(c, values, torch.zeros_like(pos), pos)
+        ref = _attend_ref(q[b * n:b * n + n], k, v, n, hd ** -0.5)
+        ref = tuple(x[:6] for x in ref)
+        r = slice(b * n, b * n + 6)
+        _check_rows(wide[r, :, :hd], lse[r], ref, m, hd)
+        assert (wide[b * n + 6:b * n + n] == 5.0).all() and (lse[b * n + 6:b * n + n] == 9.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attn_paged_workspace(dtype):
     """With and without a workspace, and with one too small: right either way, nothing past its end."""
     ns, ctx, (hq, hk, hd) = [4, 3], [9000, 30000], (16, 4, 128)
@@ -605,32 +633,32 @@ def test_attn_paged_workspace(dtype):
     assert torch.equal(out2, out)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-def test_attn_paged_long_overlaps_and_graphs(dtype):
+@pytest.mark.parametrize("dtype,n", [("bf16", 4), ("e4m3", 4), ("e4m3", 6), ("e4m3", 8)])
+def test_attn_paged_long_overlaps_and_graphs(dtype, n):
     """Calls on two streams at once and replayed graphs give the bits of one call alone."""
-    ns, ctx = [4, 4, 4], [9000, 4000, 17000]
+    ns, ctx = [n] * 3, [9000, 4000, 17000]
     c, q, cu, lens = _paged_case(12, 32, 8, 128, 16, dtype, ns, ctx)
     q2 = q.flip(0).contiguous()
-    ref, ref2 = (sv.attn_paged(x, c, cu, lens, max_q=4)[0] for x in (q, q2))
+    ref, ref2 = (sv.attn_paged(x, c, cu, lens, max_q=n)[0] for x in (q, q2))
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     got, got2 = [], []
     for _ in range(4):
         with torch.cuda.stream(a):
-            got.append(sv.attn_paged(q, c, cu, lens, max_q=4)[0])
+            got.append(sv.attn_paged(q, c, cu, lens, max_q=n)[0])
         with torch.cuda.stream(b):
-            got2.append(sv.attn_paged(q2, c, cu, lens, max_q=4)[0])
+            got2.append(sv.attn_paged(q2, c, cu, lens, max_q=n)[0])
     torch.cuda.synchronize()
     assert all(torch.equal(x, ref) for x in got) and all(torch.equal(x, ref2) for x in got2)
     gr, o = torch.cuda.CUDAGraph(), torch.zeros_like(ref)
     with torch.cuda.graph(gr):
-        sv.attn_paged(q, c, cu, lens, max_q=4, out=o)
+        sv.attn_paged(q, c, cu, lens, max_q=n, out=o)
     for new in (ctx, [1, 17000, 4], [0, 0, 0], [17000, 17000, 17000]):
         lens.copy_(_i32(new))
         gr.replay()
         torch.cuda.synchronize()
         # (as bits: the longer lengths reach slots that hold NaN)
-        assert torch.equal(o.view(torch.int16), sv.attn_paged(q, c, cu, lens, max_q=4)[0].view(torch.int16))
+        assert torch.equal(o.view(torch.int16), sv.attn_paged(q, c, cu, lens, max_q=n)[0].view(torch.int16))
 
 
 PROMPT = [  # hq, hk, hd, lengths
