@@ -39,7 +39,7 @@
 // block j of the cluster finishes the rows j, j + C, ...
 // Bound: by the copies for a few rows (64 sequences x 4096 keys of 8 heads of
 // 128, 16-bit, one token each: 128 us, 92% of a copy's rate; 16 x 16384 of 64
-// dims 72 us, 82%), by the latencies of a step's instructions (600 of 16 keys
+// dims 66 us, 90%; 64 x 4096 8-bit of 128 dims 80 us, 75%), by the latencies of a step's instructions (600 of 16 keys
 // and 24 rows, three warps a partition) for more: 24 rows of 64 x 4096 162 us
 // (76%), 8-bit 152 us (40%), which is why long 8-bit contexts go to tensor
 // memory.  One sequence of 512 keys and 24 rows takes 9 us, most of it the
@@ -72,9 +72,13 @@ struct PaLayout {
   static constexpr int tile = kPaStep * row;         // K or V of a step
   static constexpr int stage = 2 * tile + (F8 ? 32 : 0);
   static constexpr int q_bytes = NT * 8 * HD * 2;    // Q in operand order: 16 bytes a lane hold two k slices
-  // blocks on an SM: as many as the accumulators allow (NT = 4: 128 of them)
-  static constexpr int blocks = NT == 4 && HD >= 128 ? 2 : 3;
-  static constexpr int room = (blocks == 2 ? 112 : 74) * 1024 - q_bytes;
+  // Blocks on an SM: as many as the accumulators allow (NT = 4: 128 of them),
+  // more where steps are small and rows few, so that their copies leave room
+  // (64 x 4096 keys of one token, 8-bit head dim 128: 3 blocks 96 us, 4 84, 5 80;
+  // 16-bit head dim 64: 74, 67, 65; 8-bit head dim 64, whose ring is full with 4:
+  // 61, 61, 63).
+  static constexpr int blocks = NT == 4 && HD >= 128 ? 2 : NT > 2 || stage >= 5000 ? 3 : NT == 1 && stage > 3000 ? 5 : 4;
+  static constexpr int room = (blocks == 2 ? 112 : blocks == 3 ? 74 : blocks == 4 ? 55 : 44) * 1024 - q_bytes;
   static constexpr int fit = room / (kPaWarps * stage);
   static constexpr int depth = fit > 6 ? 6 : fit;
   static_assert(depth >= 2, "the ring holds the step in use and the next");
@@ -582,11 +586,16 @@ cudaError_t launch_pa(const PAttn& a, int64_t rows, int tpq, int num_sms, cudaSt
   using L = PaLayout<HD, F8, NT>;
   auto kern = pattn_kernel<HD, F8, NT>;
   const int64_t items = (int64_t)a.seqs * tpq;
-  // blocks of a cluster: until every SM has about one and a half, with at
-  // least 64 keys (four steps a block, one per warp) of the longest context each
+  // Blocks of a cluster: what the GPU holds at once, one wave of equal blocks, with
+  // at least 64 keys (four steps a block, one per warp) of the longest context
+  // each: 1, 2, 3, 4 or 8 (clusters of 7 found room badly: 8 x 8192 keys 49 us
+  // for 40; 3 for 2, 16 x 4096 keys of 24 rows and 64 dims, 27 for 30; a second,
+  // part-filled wave there 36).
   const int64_t max_keys = a.paged ? (int64_t)a.max_pages << a.page_shift : rows / (a.hq / a.hkv);
+  const int64_t room = (int64_t)L::blocks * num_sms / (items * a.hkv);
   int C = 1;
-  while (C < 8 && items * a.hkv * C * 2 < 3LL * num_sms && max_keys >= 128 * C) C *= 2;
+  while (C < 8 && C * 2 <= room && max_keys >= 128 * C) C *= 2;
+  if (C == 2 && room >= 3 && max_keys >= 192) C = 3;
   if (items * C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch_rows_smem(std::integral_constant<int, NT * 1000 + HD * 2 + F8>(), kern, dim3((unsigned)(items * C), a.hkv),
                           dim3(kPaThreads), L::smem, C, st, a, tpq, C);
@@ -620,25 +629,27 @@ bool row_aligned(const void* p, int64_t ts, int64_t hs) {
 
 // Workspace of launch_pattn_td where it is taken, else 0.  It costs 5 us a tile
 // and 10 us for its start and join, and saves up to a third of a long context's
-// time.  It is taken at head dim 128 for more than 16 rows (with pages of 64,
-// whose copies are fewer, more than 8), tables of 2048 positions or more and ten
-// units of 128 keys an SM; and for any rows and dims where (sequence, KV head,
-// tile) items are so few that the register tiles' clusters of eight blocks do
-// not cover the SMs.  The lengths being on the device, a table's width stands for
-// them.  Register tiles / this, us, 8 KV heads.  24 rows, head dim 128: 64
-// sequences x 4096 keys 152 / 116, x 2048 90 / 80, x 1024 56 / 63; 16 x 4096
-// 54 / 43, x 2048 34 / 34; 4 x 8192 33 / 29, x 4096 21 / 24; 1 x 8192 27 / 25,
-// x 4096 18 / 24, x 65536 152 / 52.  16 rows, 64 x 4096: 108 / 111, with pages of
-// 64 109 / 93; 4 rows 97 / 113, 1 x 16384 28 / 25, 2 x 16384 30 / 30.  24 rows,
-// head dim 64: 64 x 4096 105 / 105, 4 x 8192 23 / 26, 1 x 16384 32 / 26.
+// time.  It is taken at head dim 128 for more than 16 rows, tables of 2048
+// positions or more and ten units of 128 keys an SM (20 below 4096 positions),
+// for 9 to 16 with pages of 64, whose copies are fewer, and 50 units; and for any
+// rows and dims where (sequence, KV head, tile) items are so few that the register
+// tiles' clusters of eight blocks do not cover the SMs.  The lengths being on the
+// device, a table's width stands for them.  Register tiles / this, us, 8 KV heads.
+// 24 rows, head dim 128: 64 sequences x 4096 keys 151 / 116, x 2048 90 / 79,
+// x 1024 56 / 63; 16 x 4096 54 / 43, x 2048 31 / 33; 4 x 8192
+// 33 / 30, x 4096 21 / 24; 1 x 8192 27 / 25, x 4096 18 / 24, x 65536 152 / 52.  16
+// rows, 64 x 4096: 103 / 110, with pages of 64 106 / 93, 16 x 4096 36 / 39; 2 x
+// 16384 43 / 30.  4 rows: 64 x 4096 80 / 113, 1 x 16384 28 / 24, 2 x 16384 31 / 30.
+// 24 rows, head dim 64: 64 x 4096 105 / 104, 4 x 8192 23 / 26, 1 x 16384 32 / 26.
 size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
   if (!a.paged || rows < 1 || rows > kPaMaxRows || !pattn_td_supported(a)) return 0;
   const int64_t keys = (int64_t)a.max_pages << a.page_shift, items = (int64_t)a.seqs * a.hkv * ((rows + 31) / 32);
   const int64_t units = items * ((keys + 127) / 128);
   if (units > 0x7fffffffLL) return 0;
   const bool wide = rows > 16;
-  const bool many = a.hd == 128 && (wide || (rows > 8 && a.page_shift >= 6)) && keys >= 2048 && units >= 10LL * sms;
-  const bool few = items * (wide ? 8 : 16) <= sms && keys >= (wide && a.hd == 128 ? 8192 : 16384);
+  const int64_t least = !wide ? 50 : keys >= 4096 ? 10 : 20;
+  const bool many = a.hd == 128 && (wide || (rows > 8 && a.page_shift >= 6)) && keys >= 2048 && units >= least * sms;
+  const bool few = items * (rows > 8 ? 8 : 16) <= sms && keys >= (wide && a.hd == 128 ? 8192 : 16384);
   return many || few ? pattn_td_workspace(rows, a.hd, sms) : 0;
 }
 
