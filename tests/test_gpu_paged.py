@@ -604,6 +604,32 @@ def test_attn_paged_long_bound_and_strides(hd, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_pool_past_32_bit_offsets(dtype):
+    """Pages whose first element lies past 2^32: write, read-back and the attention kernels."""
+    hk, hd, ps, ctx = 8, 128, 16, 10000
+    pages = (1 << 32) // (hk * ps * hd) + ctx // ps + 8
+    c = None
+    table = (pages - 1 - torch.randperm(ctx // ps, generator=_gen(5), device="cuda")).int().view(1, -1).contiguous()
+    kw = dict(device="cuda")
+    if dtype == "e4m3":
+        k, v = (torch.empty(pages, hk, ps, hd, dtype=torch.uint8, **kw).view(torch.float8_e4m3fn) for _ in range(2))
+        c = sv.KVCache(k, v, table, *(torch.empty(pages, hk, ps, dtype=torch.uint8, **kw) for _ in range(2)))
+    else:
+        c = sv.KVCache(*(torch.empty(pages, hk, ps, hd, dtype=torch.bfloat16, **kw) for _ in range(2)), table)
+    g = _gen(6)
+    pos = torch.arange(ctx, device="cuda").int()
+    k, v = _randn(g, ctx, hk, hd).bfloat16(), _randn(g, ctx, hk, hd).bfloat16()
+    sv.kv_append(c, k, v, torch.zeros_like(pos), pos)
+    kk, vv = sv.kv_gather(c, torch.zeros_like(pos), pos, dtype=torch.float32)
+    if dtype == "bf16":
+        assert torch.equal(kk, k.float()) and torch.equal(vv, v.float())
+    for n in (1, 6, 100):
+        q = _randn(g, n, 32, hd).bfloat16()
+        out, lse = sv.attn_paged(q, c, _i32([0, n]), _i32([ctx]), max_q=n)
+        _check_rows(out, lse, _attend_ref(q, kk, vv, n, hd ** -0.5), ctx, hd)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attn_paged_workspace(dtype):
     """With and without a workspace, and with one too small: right either way, nothing past its end."""
     ns, ctx, (hq, hk, hd) = [4, 3], [9000, 30000], (16, 4, 128)
