@@ -513,6 +513,9 @@ LONG = [  # few rows per KV head over contexts that fill the GPU: hq, hk, hd, pa
     (32, 8, 128, 16, [6, 5] * 20, [5000, 1, 0, 5] + [97 * b for b in range(36)]),
     (8, 8, 128, 64, [9, 1, 16], [6000, 3, 9001]),                                         # 16 columns, one head each
     (32, 8, 128, 16, [6], [8192]),
+    (32, 8, 128, 16, [2, 5] * 8, [1500, 0, 193, 64] + [70 * b + 1 for b in range(12)]),  # three blocks a tile
+    (32, 8, 64, 32, [6] * 16, [130 * b for b in range(16)]),
+    (16, 16, 32, 16, [1] * 9, [300 * b + 7 for b in range(9)]),
 ]
 
 
