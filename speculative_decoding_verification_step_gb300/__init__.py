@@ -495,12 +495,24 @@ def _call(dev, stream, fn, *args):
         _check(rc)
 
 
+def _first_stride(name, t):
+    """Elements between t[0] and t[1] as the C structure takes them, where 0
+    stands for packed (of a single entry it is never used)."""
+    if t.shape[0] == 1:
+        return 0
+    if t.stride(0) == 0:
+        _refuse(f"{name}: a first stride of 0 (an expanded tensor); make it contiguous")
+    return t.stride(0)
+
+
 class KVCache:
     """A paged cache over caller-owned CUDA tensors: k, v [pages, n_kv_heads,
     page_size, head_dim] (bf16, or torch.float8_e4m3fn with uint8 k_scale,
     v_scale [pages, n_kv_heads, page_size]; pages may be strided, a page is
-    contiguous) and the page table, int32 [seqs, max_pages].  The tensors are
-    kept and read in place: write the table's rows as sequences grow."""
+    contiguous) and the page table, int32 [seqs, max_pages].  Rows of the table
+    may name the same pages (a shared prefix), but no tensor may be expanded
+    along its first dimension.  The tensors are kept and read in place: write
+    the table's rows as sequences grow."""
 
     def __init__(self, k, v, table, k_scale=None, v_scale=None):
         import torch
@@ -511,12 +523,14 @@ class KVCache:
         pages, heads, ps, hd = k.shape
         for t in (k, v):
             _need(t.stride()[1:] == (ps * hd, hd, 1), "a page must be contiguous")
-        _need(k.stride(0) == v.stride(0), "k and v must have one page stride")
+        stride, table_stride, scale_stride = _first_stride("k", k), _first_stride("table", table), 0
+        _need(stride == _first_stride("v", v), "k and v must have one page stride")
         if f8:
             for t in (k_scale, v_scale):
                 _need(t is not None and t.dtype == torch.uint8 and t.shape == (pages, heads, ps) and
                       t.stride()[1:] == (ps, 1), "an e4m3 cache needs uint8 scales [pages, heads, page]")
-            _need(k_scale.stride(0) == v_scale.stride(0), "the scales must have one page stride")
+            scale_stride = _first_stride("k_scale", k_scale)
+            _need(scale_stride == _first_stride("v_scale", v_scale), "the scales must have one page stride")
         else:
             _need(k_scale is None and v_scale is None, "a bf16 cache has no scales")
         for t in (k, v, table) + ((k_scale, v_scale) if f8 else ()):
@@ -528,8 +542,8 @@ class KVCache:
         self._dev = k.get_device()
         self._c = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if f8 else None,
                               v_scale.data_ptr() if f8 else None, SPEC_DTYPE_E4M3 if f8 else SPEC_DTYPE_BF16,
-                              pages, ps, heads, hd, k.stride(0), k_scale.stride(0) if f8 else 0,
-                              table.data_ptr(), table.stride(0), self.seqs, self.max_pages)
+                              pages, ps, heads, hd, stride, scale_stride, table.data_ptr(), table_stride,
+                              self.seqs, self.max_pages)
         self._ref = ctypes.byref(self._c)
         self._ws = {}                        # workspace bytes of attn_paged calls by their sizes
 

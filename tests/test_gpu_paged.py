@@ -792,3 +792,23 @@ def test_decode_loop(dtype, hd, ps):
             out, lse = sv.attn_prompt(q, k16, vv.bfloat16(), cu)
             for r, c in ((slice(0, chunk[0]), chunk[0]), (slice(chunk[0], n), chunk[1])):
                 _check_rows(out[r], lse[r], _attend_ref(q[r], k16[r], vv[r], c, hd ** -0.5), c, hd)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_cache_of_one_page_and_one_sequence(dtype):
+    """Strides of dimensions of one entry mean nothing: expanded and sliced ones are as good as packed."""
+    g = _gen(41)
+    hq, hk, hd, n = 8, 2, 64, 11
+    c, q, cu, lens = _paged_case(41, hq, hk, hd, 16, dtype, [n], [n])
+    page = int(c.table[0, 0])
+    one = lambda t: None if t is None else t[page:page + 1].expand(1, *t.shape[1:])
+    odd = lambda t: None if t is None else one(t).as_strided(t[:1].shape, (3,) + t.stride()[1:], t.stride(0) * page)
+    zero = _i32([0])
+    for f in (one, odd):
+        for table in (zero.expand(1, 1), zero.as_strided((1, 1), (7, 1))):
+            alone = sv.KVCache(f(c.k), f(c.v), table, f(c.k_scale), f(c.v_scale))
+            _paged_check(alone, q, cu, lens, [n], [n])
+    # rows of a table that is wider than what it is used for
+    both = torch.stack([c.table[0], c.table[0] * 0 - 1]).repeat_interleave(2, 0)
+    for rows in (both[:1], both[::2][:1]):
+        _paged_check(sv.KVCache(c.k, c.v, rows, c.k_scale, c.v_scale), q, cu, lens, [n], [n])

@@ -146,3 +146,19 @@ def test_binding_refusals(L):
             sv.KVCache(bad["k"], bad["v"], table, bad.get("k_scale"))
     with pytest.raises(sv.SpecError):
         sv.KVCache(k, k, table.long())
+
+
+def test_expanded_cache_refusals(L):
+    """In the C structure a stride of 0 means packed: a tensor expanded along its first
+    dimension would be read past its end, so it is refused."""
+    page = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)
+    codes, scale = page.to(torch.float8_e4m3fn), torch.zeros(1, 2, 16, dtype=torch.uint8)
+    pool, pool8, scales = (x.repeat(4, *[1] * (x.dim() - 1)) for x in (page, codes.view(torch.uint8), scale))
+    pool8 = pool8.view(torch.float8_e4m3fn)
+    row, table = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(3, 4, dtype=torch.int32)
+    wide = lambda x, n=4: x.expand(n, *x.shape[1:])
+    for args in ((pool, pool, wide(row, 3)), (wide(page), wide(page), table), (pool, wide(page), table),
+                 (pool8, pool8, table, wide(scale), wide(scale)), (pool8, pool8, table, scales, wide(scale)),
+                 (wide(codes), wide(codes), table, scales, scales)):
+        with pytest.raises(sv.SpecError, match="first stride of 0"):
+            sv.KVCache(*args)
