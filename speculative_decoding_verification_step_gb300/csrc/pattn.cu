@@ -24,15 +24,17 @@
 //   Probabilities are rounded to bf16 for P V (half a step, 2^-9 of each on
 //   average, of random sign: the size of the output's own rounding); the row
 //   sum keeps them in fp32.
-// 8-bit keys and values become f16, which holds every code exactly, two codes
-// an instruction (the bit moves that make a bf16 of a code cost two and a half
+// 8-bit keys become f16, which holds every code exactly, two codes an
+// instruction (the bit moves that make a bf16 of a code cost two and a half
 // times as much, measured, and an e4m3 mma.sync is itself emulated here: 37
 // clocks of an SM partition against 8).  Q rows are f16 too, scaled by a power
 // of two to just below 2^15: exact down to 2^-29 of the row's largest.  The
-// rows' powers of two meet the scores in fp32.  V's meet the probabilities
-// before their rounding to f16, against a reference exponent that keeps
-// usual products around 2^4 p and moves when one would pass 2^15, so that
-// neither large nor small rows leave f16's range.
+// rows' powers of two meet the scores in fp32.  Values go on from f16 to bf16,
+// also exact, and their powers of two meet the probabilities before the rounding
+// to bf16: its range holds p * 2^e of every row at once, whatever other rows and
+// queries of the tile need.  (Products in f16 against a shared reference exponent
+// lost small rows beside large ones; they took 4% less time at 4 rows of 64 dims,
+// 7% less at 12 rows and 2% more at 24.)
 // The share of the keys: a cluster of up to 8 blocks splits one tile's keys
 // and merges through distributed shared memory in a fixed order (no scratch
 // memory, no second launch, no atomics): blocks merge their four warps, then
@@ -62,7 +64,6 @@ constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaStep = 16;          // keys of a step
 constexpr float kPaLazy = 8.f;       // exponent reference moves past 2^8
-constexpr int kPaVAt = 4;            // 8-bit values: exponent of a usual product with p = 1
 constexpr float kPaNone = -1e30f;    // reference of a row that has seen nothing
 
 template <int HD, bool F8, int NT>
@@ -130,13 +131,14 @@ SV_DEV float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-SV_DEV uint32_t pa_pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 SV_DEV uint32_t pa_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// An f16 pair as a bf16 pair (exact for what codes become).
+SV_DEV uint32_t f16_to_bf16(uint32_t h) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pa_pack(v.x, v.y);
 }
 // 2^(byte - 127), NaN for 255.
 SV_DEV float f8_scale(uint32_t b) { return __uint_as_float(b == 255u ? 0x7fffffffu : b << 23); }
@@ -326,8 +328,6 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
 
   const int lr = lane & 7, l8 = (lane >> 3) & 1, l16 = lane >> 4;
   const uint4* qs = reinterpret_cast<const uint4*>(sm) + lane;
-  int vref = 0;                               // 8-bit values: O holds its sums over 2^vref
-  bool fresh = true;
   for (int j = 0; j < nj; ++j) {
     cp_async_wait<2 * D - 1>();
     __syncwarp();
@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
         pa_mma<F8>(s[nt], ka[1], w.z, w.w);
       }
     }
-    int ve[2] = {0, 0};
     bool move = false;
     if constexpr (F8) {
       const unsigned char* sc = ring + (j % D) * L::stage + 2 * L::tile;
@@ -420,40 +419,7 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
     uint32_t pb[NT][2];
     if constexpr (F8) {
       const unsigned char* sc = ring + (j % D) * L::stage + 2 * L::tile + 16;
-      ve[0] = sc[g];
-      ve[1] = sc[g + 8];
-      // p <= 2^8: products stay within 2^15 while the rows' exponents are at most 7 above vref;
-      // beyond, the products themselves decide
-      const bool high = fresh || max(ve[0], ve[1]) - 127 - vref > 7;
-      if (__any_sync(0xffffffffu, high)) {
-        int top = -1000;                      // exponent of the largest product over this step
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (x[nt][e] > 0.f && ve[e >> 1] != 255) top = max(top, (int)(__float_as_uint(x[nt][e]) >> 23) - 127 + ve[e >> 1] - 127);
-#pragma unroll
-        for (int of = 16; of > 0; of >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, of));
-        if (top > -1000 && (fresh || top - vref > 14)) {
-          const int to = top - kPaVAt;        // the largest product lands at 2^kPaVAt
-          const float f = fresh ? 0.f : exp2_fast((float)max(vref - to, -126));
-          if (!fresh) {
-#pragma unroll
-            for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f;
-          }
-          vref = to;
-          fresh = false;
-        }
-      }
-      // 2^(exponent - vref); a NaN row stays NaN
-      float vs[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        vs[e] = __uint_as_float(ve[e] == 255 ? 0x7fffffffu : (uint32_t)min(max(ve[e] - vref, 1), 254) << 23);
+      const float vs[2] = {f8_scale(sc[g]), f8_scale(sc[g + 8])};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float p[4];
@@ -464,8 +430,8 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
           for (int e = 0; e < 4; ++e)
             if (x[nt][e] == 0.f) p[e] = 0.f;
         }
-        pb[nt][0] = transpose8(pa_pack_f16(p[0], p[1]));
-        pb[nt][1] = transpose8(pa_pack_f16(p[2], p[3]));
+        pb[nt][0] = transpose8(pa_pack(p[0], p[1]));
+        pb[nt][1] = transpose8(pa_pack(p[2], p[3]));
       }
 #pragma unroll
       for (int c = 0; c < kMt; c += 2) {      // chunks of 16 dims: row g is dim 2 g, row g + 8 dim 2 g + 1
@@ -477,7 +443,9 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
           f8_to_f16(__byte_perm(w[2 * h], 0, 0x3120), va[0], va[1]);
           f8_to_f16(__byte_perm(w[2 * h + 1], 0, 0x3120), va[2], va[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) pa_mma<true>(o[c + h][nt], va, pb[nt][0], pb[nt][1]);
+          for (int i = 0; i < 4; ++i) va[i] = f16_to_bf16(va[i]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) pa_mma<false>(o[c + h][nt], va, pb[nt][0], pb[nt][1]);
         }
       }
     } else {
@@ -502,7 +470,6 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
 
   // ---- merge of the four warps: [warp][row][ld] ----
   float* part = reinterpret_cast<float*>(sm + L::q_bytes);
-  const float vf = F8 ? exp2f((float)vref) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,7 +487,7 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
         if constexpr (F8) {
-          *reinterpret_cast<float2*>(d + mt * 16 + 2 * g) = make_float2(o[mt][nt][e] * vf, o[mt][nt][e + 2] * vf);
+          *reinterpret_cast<float2*>(d + mt * 16 + 2 * g) = make_float2(o[mt][nt][e], o[mt][nt][e + 2]);
         } else {
           d[mt * 16 + g] = o[mt][nt][e];
           d[mt * 16 + g + 8] = o[mt][nt][e + 2];

@@ -812,3 +812,44 @@ def test_cache_of_one_page_and_one_sequence(dtype):
     both = torch.stack([c.table[0], c.table[0] * 0 - 1]).repeat_interleave(2, 0)
     for rows in (both[:1], both[::2][:1]):
         _paged_check(sv.KVCache(c.k, c.v, rows, c.k_scale, c.v_scale), q, cu, lens, [n], [n])
+
+
+# --------------------------------------- 8-bit rows of very different sizes
+def _filled(g, k, v, ps):
+    """An e4m3 cache of one sequence's rows k, v [keys, heads, dim], and what it holds of them."""
+    n, hk, hd = k.shape
+    c = _cache(g, 1, n, hk, ps, hd, "e4m3")
+    pos = torch.arange(n, device="cuda").int()
+    sv.kv_append(c, k, v, torch.zeros_like(pos), pos)
+    return c, *_read(c, _values(c), torch.zeros_like(pos), pos)
+
+
+SPREADS = {  # exponents of the value rows, [keys]
+    "early": lambda g, n, s: torch.where(torch.arange(n, device="cuda") < 20, s, 0),
+    "late": lambda g, n, s: torch.where(torch.arange(n, device="cuda") > n - 20, s, 0),
+    "down": lambda g, n, s: (s * (1 - torch.arange(n, device="cuda") / n)).int() - s // 2,
+    "mixed": lambda g, n, s: torch.randint(-(s // 2), s // 2 + 1, (n,), generator=g, device="cuda"),
+    "zeros": lambda g, n, s: torch.full((n,), -s, device="cuda"),
+}
+
+
+@pytest.mark.parametrize("s", [6, 12, 20, 30, 45, 60, 100])
+@pytest.mark.parametrize("kind", list(SPREADS))
+@pytest.mark.parametrize("hq,hk,hd,n", [(4, 4, 32, 1), (8, 2, 64, 4), (8, 2, 128, 1), (16, 4, 128, 6), (4, 1, 128, 8),
+                                        (8, 1, 128, 20)])
+def test_attn_paged_value_scales(hq, hk, hd, n, kind, s):
+    """Value rows 2^s apart under scores so sharp that every query row rests on a few keys of its own:
+    the small rows count for some queries as much as the large ones do for others."""
+    if kind == "zeros" and s > 50 or kind in ("early", "late") and s > 60:
+        pytest.skip("past the exponents that a write keeps")
+    g = _gen(s + hd + n)
+    ctx = 333
+    k, v = _randn(g, ctx, hk, hd) * 6.0, _randn(g, ctx, hk, hd)
+    v = v * torch.pow(2.0, SPREADS[kind](g, ctx, s).float()).view(-1, 1, 1)
+    if kind == "zeros":
+        v[torch.rand(ctx, generator=g, device="cuda") < 0.3] = 0     # stored with exponent 0
+    c, kk, vv = _filled(g, k, v, 16)
+    q = _randn(g, n, hq, hd).bfloat16()
+    out, lse = sv.attn_paged(q, c, _i32([0, n]), _i32([ctx]), max_q=n)
+    ref = _attend_ref(q, kk, vv, n, hd ** -0.5)
+    _check_rows(out, lse, ref, ctx, hd)
