@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -158,12 +159,20 @@ template <int N>
 SV_DEV void ta_regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 SV_DEV void ta_regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// Two codes in the lower bytes of each half's upper byte -> bf16 pair times
-// two powers of two (2^100 and 2^(20 + e)): code * 2^e, exact.
-SV_DEV uint32_t ta_code_pair(uint32_t x, __nv_bfloat162 up, __nv_bfloat162 scale) {
-  uint32_t b = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);   // code * 2^-120
-  __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), up), scale);
-  return *reinterpret_cast<uint32_t*>(&v);
+// Four codes times a pair of equal powers of two as bf16 pairs: exact where bf16
+// holds the value; a NaN code is NaN.
+SV_DEV void ta_codes(uint32_t w, uint64_t scale, uint32_t& lo, uint32_t& hi) {
+  uint32_t h[2];
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(h[0]), "=r"(h[1]) : "r"(w));
+  uint32_t* const out[2] = {&lo, &hi};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    float x, y;
+    ta_split(ta_mul2(ta_pair(v.x, v.y), scale), x, y);
+    *out[i] = ta_pack(x, y);
+  }
 }
 
 [[maybe_unused]] PFN_cuTensorMapEncodeTiled_v12000 ta_encoder() {

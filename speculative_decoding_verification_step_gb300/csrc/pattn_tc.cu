@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       // ---- 8-bit rows to bf16: thread = key row ----
       ta_regs_less<88>();
       const int r = threadIdx.x - 384;
-      const __nv_bfloat162 up = __floats2bfloat162_rn(1.2676506002282294e30f, 1.2676506002282294e30f);   // 2^100
       int i = 0;                               // tile: K and V of the steps of all items in turn
       bool ok = true;
       TaItem it;
@@ -281,10 +280,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           if (!ok) break;
           const uint32_t code = s_scale[rs][r];
           const bool live = (it.beg + j / 2) * kTaKeys + r < it.keys;
-          // 2^(20 + e) with e = code - 127, a NaN row NaN, a row past the length zero
-          const uint32_t sb = !live ? 0u : code == 255u ? 0x7fffu : (min(max(code + 20u, 1u), 254u) << 7);
-          const uint32_t s2 = sb | (sb << 16);
-          const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+          // 2^(byte - 127), a NaN row NaN, a row past the length zero whatever it holds
+          const float f = !live ? 0.f : __uint_as_float(code == 255u ? 0x7fffffffu : code << 23);
+          const uint64_t scale = ta_pair(f, f);
           const uint32_t src = raw_at + rs * L::raw + r * HD, dst = kv_at + s * kTile + r * 128;
 #pragma unroll
           for (int c = 0; c < HD / 16; ++c) {
@@ -293,19 +291,13 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src + (sw << 4)) : "memory");
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              o[2 * k] = ta_code_pair(__byte_perm(w[k], 0, 0x1404), up, scale);
-              o[2 * k + 1] = ta_code_pair(__byte_perm(w[k], 0, 0x3424), up, scale);
-            }
+            for (int k = 0; k < 4; ++k) ta_codes(live ? w[k] : 0u, scale, o[2 * k], o[2 * k + 1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int cc = 2 * c + h, col = cc & 7;
-              uint32_t v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = live ? o[4 * h + k] : 0u;
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                           ::"r"(dst + (cc >> 3) * (kTile / kHalf) + ((col ^ (r & 7)) << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                           : "memory");
+                           ::"r"(dst + (cc >> 3) * (kTile / kHalf) + ((col ^ (r & 7)) << 4)), "r"(o[4 * h]), "r"(o[4 * h + 1]),
+                             "r"(o[4 * h + 2]), "r"(o[4 * h + 3]) : "memory");
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // ---- V's codes to bf16 (thread = key row), and Q ----
     const int r = threadIdx.x & 127, s = (warp - 8) >> 2;   // a group of warps takes every other unit
-    const __nv_bfloat162 up = __floats2bfloat162_rn(1.2676506002282294e30f, 1.2676506002282294e30f);   // 2^100
     int i = 0, last = -1;                    // units of all parts, the last of this group
     bool ok = true;
     TdPart w = td_first(a, ta.rows, u_beg, u_end);
@@ -337,22 +336,23 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&v_empty[rs]);
         if (i >= 2) ok = __all_sync(0xffffffffu, ta_wait(&b_empty[s], (unsigned)((i / 2 - 1) & 1), &s_abort));
         if (!ok) break;
-        // 2^(20 + e) with e = code - 127, a NaN row NaN, a row past the length
-        // zero whatever its codes are (none of the 256 is a bf16 infinity or NaN)
-        const uint32_t sb = (w.off + j) * kTdKeys + r >= w.keys ? 0u
-                            : code == 255u ? 0x7fffu : (min(max(code + 20u, 1u), 254u) << 7);
-        const uint32_t s2 = sb | (sb << 16);
-        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+        // 2^(byte - 127), a NaN row NaN, a row past the length zero whatever it holds
+        const bool dead = (w.off + j) * kTdKeys + r >= w.keys;
+        if (__any_sync(0xffffffffu, dead)) {
+#pragma unroll
+          for (int c = 0; c < HD / 16; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[c][k] = dead ? 0u : x[c][k];
+        }
+        const float f = dead ? 0.f : __uint_as_float(code == 255u ? 0x7fffffffu : code << 23);
+        const uint64_t scale = ta_pair(f, f);
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              o[2 * k] = ta_code_pair(__byte_perm(x[c][2 * h + k], 0, 0x1404), up, scale);
-              o[2 * k + 1] = ta_code_pair(__byte_perm(x[c][2 * h + k], 0, 0x3424), up, scale);
-            }
+            for (int k = 0; k < 2; ++k) ta_codes(x[c][2 * h + k], scale, o[2 * k], o[2 * k + 1]);
             const int cc = 2 * c + h, col = cc & 7;
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                          ::"r"(dst + (cc >> 3) * (L::vtile / kHalf) + ((col ^ (r & 7)) << 4)), "r"(o[0]), "r"(o[1]),

@@ -853,3 +853,49 @@ def test_attn_paged_value_scales(hq, hk, hd, n, kind, s):
     out, lse = sv.attn_paged(q, c, _i32([0, n]), _i32([ctx]), max_q=n)
     ref = _attend_ref(q, kk, vv, n, hd ** -0.5)
     _check_rows(out, lse, ref, ctx, hd)
+
+
+KERNELS = {  # one call for each way the attention is computed: new tokens, context, whether a workspace is wanted
+    "few rows": (4, 300, False), "few rows of a long context": (4, 20000, True), "many rows": (100, 700, False),
+}
+
+
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("kernel", list(KERNELS))
+def test_nan_codes(kernel, hd, code):
+    """A code that is no number (a cast of a caller's own puts it where a value overflows) reads as NaN
+    everywhere: in K it takes the rows that see it, in V its column."""
+    n, ctx, ws = KERNELS[kernel]
+    hq, hk, ps = 8, 2, 16
+    c, q, cu, lens = _paged_case(hd + n, hq, hk, hd, ps, "e4m3", [n], [ctx])
+    assert (sv.lib().spec_attn_paged_workspace(c._ref, n, n, hq) > 0) == ws
+    clean, clse = sv.attn_paged(q, c, cu, lens)
+    at = lambda t, key, h, d: t.view(torch.uint8)[c.table[0, key // ps].long(), h, key % ps, d:d + 1]
+    one = lambda key: (_i32([0]), _i32([key]))
+    keep = at(c.v, 5, 1, 3).clone()
+    at(c.v, 5, 1, 3).fill_(code)
+    out, lse = sv.attn_paged(q, c, cu, lens)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[:, hq // 2:, 3] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad]) and torch.equal(lse, clse)
+    for dt in (torch.bfloat16, torch.float32):
+        k, v = sv.kv_gather(c, *one(5), dtype=dt)
+        assert torch.isnan(v[0, 1, 3]) and int(torch.isnan(v).sum()) == 1 and not torch.isnan(k).any()
+    at(c.v, 5, 1, 3).copy_(keep)
+    for key, first in ((7, 0), (ctx - 1, n - 1), (ctx - 2, n - 2)):
+        keep = at(c.k, key, 0, hd - 1).clone()
+        at(c.k, key, 0, hd - 1).fill_(code)
+        out, lse = sv.attn_paged(q, c, cu, lens)
+        bad = torch.zeros_like(lse, dtype=torch.bool)
+        bad[first:, :hq // 2] = True
+        assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+        assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clse[~bad])
+        at(c.k, key, 0, hd - 1).copy_(keep)
+    # slots past the length may hold such codes and scales of any kind
+    page, slot = c.table[0, ctx // ps if ctx % ps else 0].long(), slice(ctx % ps or ps, ps)
+    for t, s in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        t.view(torch.uint8)[page, :, slot] = code
+        s[page, :, slot] = 254
+    out, lse = sv.attn_paged(q, c, cu, lens)
+    assert torch.equal(out, clean) and torch.equal(lse, clse)
