@@ -332,7 +332,8 @@ SPEC_API int spec_sample_rows(const float* logits, int64_t row_stride, int rows,
  * [pages][2]...).  SPEC_DTYPE_E4M3 adds k_scale and v_scale,
  * [pages][n_kv_heads][page_size] bytes (scale_page_stride bytes between
  * pages, 0: packed): value = code * 2^(byte - 127), and byte 255 marks a row
- * of NaN.  Position p of sequence s is slot p mod page_size of page
+ * of NaN, as a NaN code does an element (spec_kv_append writes bytes 67..187 or
+ * 255 and no NaN codes; rows that a caller fills may hold any).  Position p of sequence s is slot p mod page_size of page
  * table[s * table_stride + p / page_size] (device int32 [seqs][max_pages];
  * table_stride 0: max_pages).
  * Checked: dtype; head_dim 32, 64 or 128; page_size a power of two in
@@ -415,7 +416,8 @@ SPEC_API int spec_kv_append(const spec_kv_cache* cache, const void* k, int64_t k
 
 /* Read rows back: position pos[t] of sequence seq[t] to k_out and v_out (fp32
  * or bf16 [tokens][n_kv_heads][head_dim], packed; either may be NULL).  The
- * value of an e4m3 row is exact in both.  A row outside the table or the pool
+ * value of an e4m3 row is exact in both (past a type's largest number infinite,
+ * rounded below bf16's normal ones).  A row outside the table or the pool
  * (as for spec_kv_append) reads as zeros. */
 SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, const int32_t* pos, int tokens,
                    void* k_out, void* v_out, int out_dtype, void* stream);
@@ -433,7 +435,8 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * the grid), are left as they were.  A length past the table's positions is cut
  * there; a table entry that is not a page of the pool reads as zero rows.
  * scale >= 0; 0: 1/sqrt(head_dim).  Scores, softmax statistics and sums are fp32,
- * probabilities bf16 in the product with v; over an e4m3 cache elements of q
+ * probabilities bf16 in the product with v; over an e4m3 cache, whose rows' powers of two should lie within 2^+-90 (the
+ * products of others may leave fp32's or bf16's normal range), elements of q
  * below 2^-10 of their row's largest may be rounded by up to 2^-17 of that.
  * Cache slots past a sequence's length are never used, whatever they hold; a
  * value row that is not finite within the length reaches the outputs of the

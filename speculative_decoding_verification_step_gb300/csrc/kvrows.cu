@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const __grid_consta
         __stcs(reinterpret_cast<float4*>(d) + 1, make_float4(bf16lo(x.z), bf16hi(x.z), bf16lo(x.w), bf16hi(x.w)));
       }
     } else {
-      const float f = __uint_as_float(sb == 255u ? 0x7fffffffu : sb << 23);   // 2^(byte - 127), or NaN
+      const float f = row_power(sb);
       const uint32_t in[4] = {x.x, x.y, x.z, x.w};
       float y[16];
 #pragma unroll

@@ -140,8 +140,6 @@ SV_DEV uint32_t f16_to_bf16(uint32_t h) {
   const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pa_pack(v.x, v.y);
 }
-// 2^(byte - 127), NaN for 255.
-SV_DEV float f8_scale(uint32_t b) { return __uint_as_float(b == 255u ? 0x7fffffffu : b << 23); }
 
 SV_DEV void cluster_arrive_wait() {
   __syncwarp();
@@ -361,7 +359,7 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
     bool move = false;
     if constexpr (F8) {
       const unsigned char* sc = ring + (j % D) * L::stage + 2 * L::tile;
-      const float k0 = f8_scale(sc[g]), k1 = f8_scale(sc[g + 8]);
+      const float k0 = row_power(sc[g]), k1 = row_power(sc[g + 8]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -419,7 +417,7 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
     uint32_t pb[NT][2];
     if constexpr (F8) {
       const unsigned char* sc = ring + (j % D) * L::stage + 2 * L::tile + 16;
-      const float vs[2] = {f8_scale(sc[g]), f8_scale(sc[g + 8])};
+      const float vs[2] = {row_power(sc[g]), row_power(sc[g + 8])};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float p[4];

@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           if (!ok) break;
           const uint32_t code = s_scale[rs][r];
           const bool live = (it.beg + j / 2) * kTaKeys + r < it.keys;
-          // 2^(byte - 127), a NaN row NaN, a row past the length zero whatever it holds
-          const float f = !live ? 0.f : __uint_as_float(code == 255u ? 0x7fffffffu : code << 23);
+          // a row past the length is zero whatever it holds
+          const float f = !live ? 0.f : row_power(code);
           const uint64_t scale = ta_pair(f, f);
           const uint32_t src = raw_at + rs * L::raw + r * HD, dst = kv_at + s * kTile + r * 128;
 #pragma unroll

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&v_empty[rs]);
         if (i >= 2) ok = __all_sync(0xffffffffu, ta_wait(&b_empty[s], (unsigned)((i / 2 - 1) & 1), &s_abort));
         if (!ok) break;
-        // 2^(byte - 127), a NaN row NaN, a row past the length zero whatever it holds
+        // a row past the length is zero whatever it holds
         const bool dead = (w.off + j) * kTdKeys + r >= w.keys;
         if (__any_sync(0xffffffffu, dead)) {
 #pragma unroll
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[c][k] = dead ? 0u : x[c][k];
         }
-        const float f = dead ? 0.f : __uint_as_float(code == 255u ? 0x7fffffffu : code << 23);
+        const float f = dead ? 0.f : row_power(code);
         const uint64_t scale = ta_pair(f, f);
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c)
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         got = __all_sync(0xffffffffu, got && ta_wait(&s_full[i & 3], (unsigned)((i / 4) & 1), &s_abort));
         ta_fence_after();
         const uint32_t code = s_ks[i % kSc][tid];
-        const float kf = __uint_as_float(code == 255u ? 0x7fffffffu : code << 23);
+        const float kf = row_power(code);
         // scores, -inf where a row does not see the key
         auto scores = [&](float* s) {
 #pragma unroll

@@ -899,3 +899,47 @@ def test_nan_codes(kernel, hd, code):
         s[page, :, slot] = 254
     out, lse = sv.attn_paged(q, c, cu, lens)
     assert torch.equal(out, clean) and torch.equal(lse, clse)
+
+
+def test_gather_every_scale():
+    """value = code * 2^(byte - 127) for every byte and code, rounded once."""
+    hd = 64
+    codes = torch.arange(256, device="cuda", dtype=torch.uint8).view(1, 4, 1, hd).expand(16, 4, 16, hd).contiguous()
+    scale = torch.arange(256, device="cuda", dtype=torch.uint8).view(16, 1, 16).expand(16, 4, 16).contiguous()
+    table = torch.arange(16, device="cuda").int().view(1, 16)
+    f8 = codes.view(torch.float8_e4m3fn)
+    c = sv.KVCache(f8, f8, table, scale, scale)
+    pos = torch.arange(256, device="cuda").int()
+    power = torch.tensor([2.0 ** (b - 127) for b in range(255)] + [math.nan], dtype=F64, device="cuda")
+    want = power.view(256, 1, 1) * f8[0, :, 0].to(F64)
+    for dt in (torch.float32, torch.bfloat16):
+        ref = want.float().to(dt)                      # (exact in fp32 down to its smallest steps)
+        for x in sv.kv_gather(c, torch.zeros_like(pos), pos, dtype=dt):
+            assert torch.equal(torch.isnan(x), torch.isnan(ref)) and torch.equal(x[~x.isnan()], ref[~ref.isnan()])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("kernel", list(KERNELS))
+def test_attn_paged_every_scale(kernel, hd):
+    """Powers of two that no write of the cache's own gives: the same scores and, but for the power, the
+    same outputs as without."""
+    n, ctx, ws = KERNELS[kernel]
+    hq, hk, ps = 8, 2, 16
+    c, q, cu, lens = _paged_case(hd + n, hq, hk, hd, ps, "e4m3", [n], [ctx])
+    assert (sv.lib().spec_attn_paged_workspace(c._ref, n, n, hq) > 0) == ws
+    g = _gen(hd)
+    live = c.k_scale != 255
+    for t in (c.k, c.v):           # codes of 1/64 to 1, which every power keeps within bf16
+        t.copy_(torch.where(live.unsqueeze(-1), (torch.randint(1, 65, t.shape, generator=g, device="cuda") / 64.0)
+                            * torch.randint(0, 2, t.shape, generator=g, device="cuda").mul(2).sub(1), math.nan))
+    for kb, vb in ((127, 127), (0, 127), (1, 120), (37, 37), (60, 217), (217, 60), (127, 235), (217, 236), (127, 110)):
+        c.k_scale.copy_(torch.where(live, kb, 255))
+        c.v_scale.copy_(torch.where(live, vb, 255))
+        scale = 2.0 ** (127 - kb) * hd ** -0.5
+        out, lse = sv.attn_paged(q, c, cu, lens, scale=scale)
+        pos = torch.arange(ctx, device="cuda").int()
+        c.k_scale.copy_(torch.where(live, 127, 255))
+        c.v_scale.copy_(torch.where(live, 127, 255))
+        k, v = _read(c, _values(c), torch.zeros_like(pos), pos)
+        out = out.to(F64) * 2.0 ** (127 - vb)
+        _check_rows(out, lse, _attend_ref(q, k, v, n, hd ** -0.5), ctx, hd)
