@@ -435,9 +435,12 @@ def sample_rows(logits, temperature, seed, step_base=0, position=1, stream=None,
 
 # ---- paged-cache operators (see include/specverify.h) ----
 # The calls run on the current stream of the tensors' device (or the raw
-# stream given), with that device current; tensors are read by pointer.  A
-# step makes a call per layer and waits for none, so the checks are plain
-# comparisons, and messages are made only where one fails.
+# stream given), with that device current; tensors are read by pointer.  What a
+# call allocates, results and workspace, belongs to the stream it runs on: with
+# `stream` given, a result that is used or dropped on another stream needs that
+# stream to wait, and record_stream.  A step makes a call per layer and waits
+# for none, so the checks are plain comparisons, and messages are made only
+# where one fails.
 _t = None
 
 
@@ -480,6 +483,15 @@ def _rows3(name, t):
 def _index(name, t, n, dev):
     if t.dtype is not _t.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
         _refuse(f"{name}: a contiguous int32 tensor of {n} on the rows' device")
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor from the memory of the stream that the call runs on: the current
+    stream's may still be in use by work queued there."""
+    if stream is None:
+        return _t.empty(shape, dtype=dtype, device=device)
+    with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=device)):
+        return _t.empty(shape, dtype=dtype, device=device)
 
 
 def _call(dev, stream, fn, *args):
@@ -585,7 +597,7 @@ def rope_rows(x, pos, plan, out=None, dtype=None, inverse=False, stream=None):
     dev = x.get_device()
     _index("pos", pos, n, dev)
     if out is None:
-        out = _t.empty(shape, dtype=x.dtype if dtype is None else dtype, device=x.device)
+        out = _empty(shape, x.dtype if dtype is None else dtype, x.device, stream)
         ys = out.stride()
     else:
         if out.shape != shape or out.get_device() != dev or (dtype is not None and dtype is not out.dtype):
@@ -624,22 +636,21 @@ def kv_gather(cache, seq, pos, dtype=None, stream=None):
     shape = (n, cache.n_kv_heads, cache.head_dim)
     if dtype is None:
         dtype = _t.bfloat16
-    k = _t.empty(shape, dtype=dtype, device=cache.device)
-    v = _t.empty(shape, dtype=dtype, device=cache.device)
+    k, v = (_empty(shape, dtype, cache.device, stream) for _ in range(2))
     _call(dev, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
           v.data_ptr(), _io_dtype(k))
     return k, v
 
 
-def _attn_out(q, shape, dev, out, lse):
+def _attn_out(q, shape, dev, out, lse, stream):
     if q.dtype is not _t.bfloat16:
         _refuse(f"q is bf16, not {q.dtype}")
     if out is None:
-        out = _t.empty(shape, dtype=_t.bfloat16, device=q.device)
+        out = _empty(shape, _t.bfloat16, q.device, stream)
     elif out.shape != shape or out.dtype is not _t.bfloat16 or out.get_device() != dev:
         _refuse("out: like q")
     if lse is None:
-        lse = _t.empty(shape[:2], dtype=_t.float32, device=q.device)
+        lse = _empty(shape[:2], _t.float32, q.device, stream)
     elif lse is not False and (lse.shape != shape[:2] or lse.dtype is not _t.float32 or lse.get_device() != dev or
                                not lse.is_contiguous()):
         _refuse("lse: contiguous fp32 [tokens, heads]")
@@ -661,7 +672,7 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
         _refuse("q must have the cache's head_dim and device")
     _index("cu_q", cu_q, seqs + 1, dev)
     _index("kv_lens", kv_lens, seqs, dev)
-    out, lse = _attn_out(q, shape, dev, out, lse)
+    out, lse = _attn_out(q, shape, dev, out, lse, stream)
     os_ = _rows3("out", out)
     if max_q is None:
         max_q = n
@@ -673,13 +684,7 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
         if len(cache._ws) > 4096:
             cache._ws.clear()
         cache._ws[key] = need
-    if not need:
-        ws = None
-    elif stream is None:
-        ws = _t.empty(need, dtype=_t.uint8, device=q.device)
-    else:                                    # memory that goes back to the stream that uses it
-        with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=q.device)):
-            ws = _t.empty(need, dtype=_t.uint8, device=q.device)
+    ws = _empty(need, _t.uint8, q.device, stream) if need else None
     _call(dev, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
           kv_lens.data_ptr(), n, max_q, h, scale, out.data_ptr(), os_[0], os_[1],
           lse.data_ptr() if lse is not False else None, ws.data_ptr() if need else None, need)
@@ -705,7 +710,7 @@ def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream
     if seqs < 1:
         _refuse("cu: int32 [sequences + 1]")
     _index("cu", cu, seqs + 1, dev)
-    out, lse = _attn_out(q, shape, dev, out, lse)
+    out, lse = _attn_out(q, shape, dev, out, lse, stream)
     os_ = _rows3("out", out)
     _call(dev, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
           v.data_ptr(), vs[0], vs[1], cu.data_ptr(), seqs, n, n if max_len is None else max_len, h, kshape[1], d,

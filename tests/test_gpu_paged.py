@@ -943,3 +943,44 @@ def test_attn_paged_every_scale(kernel, hd):
         k, v = _read(c, _values(c), torch.zeros_like(pos), pos)
         out = out.to(F64) * 2.0 ** (127 - vb)
         _check_rows(out, lse, _attend_ref(q, k, v, n, hd ** -0.5), ctx, hd)
+
+
+def _taken_blocks(call, shapes):
+    """Pointers of blocks that the current stream has freed while its queued work still writes them, one
+    of each shape, and the results of the call made meanwhile on a stream of its own."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(s, dtype=dt, device="cuda") for s, dt in shapes]
+    torch.cuda._sleep(20_000_000)
+    for x in blocks:
+        x.fill_(77)
+    at = {x.data_ptr() for x in blocks}
+    del blocks, x
+    got = call(side.cuda_stream)
+    torch.cuda.synchronize()
+    return at, got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_results_belong_to_the_given_stream(dtype):
+    """With a raw stream given, results are not taken from memory that earlier work of the current
+    stream still uses: that work would write over them."""
+    n, ctx, hq, hk, hd = 4, 9000, 16, 4, 128
+    c, q, cu, lens = _paged_case(52, hq, hk, hd, 32, dtype, [n], [ctx])
+    plan = sv.rope_plan(hd, 10000.0)
+    pos = torch.arange(n, device="cuda").int()
+    seq = torch.zeros_like(pos)
+    kv = q[:, :hk].contiguous()
+    b16, f32 = torch.bfloat16, torch.float32
+    calls = [
+        (lambda s: sv.attn_paged(q, c, cu, lens, max_q=n, stream=s), [((n, hq, hd), b16), ((n, hq), f32)]),
+        (lambda s: sv.attn_prompt(q, kv, kv, cu, stream=s), [((n, hq, hd), b16), ((n, hq), f32)]),
+        (lambda s: sv.kv_gather(c, seq, pos, stream=s), [((n, hk, hd), b16)] * 2),
+        (lambda s: (sv.rope_rows(q, pos, plan, stream=s),), [((n, hq, hd), b16)]),
+    ]
+    for call, shapes in calls:
+        want = call(None)
+        at, got = _taken_blocks(call, shapes)
+        for x, y in zip(got, want):
+            assert x.data_ptr() not in at and torch.equal(x, y)
