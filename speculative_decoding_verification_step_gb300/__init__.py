@@ -490,7 +490,9 @@ def _empty(shape, dtype, device, stream):
     stream's may still be in use by work queued there."""
     if stream is None:
         return _t.empty(shape, dtype=dtype, device=device)
-    with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=device)):
+    # (handle 0 is the default stream, of which ExternalStream makes another)
+    own = _t.cuda.ExternalStream(stream, device=device) if stream else _t.cuda.default_stream(device)
+    with _t.cuda.stream(own):
         return _t.empty(shape, dtype=dtype, device=device)
 
 

@@ -984,3 +984,18 @@ def test_results_belong_to_the_given_stream(dtype):
         at, got = _taken_blocks(call, shapes)
         for x, y in zip(got, want):
             assert x.data_ptr() not in at and torch.equal(x, y)
+
+
+def test_default_stream_by_its_handle():
+    """Handle 0 is the default stream, and all that a call allocates is that stream's own memory."""
+    n, ctx, hq, hk, hd = 4, 20000, 16, 4, 128
+    c, q, cu, lens = _paged_case(53, hq, hk, hd, 32, "e4m3", [n], [ctx])
+    assert sv.lib().spec_attn_paged_workspace(c._ref, n, n, hq) > 0
+    want = sv.attn_paged(q, c, cu, lens, max_q=n)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = {s["address"] for s in torch.cuda.memory_snapshot()}
+    got = sv.attn_paged(q, c, cu, lens, max_q=n, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(s["stream"] == 0 for s in torch.cuda.memory_snapshot() if s["address"] not in held)
