@@ -440,7 +440,9 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * below 2^-10 of their row's largest may be rounded by up to 2^-17 of that.
  * Cache slots past a sequence's length are never used, whatever they hold; a
  * value row that is not finite within the length reaches the outputs of the
- * whole chunk.
+ * whole chunk.  Every wait inside the kernels is bounded; should one run out, the
+ * rows that it served (out and lse) are NaN, never a wrong number, and the call,
+ * which has long returned, has reported nothing.
  * workspace: device memory, 16-byte aligned, of workspace_bytes (what it holds
  * before and after means nothing; calls that may overlap need their own), or
  * NULL: with fewer bytes than spec_attn_paged_workspace says the call is
@@ -523,12 +525,19 @@ SPEC_API int spec_phase_times(spec_ctx* ctx, int which, int64_t* out, int max_ph
  *   barrier, nothing is committed, and the step returns SPEC_E_TIMEOUT with
  *   the committed state unchanged.  arg = 0 disarms it.  The bound keeps
  *   every wait finite: no kernel hangs and the context stays usable.
- * SPEC_FAULT_CLEAR: disarm both (ctx may be NULL).
+ * SPEC_FAULT_ATTN_TIMEOUT (ctx must be NULL, arg >= 0): with arg > 0 every
+ *   block of the tensor-memory kernels of later spec_attn_paged and
+ *   spec_attn_prompt calls of the process waits, around its arg-th step of 128
+ *   keys, for a signal that never comes, gives up, and leaves NaN in the rows
+ *   that it had not finished (see spec_attn_paged).
+ *   arg = 0 disarms it.
+ * SPEC_FAULT_CLEAR: disarm all (ctx may be NULL).
  * Errors: SPEC_E_ARG for an unknown kind or a bad argument, SPEC_E_STATE for
  * SPEC_FAULT_WAIT_TIMEOUT on a context without persistent kernels. */
 #define SPEC_FAULT_CLEAR         0
 #define SPEC_FAULT_ALLOC         1
 #define SPEC_FAULT_WAIT_TIMEOUT  2
+#define SPEC_FAULT_ATTN_TIMEOUT  3
 SPEC_API int spec_inject_fault(spec_ctx* ctx, int kind, int arg);
 
 /* Bytes of device memory held by every live context of the process (the

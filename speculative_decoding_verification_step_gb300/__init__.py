@@ -38,6 +38,7 @@ SPEC_OPT_PHASE_TIMES = 0x10
 SPEC_FAULT_CLEAR = 0
 SPEC_FAULT_ALLOC = 1
 SPEC_FAULT_WAIT_TIMEOUT = 2
+SPEC_FAULT_ATTN_TIMEOUT = 3
 
 _LAYER_FIELDS = ("attn_norm", "wq", "wk", "wv", "wo", "ffn_norm", "w_gate", "w_up", "w_down")
 
@@ -366,6 +367,12 @@ class SpecDecoder:
 def inject_alloc_failure(n):
     """Test hook: the n-th device allocation of the next context creation fails."""
     _check(lib().spec_inject_fault(None, SPEC_FAULT_ALLOC, n))
+
+
+def inject_attention_timeout(step):
+    """Test hook: blocks of the tensor-memory attention kernels give up at their
+    step-th 128 keys (0: disarm) -- see include/specverify.h."""
+    _check(lib().spec_inject_fault(None, SPEC_FAULT_ATTN_TIMEOUT, step))
 
 
 def clear_faults():

@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.h"
 #include "specverify.h"
 
 using namespace sv;
@@ -1572,6 +1573,7 @@ int spec_sample_rows(const float* logits, int64_t row_stride, int rows, int V, f
 int spec_inject_fault(spec_ctx* c, int kind, int arg) {
   if (kind == SPEC_FAULT_CLEAR) {
     g_fail_alloc_at = 0;
+    sv::g_attn_give_up = 0;
     if (c && c->fault_ctl) {
       const int z[2] = {0, 0};
       CUDA_TRY(c, cudaMemcpyAsync(c->fault_ctl, z, sizeof z, cudaMemcpyHostToDevice, c->stream));
@@ -1594,6 +1596,12 @@ int spec_inject_fault(spec_ctx* c, int kind, int arg) {
     const int w[2] = {arg > 0 ? 1 : 0, arg};
     CUDA_TRY(c, cudaMemcpyAsync(c->fault_ctl, w, sizeof w, cudaMemcpyHostToDevice, c->stream));
     CUDA_TRY(c, cudaStreamSynchronize(c->stream));
+    return SPEC_OK;
+  }
+  if (kind == SPEC_FAULT_ATTN_TIMEOUT) {
+    if (c) return fail(c, SPEC_E_ARG, "SPEC_FAULT_ATTN_TIMEOUT applies to the stateless calls: pass a NULL context");
+    if (arg < 0) return fail(nullptr, SPEC_E_ARG, "SPEC_FAULT_ATTN_TIMEOUT needs arg >= 0");
+    sv::g_attn_give_up = arg;
     return SPEC_OK;
   }
   return fail(c, SPEC_E_ARG, "unknown fault kind");

@@ -144,15 +144,25 @@ SV_DEV void ta_tma_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uin
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)) : "memory");
 }
 // Bounded wait; false (after raising the abort flag) when it gives up.
-SV_DEV bool ta_wait(uint64_t* bar, unsigned parity, volatile int* abort) {
+SV_DEV bool ta_wait(uint64_t* bar, unsigned parity, volatile int* abort, long long limit = kTaWaitLimit) {
   long long spins = 0;
   while (!mbar_test(bar, parity)) {
-    if (*abort || ++spins > kTaWaitLimit) {
+    if (*abort || ++spins > limit) {
       *abort = 1;
       return false;
     }
   }
   return true;
+}
+
+// The products that this warp has issued, and their signals, are done (bounded).
+// Called by the issuing warp once no warp of the block goes on; bar is unused otherwise.
+SV_DEV void ta_drain(uint64_t* bar) {
+  if (ta_elect()) ta_commit(bar);
+  __syncwarp();
+  long long spins = 0;
+  while (!mbar_test(bar, 0) && ++spins < (1LL << 20)) {
+  }
 }
 
 template <int N>

@@ -93,7 +93,10 @@ struct PAttn {
   int64_t table_stride;
   int pages, page_shift, max_pages;
   float* ws;                     // workspace of launch_pattn_td, or null
+  int give_up;                   // test hook: the step of a tensor-memory block that waits for what never comes (0: none)
 };
+// SPEC_FAULT_ATTN_TIMEOUT: give_up of the calls from now on.
+extern std::atomic<int> g_attn_give_up;
 // Rows per KV head of the longest sequence beyond which the tensor-memory
 // kernel takes every call that both can.
 constexpr int kPaMaxRows = 64;

@@ -58,6 +58,8 @@
 
 namespace sv {
 
+std::atomic<int> g_attn_give_up{0};
+
 namespace {
 
 constexpr int kPaThreads = 128;
@@ -634,6 +636,7 @@ int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
     return fail(SPEC_E_ARG, w + "q and out must be 16-byte aligned with strides multiples of 8");
   if (a.scale_log2 == 0.f) a.scale_log2 = 1.f / std::sqrt((float)a.hd);
   a.scale_log2 *= 1.4426950408889634f;
+  a.give_up = g_attn_give_up.load(std::memory_order_relaxed);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -139,7 +139,8 @@ struct TaItem {
   int steps[2];       // of those, each tile's (from beg)
 };
 
-template <int HD, bool F8>
+// Hook: the form of SPEC_FAULT_ATTN_TIMEOUT, whose a.give_up-th step waits for what never comes.
+template <int HD, bool F8, bool Hook>
 __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
   using L = TaLayout<HD, F8>;
   constexpr int kHalf = HD / 64;                       // 64-dim halves of a row
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       };
       int i0 = 0, loads = 0;                  // ring fill of the item's first K, Q loads
       unsigned np[2] = {0, 0};                // steps of each tile over all items
+      [[maybe_unused]] int hook = a.give_up;
       bool ok = true;
       TaItem it;
       for (int k = 0; ok && get_item(k, it); ++k) {
@@ -457,6 +459,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         for (int j = 0; ok && j < it.nst; ++j) {
           const int iv = i0 + 2 * j + 1, ik = iv + 1;
           ok = wait(&kv_full[iv % kS], (unsigned)((iv / kS) & 1));
+          if constexpr (Hook) ok = ok && (--hook != 0 || __all_sync(0xffffffffu, ta_wait(&drained, 0, &s_abort, 0)));
           if constexpr (!F8) {
             // V's rows past the length: p is zero there, but the slots may hold anything
             const int rows = it.keys - (it.beg + j) * kTaKeys;
@@ -495,12 +498,6 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         }
         i0 += 2 * it.nst;
         ++loads;
-      }
-      if (!ok) {   // the products issued so far end before the space goes
-        signal(&drained);
-        long long spins = 0;
-        while (!mbar_test(&drained, 0) && ++spins < (1LL << 20)) {
-        }
       }
     } else if (warp == 10) {
       // ---- scheduler ----
@@ -735,8 +732,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     }
   }
   __syncthreads();
+  // a wait gave up, in whichever warp: products and copies in flight end (bounded) before the space goes
+  if (s_abort && warp == 9) ta_drain(&drained);
   if (s_abort && threadIdx.x == 0) {
-    // a wait gave up: copies in flight land (bounded) before the space goes
     constexpr int kRing = F8 ? L::raws : kS;
     for (int i = max(0, s_filled - kRing); i < s_filled; ++i) {
       long long spins = 0;
@@ -757,12 +755,17 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+template <int HD, bool F8, bool Hook>
+cudaError_t launch_ta_hook(const TaArgs& ta, cudaStream_t st) {
+  using L = TaLayout<HD, F8>;
+  auto kern = pattn_tc_kernel<HD, F8, Hook>;
+  return launch_rows_smem(std::integral_constant<int, HD * 4 + F8 * 2 + Hook>(), kern, dim3((unsigned)(ta.split * ta.items)), dim3(L::threads), L::smem,
+                          ta.split, st, ta);
+}
+
 template <int HD, bool F8>
 cudaError_t launch_ta(const TaArgs& ta, cudaStream_t st) {
-  using L = TaLayout<HD, F8>;
-  auto kern = pattn_tc_kernel<HD, F8>;
-  return launch_rows_smem(std::integral_constant<int, HD * 2 + F8>(), kern, dim3((unsigned)(ta.split * ta.items)), dim3(L::threads), L::smem,
-                          ta.split, st, ta);
+  return ta.a.give_up > 0 ? launch_ta_hook<HD, F8, true>(ta, st) : launch_ta_hook<HD, F8, false>(ta, st);
 }
 
 }  // namespace

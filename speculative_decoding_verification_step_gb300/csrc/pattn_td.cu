@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
           for (int j = 0; ok && j < w.seg; ++j, ++i) {
             // the scores before the last are read
             if (i >= 4) ok = wait(&p_full[i & 3], (unsigned)((i / 4 - 1) & 1));
+            if (i + 1 == a.give_up) ok = __all_sync(0xffffffffu, ta_wait(&drained[0], 0, &s_abort, 0));
             ok = ok && wait(&k_full[i % L::ks], (unsigned)((i / L::ks) & 1));
             if (!ok) break;
             const uint32_t k_at = base + L::k_at + (uint32_t)(i % L::ks) * L::tile;
@@ -477,13 +478,6 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
             }
             __syncwarp();
           }
-        }
-      }
-      if (!ok) {   // the products issued so far end before the space goes
-        if (ta_elect()) ta_commit(&drained[warp - 5]);
-        __syncwarp();
-        long long spins = 0;
-        while (!mbar_test(&drained[warp - 5], 0) && ++spins < (1LL << 20)) {
         }
       }
     }
@@ -697,8 +691,9 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
     }
   }
   __syncthreads();
+  // a wait gave up, in whichever warp: products and copies in flight end (bounded) before the space goes
+  if (s_abort && (warp == 5 || warp == 6)) ta_drain(&drained[warp - 5]);
   if (s_abort && threadIdx.x == 0) {
-    // a wait gave up: copies in flight land (bounded) before the space goes
     for (int i = max(0, s_kfill - L::ks); i < s_kfill; ++i) {
       long long spins = 0;
       while (!mbar_test(&k_full[i % L::ks], (unsigned)((i / L::ks) & 1)) && ++spins < (1LL << 20)) {

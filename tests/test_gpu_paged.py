@@ -999,3 +999,36 @@ def test_default_stream_by_its_handle():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(s["stream"] == 0 for s in torch.cuda.memory_snapshot() if s["address"] not in held)
+
+
+# ------------------------------------------------------- waits that run out
+def _give_up(call, q, steps):
+    """The call with the hook armed at each of `steps`: every row is NaN or as without it, some are NaN,
+    and the next call is right."""
+    clean, clse = torch.full_like(q, 7.0, memory_format=torch.contiguous_format), torch.full(q.shape[:2], 9.0, device="cuda")
+    call(clean, clse)
+    for step in steps:
+        out, lse = torch.full_like(clean, 5.0), torch.full_like(clse, 5.0)
+        torch.cuda.synchronize()
+        sv.inject_attention_timeout(step)
+        try:
+            call(out, lse)
+        finally:
+            sv.clear_faults()
+        torch.cuda.synchronize()
+        none = torch.isnan(lse)
+        assert none.any(), step
+        assert torch.isnan(out[none]).all()
+        assert torch.equal(out[~none], clean[~none]) and torch.equal(lse[~none], clse[~none])
+        call(out, lse)
+        assert torch.equal(out, clean) and torch.equal(lse, clse)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype,ns,ctx", [("bf16", [256, 130, 64], [5000, 3333, 6001]), ("e4m3", [256, 130, 64], [5000, 3333, 6001]),
+                                          ("bf16", [300], [700]), ("e4m3", [6, 3], [20000, 9000]), ("e4m3", [3], [30000])])
+def test_waits_that_run_out(hd, dtype, ns, ctx):
+    """Chunks (two blocks an item, and one) and few rows over long 8-bit contexts: a block that gives up
+    early or late leaves NaN, and its products and copies in flight end before it does."""
+    c, q, cu, lens = _paged_case(61, 16, 4, hd, 64, dtype, ns, ctx)
+    _give_up(lambda o, l: sv.attn_paged(q, c, cu, lens, max_q=max(ns), out=o, lse=l), q, (1, 2, 3))

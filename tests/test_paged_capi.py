@@ -162,3 +162,10 @@ def test_expanded_cache_refusals(L):
                  (wide(codes), wide(codes), table, scales, scales)):
         with pytest.raises(sv.SpecError, match="first stride of 0"):
             sv.KVCache(*args)
+
+
+def test_timeout_hook_arguments(L):
+    assert L.spec_inject_fault(None, sv.SPEC_FAULT_ATTN_TIMEOUT, -1) == -1
+    assert L.spec_inject_fault(None, sv.SPEC_FAULT_ATTN_TIMEOUT, 2) == 0
+    assert L.spec_inject_fault(None, sv.SPEC_FAULT_CLEAR, 0) == 0
+    sv.inject_attention_timeout(0)
