@@ -155,14 +155,19 @@ SV_DEV bool ta_wait(uint64_t* bar, unsigned parity, volatile int* abort, long lo
   return true;
 }
 
+// Bounded wait that another warp's giving up does not end.
+SV_DEV bool ta_land(uint64_t* bar, unsigned parity) {
+  long long spins = 0;
+  while (!mbar_test(bar, parity))
+    if (++spins > kTaWaitLimit) return false;
+  return true;
+}
 // The products that this warp has issued, and their signals, are done (bounded).
 // Called by the issuing warp once no warp of the block goes on; bar is unused otherwise.
 SV_DEV void ta_drain(uint64_t* bar) {
   if (ta_elect()) ta_commit(bar);
   __syncwarp();
-  long long spins = 0;
-  while (!mbar_test(bar, 0) && ++spins < (1LL << 20)) {
-  }
+  (void)ta_land(bar, 0);
 }
 
 template <int N>

@@ -255,9 +255,12 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   constexpr uint32_t o_at = 256;
 
-  // Next item of the queue (the k-th of this block); false at the end or when a wait gave up.
-  auto get_item = [&](int k, TaItem& it) {
-    const bool got = __all_sync(0xffffffffu, ta_wait(&item_full[k & 1], (unsigned)((k >> 1) & 1), &s_abort));
+  // Next item of the queue (the k-th of this block); false at the end or, but for
+  // `last`, when a wait gave up.  The softmax warps take all that is handed out:
+  // no other block will write those rows.
+  auto get_item = [&](int k, TaItem& it, bool last = false) {
+    const bool got = __all_sync(0xffffffffu, last ? ta_land(&item_full[k & 1], (unsigned)((k >> 1) & 1))
+                                                  : ta_wait(&item_full[k & 1], (unsigned)((k >> 1) & 1), &s_abort));
     it = s_item[k & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[k & 1]);
@@ -501,8 +504,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       }
     } else if (warp == 10) {
       // ---- scheduler ----
+      // (An item is handed out after all have begun the one before, so the queue's
+      // other place is free: the end of the queue is handed out without a wait.)
       TaItem it = mine;
-      bool ok = true;
       unsigned takes = 0;
       for (int k = 0;; ++k) {
         if (lane == 0) {
@@ -512,16 +516,19 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         __syncwarp();
         if (!it.valid) break;
         // one item ahead: the next is taken when all have begun this one
-        ok = __all_sync(0xffffffffu, ta_wait(&item_empty[k & 1], (unsigned)((k >> 1) & 1), &s_abort));
+        const bool ok = __all_sync(0xffffffffu, ta_wait(&item_empty[k & 1], (unsigned)((k >> 1) & 1), &s_abort));
         it.valid = 0;
-        while (ok && ta.split == 1) {          // a block of the grid that has not started and holds rows
+        // a block of the grid that has not started and holds rows; none once a wait gave up
+        while (ok && ta.split == 1 && !__any_sync(0xffffffffu, s_abort)) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&taken, 16);
             ta_take(&s_taken, &taken);
           }
-          ok = __all_sync(0xffffffffu, ta_wait(&taken, takes & 1, &s_abort));
+          // the response is waited for whatever else gave up: a block that was taken
+          // over never starts, so its item is handed out (and becomes NaN)
+          const bool got = __all_sync(0xffffffffu, ta_land(&taken, takes & 1));
           ++takes;
-          if (!ok) break;
+          if (!got) break;
           const int idx = ta_taken(&s_taken);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // read before the next response lands there
           __syncwarp();
@@ -529,11 +536,10 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           it.valid = item_at(idx, it);
           if (it.valid) break;
         }
-        if (!ok) break;
       }
-      // a response on its way lands (bounded) before the space goes
+      // had that wait run out: the response lands (bounded) before the space goes
       long long spins = 0;
-      while (!ok && takes > 0 && !mbar_test(&taken, (takes - 1) & 1) && ++spins < (1LL << 20)) {
+      while (takes > 0 && !mbar_test(&taken, (takes - 1) & 1) && ++spins < (1LL << 20)) {
       }
     }
   } else {
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     unsigned np = 0;                           // steps of this tile over all items
     bool ok = true;
     TaItem it;
-    for (int k = 0; get_item(k, it); ++k) {   // (after a wait gave up: what was handed out still gets its NaN)
+    for (int k = 0; get_item(k, it, true); ++k) {   // (after a wait gave up: what was handed out still gets its NaN)
       const int t_at = it.tok0 + t * tpt, tok = t_at + ti;
       const bool row_ok = t < it.ntile && ti < tpt && tok < it.toks;
       const int seen = row_ok ? min(it.keys, max(0, it.first_pos + tok + 1)) : 0;

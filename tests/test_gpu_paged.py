@@ -1032,3 +1032,15 @@ def test_waits_that_run_out(hd, dtype, ns, ctx):
     early or late leaves NaN, and its products and copies in flight end before it does."""
     c, q, cu, lens = _paged_case(61, 16, 4, hd, 64, dtype, ns, ctx)
     _give_up(lambda o, l: sv.attn_paged(q, c, cu, lens, max_q=max(ns), out=o, lse=l), q, (1, 2, 3))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_items_taken_by_a_block_that_gives_up(dtype, hd):
+    """Far more items than blocks at work: one that a block took over from the grid just before it gave
+    up is written (as NaN) too, however often."""
+    ns = [900, 1500, 1, 640] * 4 if dtype == "bf16" else [600, 256, 31, 500] * 5
+    ctx = ns if dtype == "bf16" else [n + 300 for n in ns]
+    c, q, cu, lens = _paged_case(62, 16, 8, hd, 64, dtype, ns, ctx)
+    for step in (1, 3, 6, 9, 14, 20):
+        _give_up(lambda o, l: sv.attn_paged(q, c, cu, lens, max_q=max(ns), out=o, lse=l), q, (step,) * 3)
