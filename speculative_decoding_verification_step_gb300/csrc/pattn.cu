@@ -620,6 +620,30 @@ size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
   return many || few ? pattn_td_workspace(rows, a.hd, sms) : 0;
 }
 
+// Up to 32 rows per KV head the register-tile kernel, beyond kPaMaxRows the
+// tensor-memory one where it applies.  Between them the first walks the keys
+// once per 32 rows but cuts them between up to eight blocks, the second walks
+// them once for all rows: it is taken where (sequence, KV head) pairs keep its
+// blocks busy, at head dim 64 only from 49 rows and 16-bit keys on.  Measured,
+// tensor memory against register tiles, 4096 keys, 8 KV heads, head dim 128:
+// 64 rows of 16 sequences 60 / 74 us (8-bit keys 83 / 89), of 8 sequences
+// 39 / 47 (49 / 54), of 4 36 / 30; 36 rows of 16 sequences 60 / 77 (83 / 92),
+// of 12 60 / 52.  Head dim 64: 64 rows of 16 sequences 44 / 57 (70 / 70), of
+// 12 44 / 39; 36 rows of 64 sequences 121 / 113 (197 / 156).  A batch with
+// both kinds goes whole: a short sequence costs the tensor-memory kernel one
+// tile's walk over the keys beside the long ones, less than a second launch
+// behind them.
+struct Way {
+  bool tc;        // pattn_tc.cu
+  size_t td_ws;   // else pattn_td.cu with a workspace of so many bytes, if not 0; else the register tiles
+};
+Way choose_way(const PAttn& a, int sms) {
+  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), pairs = (int64_t)a.seqs * a.hkv;
+  const bool many = rows > 48, busy = a.hd == 128 ? pairs * (many ? 8 : 4) >= 3 * sms : many && !a.f8 && pairs * 4 >= 3 * sms;
+  if ((rows > kPaMaxRows || (rows > 32 && busy)) && pattn_tc_supported(a)) return {true, 0};
+  return {false, td_bytes(a, rows, sms)};
+}
+
 // Both attention calls, after their own checks.
 int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
   const std::string w = std::string(who) + ": ";
@@ -641,23 +665,9 @@ int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
-  // Up to 32 rows per KV head the register-tile kernel, beyond kPaMaxRows the
-  // tensor-memory one where it applies.  Between them the first walks the keys
-  // once per 32 rows but cuts them between up to eight blocks, the second walks
-  // them once for all rows: it is taken where (sequence, KV head) pairs keep its
-  // blocks busy, at head dim 64 only from 49 rows and 16-bit keys on.  Measured,
-  // tensor memory against register tiles, 4096 keys, 8 KV heads, head dim 128:
-  // 64 rows of 16 sequences 60 / 74 us (8-bit keys 83 / 89), of 8 sequences
-  // 39 / 47 (49 / 54), of 4 36 / 30; 36 rows of 16 sequences 60 / 77 (83 / 92),
-  // of 12 60 / 52.  Head dim 64: 64 rows of 16 sequences 44 / 57 (70 / 70), of
-  // 12 44 / 39; 36 rows of 64 sequences 121 / 113 (197 / 156).  A batch with
-  // both kinds goes whole: a short sequence costs the tensor-memory kernel one
-  // tile's walk over the keys beside the long ones, less than a second launch
-  // behind them.
-  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), pairs = (int64_t)a.seqs * a.hkv;
-  const bool many = rows > 48, busy = a.hd == 128 ? pairs * (many ? 8 : 4) >= 3 * sms : many && !a.f8 && pairs * 4 >= 3 * sms;
-  if ((rows > kPaMaxRows || (rows > 32 && busy)) && pattn_tc_supported(a)) e = launch_pattn_tc(a, sms, st);
-  else if (const size_t need = td_bytes(a, rows, sms); need && a.ws && ws_bytes >= need) e = launch_pattn_td(a, sms, st);
+  const Way way = choose_way(a, sms);
+  if (way.tc) e = launch_pattn_tc(a, sms, st);
+  else if (way.td_ws && a.ws && ws_bytes >= way.td_ws) e = launch_pattn_td(a, sms, st);
   else e = a.hd == 32 ? launch_pa_hd<32>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64>(a, sms, st) : launch_pa_hd<128>(a, sms, st);
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
 }
@@ -712,8 +722,10 @@ int64_t spec_attn_paged_workspace(const spec_kv_cache* cache, int tokens, int ma
     return 0;
   PAttn a{};
   cache_fields(a, cache);
-  a.hq = n_heads;
-  return (int64_t)td_bytes(a, (int64_t)std::min(max_q, tokens) * (n_heads / a.hkv), sms);
+  // (queries and outputs with strides that the kernels take: others go to the register tiles)
+  a.hq = n_heads; a.tokens = tokens; a.max_q = max_q;
+  a.q_hs = a.o_hs = a.hd; a.q_ts = a.o_ts = (int64_t)n_heads * a.hd;
+  return (int64_t)choose_way(a, sms).td_ws;
 }
 
 int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* k, int64_t k_tok_stride,

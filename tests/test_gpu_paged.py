@@ -1044,3 +1044,27 @@ def test_items_taken_by_a_block_that_gives_up(dtype, hd):
     c, q, cu, lens = _paged_case(62, 16, 8, hd, 64, dtype, ns, ctx)
     for step in (1, 3, 6, 9, 14, 20):
         _give_up(lambda o, l: sv.attn_paged(q, c, cu, lens, max_q=max(ns), out=o, lse=l), q, (step,) * 3)
+
+
+@pytest.mark.parametrize("seqs,n,ctx,hq,hk,hd,ps", [
+    (64, 16, 4096, 32, 8, 128, 16), (64, 9, 4096, 32, 8, 128, 16), (32, 6, 4096, 32, 8, 128, 16), (3, 4, 20000, 16, 4, 64, 16),
+    (64, 16, 4096, 32, 8, 64, 64), (1, 16, 20000, 16, 4, 128, 32), (1, 64, 20000, 4, 4, 128, 32), (2, 40, 9000, 8, 4, 128, 16),
+    (16, 1, 4096, 32, 8, 128, 64), (5, 30, 2048, 8, 2, 128, 16)])
+def test_workspace_is_used_where_asked_for(seqs, n, ctx, hq, hk, hd, ps):
+    """spec_attn_paged_workspace and the call go by one rule: bytes are asked for where the call uses
+    them, and a call that asks for none leaves what it is given alone."""
+    g = _gen(71)
+    need = -(-ctx // ps)
+    table = torch.randint(0, 64, (seqs, need), generator=g, device="cuda").int()
+    c = sv.KVCache.empty(64, ps, hk, hd, table, "e4m3")
+    for t in (c.k, c.v):
+        t.copy_(_randn(g, *t.shape))
+    q, lens = _randn(g, seqs * n, hq, hd).bfloat16(), _i32([ctx] * seqs)
+    cu, L = _i32([n * b for b in range(seqs + 1)]), sv.lib()
+    want = L.spec_attn_paged_workspace(c._ref, seqs * n, n, hq)
+    ws = torch.full((max(want, 1 << 25),), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    assert L.spec_attn_paged(c._ref, q.data_ptr(), q.stride(0), q.stride(1), cu.data_ptr(), lens.data_ptr(), seqs * n, n, hq, 0.0,
+                             out.data_ptr(), hq * hd, hd, None, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out, sv.attn_paged(q, c, cu, lens, max_q=n)[0])
+    assert bool((ws != 0x5a).any()) == (want > 0)
