@@ -447,7 +447,9 @@ def sample_rows(logits, temperature, seed, step_base=0, position=1, stream=None,
 # `stream` given, a result that is used or dropped on another stream needs that
 # stream to wait, and record_stream.  A step makes a call per layer and waits
 # for none, so the checks are plain comparisons, and messages are made only
-# where one fails.
+# where one fails.  None records a backward pass, so rows that require grad are
+# refused while grad mode is on (a Function of one's own runs with it off:
+# rope_rows with `inverse` is the gradient of rope_rows).
 _t = None
 
 
@@ -479,6 +481,8 @@ def _io_dtype(t):
 
 def _rows3(name, t):
     """Strides of a CUDA tensor [tokens, heads, head_dim]."""
+    if t.requires_grad and _t.is_grad_enabled():
+        _refuse(f"{name} requires grad, and the call has no backward pass: detach it, or call under torch.no_grad()")
     if not t.is_cuda or t.dim() != 3:
         _refuse(f"{name}: a CUDA tensor [tokens, heads, head_dim]")
     st = t.stride()

@@ -1068,3 +1068,35 @@ def test_workspace_is_used_where_asked_for(seqs, n, ctx, hq, hk, hd, ps):
                              out.data_ptr(), hq * hd, hd, None, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
     assert torch.equal(out, sv.attn_paged(q, c, cu, lens, max_q=n)[0])
     assert bool((ws != 0x5a).any()) == (want > 0)
+
+
+def test_gradients_are_refused_or_whole():
+    """Rows that require grad are refused; a Function of one's own has the rotation's gradient by `inverse`."""
+    g = _gen(81)
+    n, hq, hk, hd = 9, 8, 2, 64
+    c, q, cu, lens = _paged_case(81, hq, hk, hd, 16, "bf16", [n], [40])
+    pos, plan = torch.arange(n, device="cuda").int(), sv.rope_plan(hd, 10000.0)
+    leaf, kv = q.clone().requires_grad_(), q[:, :hk].contiguous()
+    seq = torch.zeros_like(pos)
+    for call in (lambda: sv.rope_rows(leaf, pos, plan), lambda: sv.attn_paged(leaf, c, cu, lens),
+                 lambda: sv.attn_prompt(leaf, kv, kv, cu), lambda: sv.attn_prompt(q, leaf[:, :hk], kv, cu),
+                 lambda: sv.attn_prompt(q, kv, leaf[:, :hk], cu), lambda: sv.kv_append(c, leaf[:, :hk], kv, seq, pos),
+                 lambda: sv.kv_append(c, kv, leaf[:, :hk], seq, pos)):
+        with pytest.raises(sv.SpecError, match="requires grad"):
+            call()
+    with torch.no_grad():
+        assert torch.equal(sv.attn_paged(leaf, c, cu, lens)[0], sv.attn_paged(q, c, cu, lens)[0])
+
+    class Rotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return sv.rope_rows(x, pos, plan)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return sv.rope_rows(dy.contiguous(), pos, plan, inverse=True)
+
+    x, u = _randn(g, n, hq, hd).requires_grad_(), _randn(g, n, hq, hd)
+    (Rotate.apply(x) * u).sum().backward()
+    ref, size = _rope_ref(u, pos, _freqs(hd, 10000.0), False, sign=-1.0)
+    assert ((x.grad.to(F64) - ref).abs() <= size * (8 * 2.0 ** -23 + n * 2.0 ** -50) + ref.abs() * 2.0 ** -24).all()

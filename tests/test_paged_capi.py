@@ -169,3 +169,16 @@ def test_timeout_hook_arguments(L):
     assert L.spec_inject_fault(None, sv.SPEC_FAULT_ATTN_TIMEOUT, 2) == 0
     assert L.spec_inject_fault(None, sv.SPEC_FAULT_CLEAR, 0) == 0
     sv.inject_attention_timeout(0)
+
+
+def test_gradients_are_not_dropped(L):
+    """Nothing here records a backward pass: rows that require grad are refused by name while grad mode is on."""
+    sv._torch()
+    leaf = torch.zeros(2, 2, 64, dtype=torch.bfloat16, requires_grad=True)
+    i, plan, cu = torch.zeros(2, dtype=torch.int32), sv.rope_plan(64, 10000.0), torch.tensor([0, 2], dtype=torch.int32)
+    for t in (leaf, leaf * 1.0):
+        for call in (lambda: sv.rope_rows(t, i, plan), lambda: sv.attn_prompt(t, t, t, cu), lambda: sv._rows3("k", t)):
+            with pytest.raises(sv.SpecError, match="requires grad"):
+                call()
+            with torch.no_grad(), pytest.raises(sv.SpecError, match="a CUDA tensor"):   # taken as any other
+                call()
