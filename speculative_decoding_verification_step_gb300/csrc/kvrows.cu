@@ -564,7 +564,7 @@ int spec_rope_plan(const spec_rope_desc* d, spec_rope* out) {
     return fail(SPEC_E_ARG, "spec_rope_plan: the grown theta needs rot_dim >= 4");
   if (d->scaling == SPEC_ROPE_PARTS && !(d->orig_ctx > 0.0 && d->high > d->low))
     return fail(SPEC_E_ARG, "spec_rope_plan: scaling by parts needs orig_ctx > 0 and high > low");
-  if (!(d->mscale >= 0.0) || !std::isfinite(d->mscale)) return fail(SPEC_E_ARG, "spec_rope_plan: bad mscale");
+  if (!(d->mscale >= 0.0) || !std::isfinite((float)d->mscale)) return fail(SPEC_E_ARG, "spec_rope_plan: bad mscale");
   const double kTurn = 6.283185307179586476925286766559;
   spec_rope r{};
   r.rot_dim = d->rot_dim;

@@ -182,3 +182,10 @@ def test_gradients_are_not_dropped(L):
                 call()
             with torch.no_grad(), pytest.raises(sv.SpecError, match="a CUDA tensor"):   # taken as any other
                 call()
+
+
+def test_plan_mscale_past_fp32(L):
+    """The factor is applied in fp32: one that is infinite there is refused."""
+    with pytest.raises(sv.SpecError, match="mscale"):
+        sv.rope_plan(64, 10000.0, mscale=1e39)
+    assert sv.rope_plan(64, 10000.0, mscale=3e38).mscale > 2.9e38
