@@ -65,6 +65,7 @@ namespace {
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaStep = 16;          // keys of a step
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPaLazy = 8.f;       // exponent reference moves past 2^8
 constexpr float kPaNone = -1e30f;    // reference of a row that has seen nothing
 
@@ -651,15 +652,15 @@ int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
     return fail(SPEC_E_SHAPE, w + "n_heads must be a multiple of n_kv_heads (at most 1024)");
   if (a.hd != 32 && a.hd != 64 && a.hd != 128) return fail(SPEC_E_SHAPE, w + "head_dim must be 32, 64 or 128");
   if (a.tokens < 0 || a.max_q < 0 || a.seqs < 1) return fail(SPEC_E_ARG, w + "bad tokens, bound or seqs");
-  if (!(a.scale_log2 == a.scale_log2) || std::isinf(a.scale_log2) || a.scale_log2 < 0.f)
-    return fail(SPEC_E_ARG, w + "scale must be finite and not negative");
+  if (!std::isfinite(a.scale_log2 * kLog2e) || a.scale_log2 < 0.f)
+    return fail(SPEC_E_ARG, w + "scale must be finite, also times log2(e), and not negative");
   if ((int64_t)a.tokens * (a.hq / a.hkv) > 0x7fffffffLL) return fail(SPEC_E_ARG, w + "too many rows");
   if (a.tokens == 0 || a.max_q == 0) return SPEC_OK;
   if (!a.q || !a.out || !a.cu) return fail(SPEC_E_ARG, w + "null pointer");
   if (!row_aligned(a.q, a.q_ts, a.q_hs) || !row_aligned(a.out, a.o_ts, a.o_hs))
     return fail(SPEC_E_ARG, w + "q and out must be 16-byte aligned with strides multiples of 8");
   if (a.scale_log2 == 0.f) a.scale_log2 = 1.f / std::sqrt((float)a.hd);
-  a.scale_log2 *= 1.4426950408889634f;
+  a.scale_log2 *= kLog2e;
   a.give_up = g_attn_give_up.load(std::memory_order_relaxed);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -189,3 +189,11 @@ def test_plan_mscale_past_fp32(L):
     with pytest.raises(sv.SpecError, match="mscale"):
         sv.rope_plan(64, 10000.0, mscale=1e39)
     assert sv.rope_plan(64, 10000.0, mscale=3e38).mscale > 2.9e38
+
+
+def test_scale_past_fp32(L):
+    """The scale is applied to exponents of two: one that is infinite there is refused."""
+    c = ctypes.byref(_cache())
+    for scale in (3e38, 2.4e38):
+        assert L.spec_attn_paged(c, P, 256, 64, P, P, 1, 1, 4, scale, P, 256, 64, None, None, 0, None) == -1
+        assert L.spec_attn_prompt(P, 256, 64, P, 128, 64, P, 128, 64, P, 1, 1, 1, 4, 2, 64, scale, P, 256, 64, None, None) == -1
