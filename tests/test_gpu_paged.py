@@ -1100,3 +1100,49 @@ def test_gradients_are_refused_or_whole():
     (Rotate.apply(x) * u).sum().backward()
     ref, size = _rope_ref(u, pos, _freqs(hd, 10000.0), False, sign=-1.0)
     assert ((x.grad.to(F64) - ref).abs() <= size * (8 * 2.0 ** -23 + n * 2.0 ** -50) + ref.abs() * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("seqs,n,ctx,hq,hk", [(2, 4, 320, 8, 2), (2, 3, 16384, 8, 1), (60, 12, 512, 32, 8), (3, 100, 512, 8, 2),
+                                              (2, 250, 4096, 8, 2)])
+def test_lengths_past_the_table(seqs, n, ctx, hq, hk, hd, dtype):
+    """Lengths beyond what the table holds are cut there, in every kernel: few rows, few rows of a long
+    8-bit context, 48 rows, many rows, many rows of few sequences."""
+    ns = [n] * seqs
+    c, q, cu, lens = _paged_case(91 + hd, hq, hk, hd, 64, dtype, [n] * seqs, [ctx] * seqs)
+    assert c.max_pages * 64 == ctx
+    out, lse = sv.attn_paged(q, c, cu, lens, max_q=n)
+    b = seqs - 1
+    pos = torch.arange(ctx, device="cuda").int()
+    k, v = _read(c, _values(c), torch.full_like(pos, b), pos)
+    _check_rows(out[b * n:], lse[b * n:], _attend_ref(q[b * n:], k, v, n, hd ** -0.5), ctx, hd)
+    for far in (ctx + 1, ctx + 64, 2 * ctx, 2 ** 31 - 1):
+        for which in (slice(None), slice(0, 1), slice(b, None)):
+            past = lens.clone()
+            past[which] = far
+            o, l = sv.attn_paged(q, c, cu, past, max_q=n)
+            assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_gather_one_side(dtype, out):
+    """Either output alone, rows of NaN among the others, and the other output's memory left alone."""
+    g = _gen(92)
+    hk, hd, n = 3, 64, 50
+    c = _cache(g, 2, 64, hk, 32, hd, dtype)
+    x = _randn(g, n, 2 * hk, hd)
+    x[7, 1, 3] = x[9, hk + 2, 5] = math.nan
+    seq, pos = _i32([i % 2 for i in range(n)]), _i32([i // 2 for i in range(n)])
+    sv.kv_append(c, x[:, :hk], x[:, hk:], seq, pos)
+    k, v = sv.kv_gather(c, seq, pos, dtype=out)
+    row = slice(None) if dtype == "e4m3" else 3
+    assert torch.isnan(k[7, 1, row]).all() and torch.isnan(v[9, 2, slice(None) if dtype == "e4m3" else 5]).all()
+    code, L = sv.SPEC_DTYPE_F32 if out == torch.float32 else sv.SPEC_DTYPE_BF16, sv.lib()
+    bits = lambda t: t.view(torch.int32 if out == torch.float32 else torch.int16)
+    for first in (True, False):
+        y = torch.full((2, n, hk, hd), 7.0, dtype=out, device="cuda")
+        p = [y[0].data_ptr(), None] if first else [None, y[1].data_ptr()]
+        assert L.spec_kv_gather(c._ref, seq.data_ptr(), pos.data_ptr(), n, *p, code, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(bits(y[0 if first else 1]), bits(k if first else v)) and (y[1 if first else 0] == 7.0).all()
