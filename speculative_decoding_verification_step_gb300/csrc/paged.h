@@ -61,7 +61,7 @@ inline cudaError_t launch_rows_smem(Tag, void (*kernel)(KArgs...), dim3 grid, di
 // Power of two of an 8-bit row: 2^(byte - 127), of which byte 0 is below fp32's
 // normal numbers; 255 marks a row of NaN.
 SV_DEV float row_power(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0x7fffffffu : byte == 0u ? 0x00400000u : byte << 23);
+  return __uint_as_float(byte == 255u ? 0x7fffffffu : max(byte << 23, 0x00400000u));
 }
 
 // Checks of a cache description shared by the entry points; SPEC_OK or the
