@@ -675,7 +675,8 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
     [tokens, n_heads, head_dim] bf16; sequence b (row b of the cache's table)
     owns rows cu_q[b] .. cu_q[b+1]-1 and kv_lens[b] cached positions, its new
     ones included (int32 [seqs + 1], [seqs]); max_q bounds the rows of one
-    sequence (default: tokens).  Returns (out, lse [tokens, n_heads] fp32, or
+    sequence and goes into the choice of kernel (default: tokens; give the
+    real bound for batches).  Returns (out, lse [tokens, n_heads] fp32, or
     None with lse=False); rows outside every sequence are not written."""
     _torch()
     qs = _rows3("q", q)
@@ -708,7 +709,7 @@ def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream
     """Causal attention within packed sequences: rows cu[b] .. cu[b+1]-1 of q
     [tokens, n_heads, head_dim] and k, v [tokens, n_kv_heads, head_dim] (bf16,
     may be slices of one projection) are sequence b; max_len bounds their
-    lengths (default: tokens).  Returns (out, lse) as attn_paged."""
+    lengths and sizes the grid (default: tokens; give the real bound for many).  Returns (out, lse) as attn_paged."""
     _torch()
     qs, ks, vs = _rows3("q", q), _rows3("k", k), _rows3("v", v)
     shape, kshape, dev = q.shape, k.shape, q.get_device()

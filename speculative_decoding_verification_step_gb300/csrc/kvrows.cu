@@ -17,11 +17,13 @@
 // is rounded once, to e4m3 (half a step, 2^-4 relative; below 2^(e-6) the
 // step is 2^(e-9) absolute), and code * 2^e is exact in bf16.
 //
-// Measured.  Rotation of 16381 bf16 rows of 40 heads of 128 29 us (5.5 TB/s, 81%
-// of a copy's rate); a step's 6 tokens 1.9 us of the GPU's time.  Append of
-// 16000 fp32 rows of 8 heads of 128 to bf16 33 us (89%), of bf16 rows to 8-bit
-// 24 us (3.7 TB/s): K's rotation and the encoding cost more issue slots than the
-// copies take.  Read-back of 16 x 16384 8-bit rows 192 us (6.5 TB/s, 96%).
+// Measured.  Rotation of 16381 bf16 rows of 40 heads of 64 30 us (5.7 TB/s, 83%
+// of a copy's rate); a step's 6 tokens 2.2 us of the GPU's time.  Append of
+// 16000 fp32 rows of 8 heads of 128 to bf16 34 us (86%), of bf16 rows to 8-bit
+// 25 us (4.0 TB/s).  The latter fills 56% of the issue slots and 35% of DRAM's
+// rate: its 4000 blocks run in 3.3 waves, and each starts with dependent loads
+// (sequence and position, then the table), sines and a barrier.  Read-back of
+// 16 x 16384 8-bit rows 191 us (6.6 TB/s, 97%).
 // Tiles of 4 x 128 units a block, two rows of a thread in flight and the slots
 // looked up behind the loads took append from 34 to 24 us and rotation from 33
 // to 29; more rows in flight spilled or left fewer blocks (26 and 30 us).

@@ -33,18 +33,20 @@
 // also exact, and their powers of two meet the probabilities before the rounding
 // to bf16: its range holds p * 2^e of every row at once, whatever other rows and
 // queries of the tile need.  (Products in f16 against a shared reference exponent
-// lost small rows beside large ones; they took 4% less time at 4 rows of 64 dims,
-// 7% less at 12 rows and 2% more at 24.)
+// lost small rows beside large ones; they took 4% less time at 4 rows, 6% at 12
+// and 2% at 24.  Leaving them for bf16 only once rows lie far apart cost as much in
+// choices as the conversions do.)
 // The share of the keys: a cluster of up to 8 blocks splits one tile's keys
 // and merges through distributed shared memory in a fixed order (no scratch
 // memory, no second launch, no atomics): blocks merge their four warps, then
 // block j of the cluster finishes the rows j, j + C, ...
 // Bound: by the copies for a few rows (64 sequences x 4096 keys of 8 heads of
-// 128, 16-bit, one token each: 128 us, 92% of a copy's rate; 16 x 16384 of 64
-// dims 66 us, 90%; 64 x 4096 8-bit of 128 dims 80 us, 75%), by the latencies of a step's instructions (600 of 16 keys
-// and 24 rows, three warps a partition) for more: 24 rows of 64 x 4096 162 us
-// (76%), 8-bit 152 us (40%), which is why long 8-bit contexts go to tensor
-// memory.  One sequence of 512 keys and 24 rows takes 9 us, most of it the
+// 128, 16-bit, one token each: 129 us, 91% of a copy's rate; 16 x 16384 of 64
+// dims 66 us, 89%; 64 x 4096 8-bit of 128 dims 86 us, 71%), by the latencies of a
+// step's instructions (three warps a partition) for more: 24 rows of 64 x 4096
+// 164 us (75%), 8-bit 153 us (40%), which is why long 8-bit contexts go to tensor
+// memory.  8-bit rows of 64 dims hold half the bytes for the same conversions a
+// step: 64 x 4096 65 us of one token (49%), 108 us of 24 rows (29%).  One sequence of 512 keys and 24 rows takes 9 us, most of it the
 // start, one walk of a few steps and two merges.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -78,9 +80,9 @@ struct PaLayout {
   static constexpr int q_bytes = NT * 8 * HD * 2;    // Q in operand order: 16 bytes a lane hold two k slices
   // Blocks on an SM: as many as the accumulators allow (NT = 4: 128 of them),
   // more where steps are small and rows few, so that their copies leave room
-  // (64 x 4096 keys of one token, 8-bit head dim 128: 3 blocks 96 us, 4 84, 5 80;
-  // 16-bit head dim 64: 74, 67, 65; 8-bit head dim 64, whose ring is full with 4:
-  // 61, 61, 63).
+  // (64 x 4096 keys of one token, 8-bit head dim 128: 3 blocks 100 us, 4 87, 5 86;
+  // 16-bit head dim 64: 75, 70, 68; 8-bit head dim 64, whose ring is full with 4:
+  // 65, 65, 67).
   static constexpr int blocks = NT == 4 && HD >= 128 ? 2 : NT > 2 || stage >= 5000 ? 3 : NT == 1 && stage > 3000 ? 5 : 4;
   static constexpr int room = (blocks == 2 ? 112 : blocks == 3 ? 74 : blocks == 4 ? 55 : 44) * 1024 - q_bytes;
   static constexpr int fit = room / (kPaWarps * stage);
@@ -603,12 +605,12 @@ bool row_aligned(const void* p, int64_t ts, int64_t hs) {
 // rows and dims where (sequence, KV head, tile) items are so few that the register
 // tiles' clusters of eight blocks do not cover the SMs.  The lengths being on the
 // device, a table's width stands for them.  Register tiles / this, us, 8 KV heads.
-// 24 rows, head dim 128: 64 sequences x 4096 keys 151 / 116, x 2048 90 / 79,
-// x 1024 56 / 63; 16 x 4096 54 / 43, x 2048 31 / 33; 4 x 8192
-// 33 / 30, x 4096 21 / 24; 1 x 8192 27 / 25, x 4096 18 / 24, x 65536 152 / 52.  16
-// rows, 64 x 4096: 103 / 110, with pages of 64 106 / 93, 16 x 4096 36 / 39; 2 x
-// 16384 43 / 30.  4 rows: 64 x 4096 80 / 113, 1 x 16384 28 / 24, 2 x 16384 31 / 30.
-// 24 rows, head dim 64: 64 x 4096 105 / 104, 4 x 8192 23 / 26, 1 x 16384 32 / 26.
+// 24 rows, head dim 128: 64 sequences x 4096 keys 153 / 116, x 2048 92 / 79,
+// x 1024 56 / 63; 16 x 4096 49 / 43, x 2048 32 / 34; 4 x 8192
+// 33 / 30, x 4096 23 / 26; 1 x 8192 28 / 26, x 4096 18 / 24, x 65536 147 / 52.  16
+// rows, 64 x 4096: 111 / 112, with pages of 64 114 / 91, 16 x 4096 39 / 39; 2 x
+// 16384 43 / 30.  4 rows: 64 x 4096 86 / 114, 1 x 16384 29 / 25, 2 x 16384 33 / 30.
+// 24 rows, head dim 64: 64 x 4096 108 / 104, 4 x 8192 25 / 27, 1 x 16384 33 / 28.
 size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
   if (!a.paged || rows < 1 || rows > kPaMaxRows || !pattn_td_supported(a)) return 0;
   const int64_t keys = (int64_t)a.max_pages << a.page_shift, items = (int64_t)a.seqs * a.hkv * ((rows + 31) / 32);
@@ -627,10 +629,12 @@ size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
 // them once for all rows: it is taken where (sequence, KV head) pairs keep its
 // blocks busy, at head dim 64 only from 49 rows and 16-bit keys on.  Measured,
 // tensor memory against register tiles, 4096 keys, 8 KV heads, head dim 128:
-// 64 rows of 16 sequences 60 / 74 us (8-bit keys 83 / 89), of 8 sequences
-// 39 / 47 (49 / 54), of 4 36 / 30; 36 rows of 16 sequences 60 / 77 (83 / 92),
-// of 12 60 / 52.  Head dim 64: 64 rows of 16 sequences 44 / 57 (70 / 70), of
-// 12 44 / 39; 36 rows of 64 sequences 121 / 113 (197 / 156).  A batch with
+// 64 rows of 16 sequences 61 / 75 us (8-bit keys 76 / 93), of 8 sequences
+// 39 / 47 (45 / 56), of 4 37 / 31; 36 rows of 16 sequences 60 / 78 (76 / 94),
+// of 12 60 / 52.  Head dim 64: 64 rows of 16 sequences 44 / 57 (67 / 72), of
+// 12 44 / 39; 36 rows of 64 sequences 122 / 114 (191 / 160).  (The few-rows kernel
+// takes 72 us for those 64 rows of 16 sequences of 8-bit keys, 62 for the 36, and
+// 205 / 217 for 36 rows of 64 sequences: it is not asked here.)  A batch with
 // both kinds goes whole: a short sequence costs the tensor-memory kernel one
 // tile's walk over the keys beside the long ones, less than a second launch
 // behind them.

@@ -45,11 +45,15 @@
 // With few items (chunks of a few sequences) a cluster of two blocks shares an
 // item's keys; block t finishes tile t with the other's sums, read from its
 // shared memory.
-// Bound by the tensor pipe, 64 rounds of exponentials next to it and the causal
-// triangle's ragged ends.  Measured at head dim 128, 32 heads on 8: six packed
-// prompts of 4096 276 us (1.31 PFLOP/s, 69% of the library product's rate), one
-// of 16384 1253 us (93%), 16 of 1024 142 us; four chunks of up to 512 tokens over
-// 16384 keys 164 us (1.1 PFLOP/s); head dim 64, four of 4096 297 us.
+// Bound by the tensor pipe where walks are long, and by a fixed 4 to 5 us an item
+// (the softmax warps also drain, scale and store O before their next item): at 64
+// steps an item takes 1.4 us a step, at 4.5 steps 10 us.  8-bit keys add the
+// conversion of both tiles by four warps.  Measured at head dim 128, 32 heads on 8:
+// six packed prompts of up to 4096 276 us (1.31 PFLOP/s, 69% of the library
+// product's rate), one of 16384 1260 to 1300 us (90%), 16 of 1024 139 us (52%);
+// four chunks of up to 512 tokens over up to 16384 keys 164 us (1.1 PFLOP/s), four
+// of 512 over 16384 364 us (78%), with 8-bit keys 514 us (56%); head dim 64, four
+// prompts of 4096 349 us (42%).
 #include <cuda_runtime.h>
 
 #include <algorithm>

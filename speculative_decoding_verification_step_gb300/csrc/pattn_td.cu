@@ -33,11 +33,11 @@
 // Bound by the softmax warps' latencies (1500 clocks a unit of 16 rows, 1800 of
 // 24, 2000 of 32; the next unit's scores loaded early cost registers and were 4%
 // slower, two units a pass 40%, a second softmax group with half of the rows 7%),
-// by the copies of small pages next to them (16 rows over pages of 16 110 us, of
-// 64 93) and by 5 us at the ends of a tile.  Measured (8 KV
+// by the copies of small pages next to them (16 rows over pages of 16 112 us, of
+// 64 91) and by 5 us at the ends of a tile.  Measured (8 KV
 // heads, head dim 128, 24 rows) against the register-tile kernel: 64 x 4096 keys
-// 116 / 152 us (3.5 TB/s), 16 x 16384 116 / 169, 16 x 4096 43 / 54, 1 x 16384
-// 28 / 46, 1 x 65536 52 / 152.
+// 116 / 153 us (3.5 TB/s), 16 x 16384 115 / 140, 16 x 4096 43 / 49, 1 x 16384
+// 29 / 45, 1 x 65536 52 / 147.
 #include <cuda_runtime.h>
 
 #include <algorithm>
