@@ -496,15 +496,15 @@ def _index(name, t, n, dev):
         _refuse(f"{name}: a contiguous int32 tensor of {n} on the rows' device")
 
 
-def _empty(shape, dtype, device, stream):
-    """A tensor from the memory of the stream that the call runs on: the current
-    stream's may still be in use by work queued there."""
-    if stream is None:
-        return _t.empty(shape, dtype=dtype, device=device)
+def _alloc(stream, device, make):
+    """make()'s tensors from the memory of the stream that the call runs on: the
+    current stream's may still be in use by work queued there."""
+    if stream is None or stream == _t._C._cuda_getCurrentRawStream(device.index):
+        return make()
     # (handle 0 is the default stream, of which ExternalStream makes another)
     own = _t.cuda.ExternalStream(stream, device=device) if stream else _t.cuda.default_stream(device)
     with _t.cuda.stream(own):
-        return _t.empty(shape, dtype=dtype, device=device)
+        return make()
 
 
 def _call(dev, stream, fn, *args):
@@ -610,7 +610,7 @@ def rope_rows(x, pos, plan, out=None, dtype=None, inverse=False, stream=None):
     dev = x.get_device()
     _index("pos", pos, n, dev)
     if out is None:
-        out = _empty(shape, x.dtype if dtype is None else dtype, x.device, stream)
+        out = _alloc(stream, x.device, lambda: _t.empty(shape, dtype=x.dtype if dtype is None else dtype, device=x.device))
         ys = out.stride()
     else:
         if out.shape != shape or out.get_device() != dev or (dtype is not None and dtype is not out.dtype):
@@ -649,25 +649,30 @@ def kv_gather(cache, seq, pos, dtype=None, stream=None):
     shape = (n, cache.n_kv_heads, cache.head_dim)
     if dtype is None:
         dtype = _t.bfloat16
-    k, v = (_empty(shape, dtype, cache.device, stream) for _ in range(2))
+    where = cache.device
+    k, v = _alloc(stream, where, lambda: (_t.empty(shape, dtype=dtype, device=where),
+                                          _t.empty(shape, dtype=dtype, device=where)))
     _call(dev, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
           v.data_ptr(), _io_dtype(k))
     return k, v
 
 
-def _attn_out(q, shape, dev, out, lse, stream):
+def _attn_out(q, shape, dev, out, lse, need, stream):
+    """The call's out, lse and workspace of `need` bytes, checked or new."""
     if q.dtype is not _t.bfloat16:
         _refuse(f"q is bf16, not {q.dtype}")
-    if out is None:
-        out = _empty(shape, _t.bfloat16, q.device, stream)
-    elif out.shape != shape or out.dtype is not _t.bfloat16 or out.get_device() != dev:
+    if out is not None and (out.shape != shape or out.dtype is not _t.bfloat16 or out.get_device() != dev):
         _refuse("out: like q")
-    if lse is None:
-        lse = _empty(shape[:2], _t.float32, q.device, stream)
-    elif lse is not False and (lse.shape != shape[:2] or lse.dtype is not _t.float32 or lse.get_device() != dev or
+    if lse is not None and lse is not False and (lse.shape != shape[:2] or lse.dtype is not _t.float32 or lse.get_device() != dev or
                                not lse.is_contiguous()):
         _refuse("lse: contiguous fp32 [tokens, heads]")
-    return out, lse
+    if out is not None and lse is not None and not need:
+        return out, lse, None
+    where = q.device
+    return _alloc(stream, where, lambda: (
+        _t.empty(shape, dtype=_t.bfloat16, device=where) if out is None else out,
+        _t.empty(shape[:2], dtype=_t.float32, device=where) if lse is None else lse,
+        _t.empty(need, dtype=_t.uint8, device=where) if need else None))
 
 
 def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=None, stream=None):
@@ -686,8 +691,6 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
         _refuse("q must have the cache's head_dim and device")
     _index("cu_q", cu_q, seqs + 1, dev)
     _index("kv_lens", kv_lens, seqs, dev)
-    out, lse = _attn_out(q, shape, dev, out, lse, stream)
-    os_ = _rows3("out", out)
     if max_q is None:
         max_q = n
     key = n, max_q, h
@@ -698,7 +701,8 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
         if len(cache._ws) > 4096:
             cache._ws.clear()
         cache._ws[key] = need
-    ws = _empty(need, _t.uint8, q.device, stream) if need else None
+    out, lse, ws = _attn_out(q, shape, dev, out, lse, need, stream)
+    os_ = _rows3("out", out)
     _call(dev, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
           kv_lens.data_ptr(), n, max_q, h, scale, out.data_ptr(), os_[0], os_[1],
           lse.data_ptr() if lse is not False else None, ws.data_ptr() if need else None, need)
@@ -724,7 +728,7 @@ def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream
     if seqs < 1:
         _refuse("cu: int32 [sequences + 1]")
     _index("cu", cu, seqs + 1, dev)
-    out, lse = _attn_out(q, shape, dev, out, lse, stream)
+    out, lse, _ = _attn_out(q, shape, dev, out, lse, 0, stream)
     os_ = _rows3("out", out)
     _call(dev, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
           v.data_ptr(), vs[0], vs[1], cu.data_ptr(), seqs, n, n if max_len is None else max_len, h, kshape[1], d,
