@@ -437,9 +437,10 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * out may not overlap the inputs.
  * scale >= 0, finite also times log2(e); 0: 1/sqrt(head_dim).  Scores, softmax
  * statistics and sums are fp32 (rows with scores past 2^29 mean nothing),
- * probabilities bf16 in the product with v; over an e4m3 cache, whose rows' powers of two should lie within 2^+-90 (the
- * products of others may leave fp32's or bf16's normal range), elements of q
- * below 2^-10 of their row's largest may be rounded by up to 2^-17 of that.
+ * probabilities bf16 in the product with v.  Over an e4m3 cache elements of q
+ * below 2^-10 of their row's largest may be rounded by up to 2^-17 of that, and
+ * rows' powers of two should lie within 2^+-90 (products of others may leave
+ * fp32's or bf16's normal range).
  * Cache slots past a sequence's length are never used, whatever they hold; a
  * value row that is not finite within the length reaches the outputs of the
  * whole chunk.  Every wait inside the kernels is bounded; should one run out, the
