@@ -430,10 +430,11 @@ SPEC_API int spec_kv_gather(const spec_kv_cache* cache, const int32_t* seq, cons
  * 0 .. kv_lens[b] - n + i; query head h reads KV head h * n_kv_heads /
  * n_heads.  out: bf16 like q with its own strides; lse (may be NULL): fp32
  * [tokens][n_heads], the log of the row's sum of exp(scale * q.k).  A row
- * that sees nothing (or scores of -inf only) gets zeros and lse -inf.  Rows outside every sequence, and
- * rows past a sequence's first max_q (a bound on the chunks' lengths, sizing
- * the grid), are left as they were.  A length past the table's positions is cut
- * there; a table entry that is not a page of the pool reads as zero rows.
+ * that sees nothing (or scores of -inf only) gets zeros and lse -inf.  Rows
+ * outside every sequence, and rows past a sequence's first max_q (a bound on the
+ * chunks' lengths, sizing the grid), are left as they were.  A length past the
+ * table's positions is cut there; a table entry that is not a page of the pool
+ * reads as zero rows.
  * out may not overlap the inputs.
  * scale >= 0, finite also times log2(e); 0: 1/sqrt(head_dim).  Scores, softmax
  * statistics and sums are fp32 (rows with scores past 2^29 mean nothing),
