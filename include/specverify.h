@@ -414,6 +414,61 @@ SPEC_API int spec_kv_append(const spec_kv_cache* cache, const void* k, int64_t k
                    const void* v, int64_t v_tok_stride, int64_t v_head_stride, int dtype,
                    const int32_t* seq, const int32_t* pos, int tokens, const spec_rope* plan, void* stream);
 
+/* The whole of a layer's rows behind its q/k/v projection in one launch: q
+ * [tokens][n_heads][head_dim], normed per head and rotated, to q_out (bf16);
+ * k, normed and rotated, and v to the cache as spec_kv_append writes them.  The
+ * norm of a head is x * gain / sqrt(mean(x^2) + eps) over its head_dim elements,
+ * the rotation comes behind it; both in fp32 (a sum of squares that leaves its
+ * range makes the row zero or NaN), one rounding.  q_gain, k_gain: fp32 [head_dim]
+ * (device), NULL: no norm.  plan NULL: no rotation.  dtype is that of q, k and v.
+ * q_out may be q (bf16, equal strides), and overlaps nothing else.  A token that
+ * spec_kv_append skips still gets its row of q_out. */
+SPEC_API int spec_qkv_append(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const void* k, int64_t k_tok_stride, int64_t k_head_stride, const void* v, int64_t v_tok_stride,
+                    int64_t v_head_stride, int dtype, const int32_t* seq, const int32_t* pos, int tokens, int n_heads,
+                    const spec_rope* plan, const float* q_gain, const float* k_gain, float eps, void* q_out,
+                    int64_t out_tok_stride, int64_t out_head_stride, void* stream);
+
+/* spec_rope_rows behind the same norm of each head: y[t][h] = R(pos[t]) [x[t][h] *
+ * gain[h] / sqrt(mean + eps)], the mean over all head_dim elements, rotated ones
+ * or not.  gain: fp32, gain_head_stride elements between heads (0: one for all;
+ * the q and k heads of a fused projection are one call with a gain each).
+ * head_dim: even, 2..512. */
+SPEC_API int spec_rope_norm_rows(const void* x, int x_dtype, int64_t x_tok_stride, int64_t x_head_stride,
+                        void* y, int y_dtype, int64_t y_tok_stride, int64_t y_head_stride,
+                        const int32_t* pos, int tokens, int heads, int head_dim, const float* gain,
+                        int64_t gain_head_stride, float eps, const spec_rope* plan, void* stream);
+
+/* Pages and index arrays of a step.  A sequence of length L holds the first
+ * ceil(L / page_size) entries of its row of the table; pages that no sequence
+ * holds lie in a stack: free_pages[0 .. *n_free - 1] of a device array of
+ * free_cap entries (*n_free outside 0..free_cap counts as the nearer end).
+ *
+ * spec_kv_reserve: sequence b asks for counts[b] new tokens (negative: none) behind
+ * its kv_lens[b] positions.  In order, over the requests that the table has room
+ * for (0 <= kv_lens[b], new length <= max_pages * page_size), one is served
+ * whole if the pages asked for up to it are within the stack's (or it needs
+ * none) and the tokens up to it within `tokens`; else it gets nothing.  Writes
+ * the table's new entries (the i-th page needed is the i-th from the top),
+ * *n_free, the new lengths, cu_q [seqs + 1], of every token its sequence and
+ * position (seq, pos [tokens]; -1 past the last token, which the row calls
+ * skip), and *lacking, the pages asked for beyond the stack's (0: none).
+ * kv_lens_out must not overlap kv_lens.
+ *
+ * spec_kv_release: sequence b keeps the first keep[b] of its kv_lens[b] positions
+ * (both cut to 0 .. the table's room, keep to the length); the pages past them
+ * go back to the stack in order of sequences and positions, and their entries
+ * become -1.  A page that several rows name (a shared prefix) must not be
+ * dropped by more than one of them.  What the stack has no room for is lost.
+ *
+ * The cache's pools are not touched.  Both read and write n_free, the stack and
+ * the table in place: calls on one cache go one behind the other. */
+SPEC_API int spec_kv_reserve(const spec_kv_cache* cache, const int32_t* kv_lens, const int32_t* counts,
+                    int32_t* free_pages, int32_t* n_free, int free_cap, int tokens, int32_t* cu_q,
+                    int32_t* kv_lens_out, int32_t* seq, int32_t* pos, int32_t* lacking, void* stream);
+SPEC_API int spec_kv_release(const spec_kv_cache* cache, const int32_t* kv_lens, const int32_t* keep,
+                    int32_t* free_pages, int32_t* n_free, int free_cap, void* stream);
+
 /* Read rows back: position pos[t] of sequence seq[t] to k_out and v_out (fp32
  * or bf16 [tokens][n_kv_heads][head_dim], packed; either may be NULL).  The
  * value of an e4m3 row is exact in both (past a type's largest number infinite,

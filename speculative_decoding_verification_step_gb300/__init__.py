@@ -15,7 +15,8 @@ from ._build import LIB, build
 __all__ = ["build", "lib", "SpecError", "SpecDecoder", "accept_rows", "sample_rows",
            "SPEC_DTYPE_F32", "SPEC_DTYPE_BF16", "SPEC_OPT_NO_GRAPH", "SPEC_OPT_TIMING",
            "SPEC_FLAG_RESID_ZERO", "SPEC_FLAG_ALL_ACCEPTED", "KVCache", "rope_plan", "rope_rows",
-           "kv_append", "kv_gather", "attn_paged", "attn_prompt"]
+           "kv_append", "kv_gather", "attn_paged", "attn_prompt", "rope_norm_rows", "qkv_append", "kv_reserve",
+           "kv_release"]
 
 SPEC_OK = 0
 ERRORS = {-1: "SPEC_E_ARG", -2: "SPEC_E_VOCAB", -3: "SPEC_E_SHAPE", -4: "SPEC_E_CAPACITY",
@@ -148,6 +149,12 @@ SIGNATURES = {
                                       _VP, _INT, _VP]),
     "spec_kv_append": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _INT, _VP, _VP, _INT, _VP, _VP]),
     "spec_kv_gather": (ctypes.c_int, [_VP, _VP, _VP, _INT, _VP, _VP, _INT, _VP]),
+    "spec_qkv_append": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _INT, _VP, _VP, _INT,
+                                       _INT, _VP, _VP, _VP, ctypes.c_float, _VP, _I64, _I64, _VP]),
+    "spec_rope_norm_rows": (ctypes.c_int, [_VP, _INT, _I64, _I64, _VP, _INT, _I64, _I64, _VP, _INT, _INT, _INT,
+                                           _VP, _I64, ctypes.c_float, _VP, _VP]),
+    "spec_kv_reserve": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _INT, _INT, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "spec_kv_release": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _INT, _VP]),
     "spec_attn_paged": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _VP, _INT, _INT, _INT, ctypes.c_float,
                                        _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
     "spec_attn_paged_workspace": (ctypes.c_int64, [_VP, _INT, _INT, _INT]),
@@ -655,6 +662,122 @@ def kv_gather(cache, seq, pos, dtype=None, stream=None):
     _call(dev, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
           v.data_ptr(), _io_dtype(k))
     return k, v
+
+
+def _gain(name, t, shape, dev):
+    if t.dtype is not _t.float32 or t.shape != shape or t.get_device() != dev or t.stride(-1) != 1:
+        _refuse(f"{name}: fp32 {list(shape)} on the rows' device")
+    if t.requires_grad and _t.is_grad_enabled():
+        _refuse(f"{name} requires grad, and the call has no backward pass: detach it, or call under torch.no_grad()")
+
+
+def rope_norm_rows(x, pos, plan, gain, eps=1e-5, out=None, dtype=None, stream=None):
+    """rope_rows behind an RMS norm of each head: x * gain / sqrt(mean(x^2) +
+    eps) over head_dim, then rotated.  gain: fp32 [head_dim], or [heads,
+    head_dim] for a gain of each head (the q and k heads of one projection)."""
+    _torch()
+    xs = _rows3("x", x)
+    shape = x.shape
+    n, h, d = shape
+    dev = x.get_device()
+    _index("pos", pos, n, dev)
+    _gain("gain", gain, shape[2:] if gain.dim() == 1 else shape[1:], dev)
+    if out is None:
+        out = _alloc(stream, x.device, lambda: _t.empty(shape, dtype=x.dtype if dtype is None else dtype, device=x.device))
+        ys = out.stride()
+    else:
+        if out.shape != shape or out.get_device() != dev or (dtype is not None and dtype is not out.dtype):
+            _refuse("out: x's shape and device")
+        ys = _rows3("out", out)
+    _call(dev, stream, lib().spec_rope_norm_rows, x.data_ptr(), _io_dtype(x), xs[0], xs[1], out.data_ptr(),
+          _io_dtype(out), ys[0], ys[1], pos.data_ptr(), n, h, d, gain.data_ptr(),
+          gain.stride(0) if gain.dim() == 2 else 0, eps, plan._ref)
+    return out
+
+
+def qkv_append(cache, q, k, v, seq, pos, plan=None, q_norm=None, k_norm=None, eps=1e-5, out=None, stream=None):
+    """A layer's rows behind its q/k/v projection in one launch: the heads of q
+    [tokens, n_heads, head_dim] and k [tokens, n_kv_heads, head_dim] normed
+    (fp32 gains [head_dim], if given) and rotated (plan, if given), q returned
+    in bf16 (out, given or new; may be q itself), k and v written to positions
+    pos of sequences seq as kv_append does."""
+    _torch()
+    qs, ks, vs = _rows3("q", q), _rows3("k", k), _rows3("v", v)
+    qshape, shape, dev = q.shape, k.shape, cache._dev
+    n, h, d = shape
+    if v.shape != shape or k.dtype is not v.dtype or h != cache.n_kv_heads or d != cache.head_dim:
+        _refuse("k and v: equal [tokens, n_kv_heads, head_dim] of the cache")
+    if qshape[0] != n or qshape[2] != d or q.dtype is not k.dtype:
+        _refuse("q: the tokens, head_dim and type of k")
+    if q.get_device() != dev or k.get_device() != dev or v.get_device() != dev:
+        _refuse("q, k, v and the cache must be on one device")
+    _index("seq", seq, n, dev)
+    _index("pos", pos, n, dev)
+    for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if g is not None:
+            _gain(name, g, shape[2:], dev)
+    if out is None:
+        out = _alloc(stream, cache.device, lambda: _t.empty(qshape, dtype=_t.bfloat16, device=cache.device))
+        os_ = out.stride()
+    else:
+        if out.shape != qshape or out.dtype is not _t.bfloat16 or out.get_device() != dev:
+            _refuse("out: bf16 of q's shape and device")
+        os_ = _rows3("out", out)
+    _call(dev, stream, lib().spec_qkv_append, cache._ref, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+          v.data_ptr(), vs[0], vs[1], _io_dtype(k), seq.data_ptr(), pos.data_ptr(), n, qshape[1],
+          plan._ref if plan is not None else None, q_norm.data_ptr() if q_norm is not None else None,
+          k_norm.data_ptr() if k_norm is not None else None, eps, out.data_ptr(), os_[0], os_[1])
+    return out
+
+
+def _stack(cache, free, n_free):
+    if free.dim() != 1:
+        _refuse("free: a contiguous int32 tensor of page numbers")
+    _index("free", free, free.shape[0], cache._dev)
+    _index("n_free", n_free, 1, cache._dev)
+
+
+def kv_reserve(cache, kv_lens, counts, free, n_free, tokens, stream=None):
+    """Pages and index arrays of counts[b] new tokens of every sequence b
+    (int32 [seqs]) behind its kv_lens[b] positions: takes the pages from the
+    stack free[: n_free] (int32, n_free int32 [1]; both changed in place), writes
+    them into the cache's table, and returns (cu_q [seqs + 1], kv_lens with the
+    new tokens [seqs], seq [tokens], pos [tokens], lacking [1]), as the row and
+    attention calls take them; `tokens` bounds the step's tokens, and entries
+    past them are -1.  Requests are served in order and whole; one that does
+    not fit gets nothing (its length is as before), and lacking counts the
+    pages that were missing."""
+    _torch()
+    dev, seqs = cache._dev, cache.seqs
+    _index("kv_lens", kv_lens, seqs, dev)
+    _index("counts", counts, seqs, dev)
+    _stack(cache, free, n_free)
+    if tokens < 0:
+        _refuse("tokens: a bound on the step's tokens")
+    up = (seqs + 4) & ~3, (tokens + 3) & ~3            # one allocation, its parts on 16-byte boundaries
+    buf = _alloc(stream, cache.device, lambda: _t.empty(2 * up[0] + 2 * up[1] + 4, dtype=_t.int32, device=cache.device))
+    at = buf.data_ptr()
+    cu, lens = buf[:seqs + 1], buf[up[0]:up[0] + seqs]
+    o = 2 * up[0]
+    seq, pos, lacking = buf[o:o + tokens], buf[o + up[1]:o + up[1] + tokens], buf[o + 2 * up[1]:o + 2 * up[1] + 1]
+    _call(dev, stream, lib().spec_kv_reserve, cache._ref, kv_lens.data_ptr(), counts.data_ptr(), free.data_ptr(),
+          n_free.data_ptr(), free.shape[0], tokens, at, at + 4 * up[0], at + 4 * o, at + 4 * (o + up[1]),
+          at + 4 * (o + 2 * up[1]))
+    return cu, lens, seq, pos, lacking
+
+
+def kv_release(cache, kv_lens, keep, free, n_free, stream=None):
+    """The pages of positions keep[b] .. kv_lens[b] - 1 of every sequence b
+    (int32 [seqs]: the lengths with the tokens that are dropped, and without)
+    back to the stack free[: n_free]; their entries of the table become -1.  A
+    page that several sequences name must not be dropped by more than one."""
+    _torch()
+    dev = cache._dev
+    _index("kv_lens", kv_lens, cache.seqs, dev)
+    _index("keep", keep, cache.seqs, dev)
+    _stack(cache, free, n_free)
+    _call(dev, stream, lib().spec_kv_release, cache._ref, kv_lens.data_ptr(), keep.data_ptr(), free.data_ptr(),
+          n_free.data_ptr(), free.shape[0])
 
 
 def _attn_out(q, shape, dev, out, lse, need, stream):
