@@ -527,6 +527,48 @@ SPEC_API int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_hea
                      int n_heads, int n_kv_heads, int head_dim, float scale, void* out,
                      int64_t out_tok_stride, int64_t out_head_stride, float* lse, void* stream);
 
+/* The same attention with a sliding window: the row at position p sees position j <= p
+ * if j > p - window or j < sinks (the first tokens stay visible); window 0: all
+ * of them.  Positions that no row of the call's chunk sees are not read where
+ * whole pages (or a tile's rows) of them lie together, so their table entries need
+ * not name pages that hold them any more; what else such a slot holds never
+ * reaches an output.  The rest as for spec_attn_paged (which has no use for a
+ * workspace here, NULL) and spec_attn_prompt. */
+SPEC_API int spec_attn_paged_window(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const int32_t* cu_q, const int32_t* kv_lens, int tokens, int max_q, int n_heads,
+                    float scale, int window, int sinks, void* out, int64_t out_tok_stride, int64_t out_head_stride,
+                    float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+SPEC_API int spec_attn_prompt_window(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* k,
+                     int64_t k_tok_stride, int64_t k_head_stride, const void* v, int64_t v_tok_stride,
+                     int64_t v_head_stride, const int32_t* cu, int seqs, int tokens, int max_len,
+                     int n_heads, int n_kv_heads, int head_dim, float scale, int window, int sinks, void* out,
+                     int64_t out_tok_stride, int64_t out_head_stride, float* lse, void* stream);
+
+/* spec_attn_paged for sequences whose rows of the table name the same pages at their
+ * beginning (a shared prompt): those positions are read once for all of them.
+ * Group g is the sequences groups[g] .. groups[g+1] - 1 (device int32 [n_groups +
+ * 1], ascending; NULL with n_groups 1: all), and the caller says that their rows
+ * of the table name the same pages for the first shared[g] positions (device int32;
+ * any number, it need not end with a page and is cut to what every row of the group
+ * sees).  Sequences outside every group share nothing.  The result is that
+ * of spec_attn_paged, some roundings apart: the sums over the prefix and over the
+ * rest of a row are fp32 and joined in fp32.  Which row of the table the prefix
+ * is read by is not said, so where the rows name other pages the result is neither's.
+ * Groups or cu_q out of order give rows without meaning, and no access outside
+ * the buffers.  A value row that is not finite within the prefix reaches
+ * the rows of the whole group.
+ * workspace as for spec_attn_paged; with fewer bytes than
+ * spec_attn_shared_workspace says, and where sharing does not pay (more than 64
+ * rows max_q * n_heads / n_kv_heads, head_dim 32, few or short sequences),
+ * nothing is shared and the call is spec_attn_paged. */
+SPEC_API int spec_attn_shared(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const int32_t* cu_q, const int32_t* kv_lens, const int32_t* groups, int n_groups,
+                    const int32_t* shared, int tokens, int max_q, int n_heads, float scale, void* out,
+                    int64_t out_tok_stride, int64_t out_head_stride, float* lse, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+SPEC_API int64_t spec_attn_shared_workspace(const spec_kv_cache* cache, int n_groups, int tokens, int max_q,
+                    int n_heads);
+
 /* Phase timing of the step as run in production (CUDA graphs, CUDA events
  * on the context's stream), averaged over `iters` replays after two
  * warm-up replays: the draft loop (K draft passes + samplers), the verify

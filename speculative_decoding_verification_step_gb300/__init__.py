@@ -15,8 +15,8 @@ from ._build import LIB, build
 __all__ = ["build", "lib", "SpecError", "SpecDecoder", "accept_rows", "sample_rows",
            "SPEC_DTYPE_F32", "SPEC_DTYPE_BF16", "SPEC_OPT_NO_GRAPH", "SPEC_OPT_TIMING",
            "SPEC_FLAG_RESID_ZERO", "SPEC_FLAG_ALL_ACCEPTED", "KVCache", "rope_plan", "rope_rows",
-           "kv_append", "kv_gather", "attn_paged", "attn_prompt", "rope_norm_rows", "qkv_append", "kv_reserve",
-           "kv_release"]
+           "kv_append", "kv_gather", "attn_paged", "attn_prompt", "attn_shared", "rope_norm_rows", "qkv_append",
+           "kv_reserve", "kv_release"]
 
 SPEC_OK = 0
 ERRORS = {-1: "SPEC_E_ARG", -2: "SPEC_E_VOCAB", -3: "SPEC_E_SHAPE", -4: "SPEC_E_CAPACITY",
@@ -160,6 +160,14 @@ SIGNATURES = {
     "spec_attn_paged_workspace": (ctypes.c_int64, [_VP, _INT, _INT, _INT]),
     "spec_attn_prompt": (ctypes.c_int, [_VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _INT, _INT,
                                         _INT, _INT, _INT, _INT, ctypes.c_float, _VP, _I64, _I64, _VP, _VP]),
+    "spec_attn_paged_window": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _VP, _INT, _INT, _INT, ctypes.c_float,
+                                              _INT, _INT, _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
+    "spec_attn_prompt_window": (ctypes.c_int, [_VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _INT, _INT,
+                                               _INT, _INT, _INT, _INT, ctypes.c_float, _INT, _INT, _VP, _I64, _I64,
+                                               _VP, _VP]),
+    "spec_attn_shared": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _VP, _VP, _INT, _VP, _INT, _INT, _INT,
+                                        ctypes.c_float, _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
+    "spec_attn_shared_workspace": (ctypes.c_int64, [_VP, _INT, _INT, _INT, _INT]),
     "spec_profile": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.POINTER(Profile)]),
     "spec_phase_times": (ctypes.c_int, [_VP, ctypes.c_int, _VP, ctypes.c_int,
                                         ctypes.POINTER(ctypes.c_int)]),
@@ -798,32 +806,52 @@ def _attn_out(q, shape, dev, out, lse, need, stream):
         _t.empty(need, dtype=_t.uint8, device=where) if need else None))
 
 
-def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=None, stream=None):
+def _paged_args(q, cache, cu_q, kv_lens):
+    """(strides, shape, device) of an attention call over the cache."""
+    qs = _rows3("q", q)
+    shape, dev, seqs = q.shape, cache._dev, cache.seqs
+    if shape[2] != cache.head_dim or q.get_device() != dev:
+        _refuse("q must have the cache's head_dim and device")
+    _index("cu_q", cu_q, seqs + 1, dev)
+    _index("kv_lens", kv_lens, seqs, dev)
+    return qs, shape, dev
+
+
+def _ws_bytes(cache, key, dev, ask):
+    """Workspace bytes of a call by its sizes (key), a function of them alone."""
+    need = cache._ws.get(key)
+    if need is None:
+        with _t.cuda.device(dev):
+            need = ask()
+        if len(cache._ws) > 4096:
+            cache._ws.clear()
+        cache._ws[key] = need
+    return need
+
+
+def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=None, stream=None, window=0, sinks=0):
     """Causal attention of the sequences' newest tokens over the cache.  q
     [tokens, n_heads, head_dim] bf16; sequence b (row b of the cache's table)
     owns rows cu_q[b] .. cu_q[b+1]-1 and kv_lens[b] cached positions, its new
     ones included (int32 [seqs + 1], [seqs]); max_q bounds the rows of one
     sequence and goes into the choice of kernel (default: tokens; give the
-    real bound for batches).  Returns (out, lse [tokens, n_heads] fp32, or
-    None with lse=False); rows outside every sequence are not written."""
+    real bound for batches).  window > 0: the row at position p sees positions
+    j <= p with j > p - window or j < sinks.  Returns (out, lse [tokens,
+    n_heads] fp32, or None with lse=False); rows outside every sequence are
+    not written."""
     _torch()
-    qs = _rows3("q", q)
-    shape, dev, seqs = q.shape, cache._dev, cache.seqs
+    qs, shape, dev = _paged_args(q, cache, cu_q, kv_lens)
     n, h, d = shape
-    if d != cache.head_dim or q.get_device() != dev:
-        _refuse("q must have the cache's head_dim and device")
-    _index("cu_q", cu_q, seqs + 1, dev)
-    _index("kv_lens", kv_lens, seqs, dev)
     if max_q is None:
         max_q = n
-    key = n, max_q, h
-    need = cache._ws.get(key)                # a function of the sizes alone
-    if need is None:
-        with _t.cuda.device(dev):
-            need = lib().spec_attn_paged_workspace(cache._ref, n, max_q, h)
-        if len(cache._ws) > 4096:
-            cache._ws.clear()
-        cache._ws[key] = need
+    if window or sinks:
+        out, lse, _ = _attn_out(q, shape, dev, out, lse, 0, stream)
+        os_ = _rows3("out", out)
+        _call(dev, stream, lib().spec_attn_paged_window, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
+              kv_lens.data_ptr(), n, max_q, h, scale, min(window, 0x7fffffff), min(sinks, 0x7fffffff),
+              out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None, None, 0)
+        return out, (lse if lse is not False else None)
+    need = _ws_bytes(cache, (n, max_q, h), dev, lambda: lib().spec_attn_paged_workspace(cache._ref, n, max_q, h))
     out, lse, ws = _attn_out(q, shape, dev, out, lse, need, stream)
     os_ = _rows3("out", out)
     _call(dev, stream, lib().spec_attn_paged, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
@@ -832,11 +860,40 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
     return out, (lse if lse is not False else None)
 
 
-def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream=None):
+def attn_shared(q, cache, cu_q, kv_lens, shared, groups=None, max_q=None, scale=0.0, out=None, lse=None, stream=None):
+    """attn_paged for sequences whose rows of the cache's table name the same
+    pages at their beginning: the first shared[g] positions (int32 [groups]) of
+    the sequences groups[g] .. groups[g+1]-1 (int32 [groups + 1]; default: one
+    group of all) are read once for the group.  Any number of positions; it is
+    cut to what every row of the group sees."""
+    _torch()
+    qs, shape, dev = _paged_args(q, cache, cu_q, kv_lens)
+    n, h, d = shape
+    ng = 1 if groups is None else groups.shape[0] - 1 if groups.dim() == 1 else 0
+    if ng < 1:
+        _refuse("groups: int32 [groups + 1]")
+    if groups is not None:
+        _index("groups", groups, ng + 1, dev)
+    _index("shared", shared, ng, dev)
+    if max_q is None:
+        max_q = n
+    need = _ws_bytes(cache, (n, max_q, h, ng), dev,
+                     lambda: lib().spec_attn_shared_workspace(cache._ref, ng, n, max_q, h))
+    out, lse, ws = _attn_out(q, shape, dev, out, lse, need, stream)
+    os_ = _rows3("out", out)
+    _call(dev, stream, lib().spec_attn_shared, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
+          kv_lens.data_ptr(), groups.data_ptr() if groups is not None else None, ng, shared.data_ptr(), n, max_q, h,
+          scale, out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None,
+          ws.data_ptr() if need else None, need)
+    return out, (lse if lse is not False else None)
+
+
+def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream=None, window=0, sinks=0):
     """Causal attention within packed sequences: rows cu[b] .. cu[b+1]-1 of q
     [tokens, n_heads, head_dim] and k, v [tokens, n_kv_heads, head_dim] (bf16,
     may be slices of one projection) are sequence b; max_len bounds their
-    lengths and sizes the grid (default: tokens; give the real bound for many).  Returns (out, lse) as attn_paged."""
+    lengths and sizes the grid (default: tokens; give the real bound for many);
+    window and sinks as for attn_paged.  Returns (out, lse) as attn_paged."""
     _torch()
     qs, ks, vs = _rows3("q", q), _rows3("k", k), _rows3("v", v)
     shape, kshape, dev = q.shape, k.shape, q.get_device()
@@ -853,6 +910,12 @@ def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream
     _index("cu", cu, seqs + 1, dev)
     out, lse, _ = _attn_out(q, shape, dev, out, lse, 0, stream)
     os_ = _rows3("out", out)
+    if window or sinks:
+        _call(dev, stream, lib().spec_attn_prompt_window, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+              v.data_ptr(), vs[0], vs[1], cu.data_ptr(), seqs, n, n if max_len is None else max_len, h, kshape[1], d,
+              scale, min(window, 0x7fffffff), min(sinks, 0x7fffffff), out.data_ptr(), os_[0], os_[1],
+              lse.data_ptr() if lse is not False else None)
+        return out, (lse if lse is not False else None)
     _call(dev, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
           v.data_ptr(), vs[0], vs[1], cu.data_ptr(), seqs, n, n if max_len is None else max_len, h, kshape[1], d,
           scale, out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None)

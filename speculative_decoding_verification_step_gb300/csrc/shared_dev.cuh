@@ -1,0 +1,37 @@
+// Shared prefixes: what a group of sequences shares, as the kernels work it out.
+#pragma once
+#include "common.cuh"
+#include "paged.h"
+
+namespace sv {
+
+namespace {
+
+// The rows of sequences first .. last - 1, none unless they lie in the call's.
+struct ShRows {
+  int row0, toks;
+};
+SV_DEV ShRows sh_rows(const PAttn& a, int first, int last) {
+  if (first < 0 || last > a.seqs || first >= last) return ShRows{0, 0};
+  const int r0 = __ldg(a.cu + first), r1 = __ldg(a.cu + last);
+  if (r0 < 0 || r1 <= r0 || r1 > a.tokens) return ShRows{0, 0};
+  return ShRows{r0, r1 - r0};
+}
+// The least position of a first new token among sequences first + threadIdx.x, ... (the
+// caller joins the block's threads); sequences without rows do not count.
+SV_DEV int sh_least(const PAttn& a, int first, int last) {
+  int least = 0x7fffffff;
+  const int cap = (int)min((int64_t)0x7fffffff, (int64_t)a.max_pages << a.page_shift);
+  for (int s = max(first, 0) + (int)threadIdx.x; s < min(last, a.seqs); s += blockDim.x) {
+    const int r = __ldg(a.cu + s), n = __ldg(a.cu + s + 1) - r, keys = min(max(__ldg(a.lens + s), 0), cap);
+    if (r >= 0 && n > 0 && n <= a.tokens - r) least = min(least, max(0, keys - n));
+  }
+  return least;
+}
+SV_DEV int sh_eff(const PAttn& a, int group, int least) {
+  return least == 0x7fffffff ? 0 : max(0, min(__ldg(a.shared + group), least));
+}
+
+}  // namespace
+
+}  // namespace sv

@@ -1,0 +1,423 @@
+"""Attention with a sliding window and first tokens that stay visible, and attention of
+sequences behind a shared prefix, against plain 64-bit forms.
+
+Tolerances are those of the paged attention (they count the keys' roundings and one
+bf16 rounding of a weight and of the output).  A row joined from parts has for each
+part a factor 2^(m_i - M), off by 2 units (2^-22) and one product's rounding, in its
+sums: parts times 2^-21 of sum w|v| at most, and the same of the row's sum; parts are
+at most keys / 128 + 2, which the bound's keys * 2^-23 covers from 600 keys on, and
+the 2^-20 for the two or three parts of fewer.
+"""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_verification_step_gb300 as sv
+from test_gpu_paged import (F64, _cache, _check_rows, _gen, _give_up, _i32, _paged_case, _paged_check, _randn, _read,
+                            _values)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    sv.build()
+    sv.lib()
+
+
+def _see(n, ctx, window, sinks):
+    p, j = torch.arange(ctx - n, ctx, device="cuda")[:, None], torch.arange(ctx, device="cuda")
+    return (j <= p) & ((j > p - window) | (j < sinks) if window else j >= 0)
+
+
+def _ref(q, ks, vs, see, scale):
+    """Rows q [n, hq, d] over the keys ks, vs [keys, hk, d] that see [n, keys] names, in 64 bits:
+    out, lse and the bounds' sums (sum w|v|, largest scale sum|q k|)."""
+    rep = q.shape[1] // ks.shape[1]
+    q, ks, vs = q.to(F64), ks.to(F64).repeat_interleave(rep, 1), vs.to(F64).repeat_interleave(rep, 1)
+    some = see.any(0)                              # what no row sees may hold anything
+    ks, vs, see = ks[some], vs[some], see[:, some]
+    if see.shape[1] == 0:
+        z = torch.zeros_like(q)
+        return z, torch.full(q.shape[:2], -math.inf, dtype=F64, device="cuda"), z, torch.zeros(1, 1, 1, device="cuda")
+    s = torch.einsum("nhd,khd->hnk", q, ks) * scale
+    size = torch.einsum("nhd,khd->hnk", q.abs(), ks.abs()) * scale
+    s = s.masked_fill(~see, -math.inf)
+    lse = torch.logsumexp(s, -1)
+    w = torch.where(see, torch.exp(s - lse.clamp_min(-1e300).unsqueeze(-1)), torch.zeros_like(s))
+    dot = size.masked_fill(~see, 0).amax(-1)
+    return torch.einsum("hnk,khd->nhd", w, vs), lse.T, torch.einsum("hnk,khd->nhd", w, vs.abs()), dot.T.unsqueeze(-1)
+
+
+def _evict(cache, ns, ctx, window, sinks):
+    """What no row of the chunks sees becomes NaN; whole pages of it leave the table."""
+    ps = cache.page_size
+    for b, (n, c) in enumerate(zip(ns, ctx)):
+        if not n or not c:
+            continue
+        lo = max(0, max(0, c - n) - window + 1)
+        for j in range(min(sinks, c), lo):
+            page = int(cache.table[b, j // ps])
+            if page < 0:
+                continue
+            if (j // ps) * ps >= sinks and (j // ps + 1) * ps <= lo:
+                cache.table[b, j // ps] = -1
+                continue
+            for t in (cache.k, cache.v):
+                t[page, :, j % ps] = math.nan if t.dtype is torch.bfloat16 else t[page, :, j % ps]
+            if cache.k_scale is not None:
+                cache.k_scale[page, :, j % ps] = cache.v_scale[page, :, j % ps] = 255
+
+
+def _window_check(c, q, cu, lens, ns, ctx, window, sinks, values, max_q=None):
+    hd = q.shape[2]
+    out = torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    sv.attn_paged(q, c, cu, lens, max_q=max_q, out=out, lse=lse, window=window, sinks=sinks)
+    r = 0
+    for b, (n, m) in enumerate(zip(ns, ctx)):
+        k, v = values[b]
+        _check_rows(out[r:r + n], lse[r:r + n], _ref(q[r:r + n], k, v, _see(n, m, window, sinks), hd ** -0.5), m, hd)
+        r += n
+    assert (out[r:] == 7.0).all() and (lse[r:] == 9.0).all()
+    return out, lse
+
+
+def _all_values(c, ctx):
+    values = _values(c)
+    return [_read(c, values, torch.full((m,), b, dtype=torch.int32, device="cuda"), torch.arange(m, device="cuda").int())
+            for b, m in enumerate(ctx)]
+
+
+WINDOW = [  # hq, hk, hd, page, new tokens, contexts, window, sinks
+    (32, 8, 128, 16, [6], [512], 100, 4),
+    (32, 8, 128, 16, [6, 6, 6], [513, 47, 1000], 64, 0),
+    (32, 8, 64, 32, [1] * 5, [1, 2, 16, 17, 3000], 16, 1),
+    (8, 2, 32, 16, [5, 1, 9], [5, 333, 64], 1, 0),              # a row sees itself alone
+    (4, 4, 64, 64, [1, 17, 16], [129, 17, 700], 33, 17),
+    (7, 1, 128, 32, [3, 5], [300, 5], 10, 300),                 # more first tokens than keys
+    (12, 4, 128, 256, [2, 0, 4], [40, 10, 600], 700, 3),        # a window past the contexts
+    (8, 2, 64, 16, [4, 3, 2], [2, 0, 1], 2, 1),                 # chunks longer than their contexts: empty rows
+    (8, 2, 64, 16, [2, 1, 1], [40, 25, 31], 15, 9),             # the first tokens end beside the window
+    (2, 2, 64, 16, [1], [20000], 5000, 100),
+    (16, 2, 128, 16, [4, 4], [20000, 9000], 4096, 4),
+    (8, 2, 64, 64, [130, 257, 1], [500, 257, 100], 50, 4),
+    (32, 8, 128, 32, [129], [1500], 200, 0),
+    (32, 8, 128, 16, [40, 300, 3], [900, 2000, 300], 129, 140),  # first tokens over two steps of 128
+    (4, 2, 128, 64, [200, 400], [200, 3000], 1, 1),
+    (16, 4, 64, 16, [300], [5000], 700, 16),
+    (32, 8, 128, 16, [128] * 4, [1000, 800, 300, 128], 128, 128),
+    (8, 8, 128, 16, [400], [900], 2 ** 31 - 1, 2 ** 31 - 1),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hk,hd,ps,ns,ctx,window,sinks", WINDOW)
+def test_window_paged(hq, hk, hd, ps, ns, ctx, window, sinks, dtype):
+    c, q, cu, lens = _paged_case(sum(ctx) + hd, hq, hk, hd, ps, dtype, ns, ctx, pad=2)
+    values = _all_values(c, ctx)
+    _evict(c, ns, ctx, window, sinks)
+    a = _window_check(c, q, cu, lens, ns, ctx, window, sinks, values)
+    b = _window_check(c, q, cu, lens, ns, ctx, window, sinks, values, max_q=max(ns))
+    again = sv.attn_paged(q, c, cu, lens, max_q=max(ns), window=window, sinks=sinks)
+    n = sum(ns)
+    assert torch.equal(again[0][:n], b[0][:n]) and torch.equal(again[1][:n], b[1][:n])
+    assert a[0].shape == b[0].shape
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 6, 40, 200])
+def test_window_of_everything(dtype, n):
+    """A window as long as the contexts is plain attention, and window 0 is the call without one."""
+    ns, ctx = [n, n], [700, 513]
+    c, q, cu, lens = _paged_case(77, 16, 4, 128, 32, dtype, ns, ctx)
+    _paged_check(c, q, cu, lens, ns, ctx, max_q=n, window=700)
+    ref = sv.attn_paged(q, c, cu, lens, max_q=n)
+    for kw in (dict(window=0), dict(window=0, sinks=5)):
+        got = sv.attn_paged(q, c, cu, lens, max_q=n, **kw)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [6, 130])
+def test_window_bounds_and_bad_indices(dtype, n):
+    """max_q leaves rows, lengths past the table are cut, bad entries read as zeros, broken row starts
+    are skipped, and neighbours are as they were."""
+    ns, ctx = [n, n, n], [300, 700, 450]
+    c, q, cu, lens = _paged_case(31, 8, 2, 64, 16, dtype, ns, ctx)
+    kw = dict(window=100, sinks=4)
+    ref, rl = sv.attn_paged(q, c, cu, lens, max_q=n, **kw)
+    out, lse = torch.full_like(ref, 3.0), torch.full_like(rl, 3.0)
+    sv.attn_paged(q, c, cu, lens, max_q=2, out=out, lse=lse, **kw)
+    assert (out.view(3, n, 8, 64)[:, 2:] == 3.0).all() and torch.isfinite(out.float()).all()
+    for bad in ([0, n, 2 * n, 10 ** 6], [-5, n, 2 * n, 3 * n], [0, n, n, 3 * n]):
+        got, _ = sv.attn_paged(q, c, _i32(bad), lens, max_q=n, out=torch.full_like(ref, 3.0), **kw)
+        same = slice(n, 2 * n) if bad[2] == 2 * n else slice(0, n)
+        assert torch.equal(got[same], ref[same])
+    saved = c.table.clone()
+    c.table[0, :] = 2 ** 30
+    c.table[1, 30:] = -3
+    got, gl = sv.attn_paged(q, c, cu, lens, max_q=n, **kw)
+    assert torch.equal(got[2 * n:], ref[2 * n:]) and (got[:n] == 0).all()
+    assert torch.isfinite(gl[:n]).all()                       # keys of zeros: scores of 0
+    c.table.copy_(saved)
+    cap = c.max_pages * 16
+    over, want = (sv.attn_paged(q, c, cu, _i32([300, x, 450]), max_q=n, **kw)[0] for x in (2 ** 31 - 1, cap))
+    assert torch.equal(over.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("hq,hk,hd,ns,window,sinks", [
+    (8, 2, 64, [130, 1, 77], 20, 4),
+    (32, 8, 128, [17], 5, 1),
+    (8, 2, 32, [100, 33], 1, 0),
+    (7, 1, 128, [64, 0, 65, 200], 50, 60),
+    (12, 4, 64, [600, 129, 3], 128, 0),
+    (4, 4, 128, [1025], 300, 4),
+    (32, 8, 128, [900, 1500], 129, 130),
+    (16, 2, 64, [2000], 1000, 7),
+    (32, 8, 128, [2100], 64, 16),
+])
+def test_window_prompt(hq, hk, hd, ns, window, sinks):
+    g = _gen(sum(ns))
+    total = sum(ns)
+    x = _randn(g, total + 3, hq + 2 * hk, hd).bfloat16()
+    x[total:] = math.nan                          # rows behind the last sequence
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    cu = [0]
+    for n in ns:
+        cu.append(cu[-1] + n)
+    for bound in (None, max(ns)):
+        out = torch.full((total + 3, hq, hd), 7.0, device="cuda", dtype=torch.bfloat16)
+        lse = torch.full((total + 3, hq), 9.0, device="cuda")
+        sv.attn_prompt(q, k, v, _i32(cu), max_len=bound, out=out, lse=lse, window=window, sinks=sinks)
+        for b, n in enumerate(ns):
+            r = slice(cu[b], cu[b + 1])
+            if n:
+                _check_rows(out[r], lse[r], _ref(q[r], k[r], v[r], _see(n, n, window, sinks), hd ** -0.5), n, hd)
+        assert (out[total:] == 7.0).all() and (lse[total:] == 9.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_window_waits_that_run_out(hd, dtype):
+    ns, ctx = [256, 130, 64], [5000, 3333, 6001]
+    c, q, cu, lens = _paged_case(63, 16, 4, hd, 64, dtype, ns, ctx)
+    _give_up(lambda o, l: sv.attn_paged(q, c, cu, lens, max_q=256, out=o, lse=l, window=1500, sinks=4), q, (1, 2, 5))
+
+
+# ------------------------------------------------------------ shared prefixes
+def _shared_case(seed, hq, hk, hd, ps, dtype, ns, first, shared, rests, pad=0):
+    """Sequences whose rows of the table begin alike within a group; slots past the lengths hold NaN.
+    first: the groups' first sequences and the end; rests: positions of every sequence behind the prefix."""
+    g = _gen(seed)
+    group = [max((i for i, f in enumerate(first[:-1]) if f <= b), default=-1) if b < first[-1] else -1 for b in range(len(ns))]
+    lens = [(max(shared[x], 0) if x >= 0 else 0) + r for x, r in zip(group, rests)]
+    cache = _cache(g, len(ns), max(max(lens), 1), hk, ps, hd, dtype)
+    for b, x in enumerate(group):
+        if x >= 0:
+            k = -(-max(shared[x], 0) // ps)
+            cache.table[b, :k] = cache.table[first[x], :k]
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).fill_(0x7f) if dtype == "e4m3" else t.fill_(math.nan)
+    if dtype == "e4m3":
+        cache.k_scale.fill_(255)
+        cache.v_scale.fill_(255)
+    rows = [(b, p) for b, n in enumerate(lens) for p in range(n)]
+    if rows:
+        seq, pos = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in zip(*rows))
+        slot = cache.table[seq.long(), (pos // ps).long()].long() * ps + pos % ps
+        _, inv = torch.unique(slot, return_inverse=True)         # one writer a slot
+        once = torch.full((int(inv.max()) + 1,), len(rows), device="cuda").scatter_reduce(
+            0, inv, torch.arange(len(rows), device="cuda"), "amin")
+        seq, pos = seq[once], pos[once]
+        sv.kv_append(cache, _randn(g, len(once), hk, hd), _randn(g, len(once), hk, hd), seq, pos)
+    cu = [0]
+    for n in ns:
+        cu.append(cu[-1] + n)
+    q = _randn(g, cu[-1] + pad, hq + 1, hd).bfloat16()[:, :hq]
+    return cache, q, _i32(cu), _i32(lens), lens
+
+
+def _shared_check(c, q, cu, lens, ns, ctx, shared, groups, max_q):
+    hd = q.shape[2]
+    out = torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    got = sv.attn_shared(q, c, cu, lens, shared, groups=groups, max_q=max_q, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    r = 0
+    for b, ((k, v), n, m) in enumerate(zip(_all_values(c, ctx), ns, ctx)):
+        k, v = k[:m], v[:m]
+        _check_rows(out[r:r + n], lse[r:r + n], _ref(q[r:r + n], k, v, _see(n, m, 0, 0), hd ** -0.5), m, hd)
+        r += n
+    assert (out[r:] == 7.0).all() and (lse[r:] == 9.0).all()
+    return out, lse
+
+
+SHARED = [  # hq, hk, hd, page, new tokens, groups, shared, positions behind the prefix
+    (32, 8, 128, 16, [6] * 4, [0, 4], [512], [6, 50, 64, 17]),
+    (32, 8, 128, 16, [1] * 9, [0, 9], [3000], [1, 2, 16, 17, 33, 100, 1, 5, 300]),
+    (8, 2, 64, 32, [1, 4, 9, 2], [0, 2, 4], [640, 1024], [1, 20, 9, 700]),
+    (8, 2, 64, 64, [3, 3, 3, 3, 3], [1, 3], [129], [10, 4, 5, 300, 3]),           # three outside the group
+    (7, 1, 128, 32, [3, 5, 1], [0, 3], [777], [40, 30, 60]),                      # ends inside a page
+    (12, 4, 128, 256, [2, 0, 4, 1], [0, 4], [512], [40, 10, 60, 1]),              # a sequence without new tokens
+    (16, 2, 128, 16, [8] * 5, [0, 1, 5], [100, 2000], [8, 8, 9, 10, 300]),        # a group of one
+    (8, 8, 64, 16, [1, 60, 2], [0, 3], [300], [1, 60, 300]),                      # 60 rows a KV head
+    (32, 8, 64, 16, [2] * 40, [0, 10, 20, 30, 40], [400, 16, 0, 2000], [2 + i for i in range(40)]),
+    (128, 1, 128, 16, [1] * 6, [0, 6], [700], [1, 9, 20, 33, 1, 64]),             # a tile holds one token
+    (4, 4, 128, 16, [1] * 300, [0, 300], [256], [1 + i % 40 for i in range(300)]),  # two row pairs a head
+    (6, 2, 64, 16, [1, 1], [0, 2], [-5], [30, 40]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hk,hd,ps,ns,first,shared,rests", SHARED)
+def test_shared(hq, hk, hd, ps, ns, first, shared, rests, dtype):
+    c, q, cu, lens, ctx = _shared_case(sum(rests) + hd, hq, hk, hd, ps, dtype, ns, first, shared, rests, pad=3)
+    sh, gr = _i32(shared), _i32(first)
+    a = _shared_check(c, q, cu, lens, ns, ctx, sh, gr, max(ns))
+    if first == [0, len(ns)]:
+        b = sv.attn_shared(q, c, cu, lens, sh, max_q=max(ns))
+        n = sum(ns)
+        assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:n], b[1][:n])
+    # a number past what every row sees is cut there (within the table's alike pages), a smaller one is as good
+    for less in ([max(0, s - 37) for s in shared], [s // 3 for s in shared]):
+        _shared_check(c, q, cu, lens, ns, ctx, _i32(less), gr, max(ns))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_shared_is_cut_to_what_rows_see(dtype, hd):
+    """Sequences that name the same pages all along, of different lengths: the shortest one's new
+    tokens bound what is shared, whatever the call says."""
+    ns, ctx = [2, 1, 3, 0], [900, 400, 650, 3]
+    g = _gen(hd)
+    c = _cache(g, 4, 900, 2, 16, hd, dtype)
+    c.table.copy_(c.table[:1].expand_as(c.table).clone())
+    pos = torch.arange(900, device="cuda").int()
+    sv.kv_append(c, _randn(g, 900, 2, hd), _randn(g, 900, 2, hd), torch.zeros_like(pos), pos)
+    q = _randn(g, 6, 8, hd).bfloat16()
+    cu, lens = _i32([0, 2, 3, 6, 6]), _i32(ctx)
+    for shared in (399, 400, 900, 2 ** 31 - 1, 384, 1, 0):
+        _shared_check(c, q, cu, lens, ns, ctx, _i32([shared]), None, 3)
+    _shared_check(c, q, cu, _i32([900, 1, 650, 3]), ns, [900, 1, 650, 3], _i32([500]), None, 3)    # nothing left
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_shared_bad_indices(dtype):
+    """Groups and row starts that make no sense: nothing outside the rows is written, sequences of sound
+    groups are as they were."""
+    ns, first, shared = [4] * 6, [0, 3, 6], [600, 300]
+    c, q, cu, lens, ctx = _shared_case(5, 16, 4, 128, 16, dtype, ns, first, shared, [20] * 6, pad=2)
+    ref, _ = sv.attn_shared(q, c, cu, lens, _i32(shared), groups=_i32(first), max_q=4)
+    call = lambda g, cu=cu, t=None: sv.attn_shared(q, c, cu, lens, _i32(shared), groups=_i32(g), max_q=4,
+                                                   out=torch.full_like(ref, 7.0))[0]
+    for g in ([0, 3, 7], [-1, 3, 6], [0, 3, 2 ** 31 - 1], [3, 6, 0], [5, 2, 6], [0, 6, 3], [-2 ** 31, 0, 2 ** 31 - 1]):
+        assert (call(g)[24:] == 7.0).all()
+    out = call([3, 3, 6])
+    plain, _ = sv.attn_paged(q, c, cu, lens, max_q=4)
+    assert torch.allclose(out[:12].float(), plain[:12].float(), rtol=2 ** -6, atol=2 ** -6)     # (in no group: whole)
+    assert torch.equal(call([0, 3, 6])[:24], ref[:24])
+    for bad in ([0, 4, 8, 12, 16, 20, 10 ** 6], [-9, 4, 8, 12, 16, 20, 24], [0, 20, 4, 12, 16, 20, 24]):
+        assert (call(first, cu=_i32(bad))[24:] == 7.0).all()
+    c.table[:3, 5] = 2 ** 30                                     # a page outside the pool reads as zeros
+    got = call(first)
+    assert torch.equal(got[12:24], ref[12:24]) and torch.isfinite(got[:12].float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_shared_streams_graphs_workspaces(dtype):
+    """The same bits on streams beside one another, replayed with new lengths and prefixes, and with a
+    workspace that holds anything; without one the call is attn_paged."""
+    ns, first, shared = [3] * 8, [0, 5, 8], [2000, 900]
+    c, q, cu, lens, ctx = _shared_case(9, 32, 8, 128, 16, dtype, ns, first, shared, [30, 200] * 4)
+    sh, gr = _i32(shared), _i32(first)
+    q2 = q.flip(0).contiguous()
+    call = lambda x, **kw: sv.attn_shared(x, c, cu, lens, sh, groups=gr, max_q=3, **kw)
+    ref, ref2 = call(q), call(q2)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, got2 = [], []
+    for _ in range(10):
+        with torch.cuda.stream(a):
+            got.append(call(q))
+        got2.append(call(q2, stream=b.cuda_stream))
+    torch.cuda.synchronize()
+    for x, want in [(x, ref) for x in got] + [(x, ref2) for x in got2]:
+        assert torch.equal(x[0], want[0]) and torch.equal(x[1], want[1])
+    L, n = sv.lib(), 24
+    need = L.spec_attn_shared_workspace(c._ref, 2, n, 3, 32)
+    ws = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
+    plain = sv.attn_paged(q, c, cu, lens, max_q=3)
+    for size in (0, max(0, need - 16), need):
+        out, lse = torch.zeros(n, 32, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 32, device="cuda")
+        assert L.spec_attn_shared(c._ref, q.data_ptr(), q.stride(0), q.stride(1), cu.data_ptr(), lens.data_ptr(),
+                                  gr.data_ptr(), 2, sh.data_ptr(), n, 3, 32, 0.0, out.data_ptr(), 32 * 128, 128,
+                                  lse.data_ptr(), ws.data_ptr() if size else None, size,
+                                  torch.cuda.current_stream().cuda_stream) == 0
+        if size == need:
+            assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+        else:
+            assert torch.allclose(out.float(), plain[0].float(), rtol=2 ** -6, atol=2 ** -6)
+    assert (ws[need:] == 0xff).all()
+    graph, o = torch.cuda.CUDAGraph(), torch.zeros_like(ref[0])
+    with torch.cuda.graph(graph):
+        call(q, out=o)
+    for new, less in ((shared, 0), ([640, 0], 0), ([1999, 17], 5), ([0, 0], 0), ([5000, 5000], 1)):
+        sh.copy_(_i32(new))
+        lens.copy_(_i32([x - less for x in ctx]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, call(q)[0])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_shared_waits_that_run_out(dtype, hd):
+    """A prefix block that gives up leaves NaN in the rows of all parts of its run, also of those that it
+    did not come to."""
+    ns, first, shared = [4] * 40, [0, 30, 40], [3000, 900]
+    c, q, cu, lens, ctx = _shared_case(19, 16, 4, hd, 16, dtype, ns, first, shared, [9] * 40)
+    sh, gr = _i32(shared), _i32(first)
+    _give_up(lambda o, l: sv.attn_shared(q, c, cu, lens, sh, groups=gr, max_q=4, out=o, lse=l), q, (1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd,ps", [(128, 16), (64, 64)])
+def test_serving_loop(dtype, hd, ps):
+    """The calls as a program runs them together: a prompt for all sequences, then verify steps whose
+    pages are reserved and given back on the device, rows normed, rotated and written in one call, and
+    attention behind the prompt and in a window, all against 64-bit forms of the cache's values."""
+    g = _gen(hd)
+    hq, hk, seqs, width = 8, 2, 5, 640 // ps + 2
+    prompt = 512
+    shared_pages = prompt // ps
+    table = torch.full((seqs, width), -1, dtype=torch.int32, device="cuda")
+    pool = shared_pages + seqs * (width - shared_pages)
+    c = sv.KVCache.empty(pool, ps, hk, hd, table, dtype)
+    table[:, :shared_pages] = torch.arange(shared_pages, device="cuda").int()
+    free = torch.arange(shared_pages, pool, device="cuda").int()
+    n_free = _i32([pool - shared_pages])
+    plan, gq, gk = sv.rope_plan(hd, 500000.0), *(torch.exp(0.3 * _randn(g, hd)) for _ in range(2))
+
+    def rows(n, seq, pos):
+        x = _randn(g, n, hq + 2 * hk, hd).bfloat16()
+        return sv.qkv_append(c, x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], seq, pos, plan, gq, gk)
+
+    pos = torch.arange(prompt, device="cuda").int()
+    rows(prompt, torch.zeros_like(pos), pos)                     # the prompt, once
+    lens, shared = _i32([prompt] * seqs), _i32([prompt])
+    held = n_free.item()
+    for counts, kept in (([6] * 5, [1, 6, 3, 2, 4]), ([6, 1, 0, 6, 6], [2, 1, 0, 6, 1]), ([40] * 5, [40, 1, 17, 33, 2])):
+        cap = sum(counts) + 7
+        cu, now, seq, pos, lacking = sv.kv_reserve(c, lens, _i32(counts), free, n_free, cap)
+        assert lacking.item() == 0 and now.tolist() == [a + b for a, b in zip(lens.tolist(), counts)]
+        q = rows(cap, seq, pos)
+        _shared_check(c, q, cu, now, counts, now.tolist(), shared, None, max(counts))
+        _window_check(c, q, cu, now, counts, now.tolist(), 50, 4, _all_values(c, now.tolist()), max_q=max(counts))
+        lens = lens + _i32(kept)
+        sv.kv_release(c, now, lens, free, n_free)
+        pages = sum(-(-x // ps) - shared_pages for x in lens.tolist())
+        assert n_free.item() == held - pages
+    sv.kv_release(c, lens, _i32([prompt] * seqs), free, n_free)
+    assert n_free.item() == held and sorted(free.tolist()) == list(range(shared_pages, pool))

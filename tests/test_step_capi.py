@@ -77,6 +77,53 @@ def test_row_refusals(L):
     assert _norm(L, n=0) == 0
 
 
+def _window(L, c, **k):
+    return L.spec_attn_paged_window(c, k.get("q", P), k.get("qs", 256), 64, k.get("cu", P), k.get("lens", P), k.get("n", 1),
+                                    k.get("m", 1), k.get("h", 4), k.get("scale", 0.0), k.get("window", 8), k.get("sinks", 1),
+                                    k.get("out", P), 256, 64, None, k.get("ws"), k.get("wb", 0), None)
+
+
+def _prompt(L, **k):
+    return L.spec_attn_prompt_window(k.get("q", P), 256, 64, k.get("k", P), 128, 64, k.get("v", P), k.get("vs", 128), 64,
+                                     k.get("cu", P), k.get("seqs", 1), k.get("n", 1), 1, k.get("h", 4), 2, k.get("hd", 64),
+                                     k.get("scale", 0.0), k.get("window", 8), k.get("sinks", 1), P, 256, 64, None, None)
+
+
+def _shared(L, c, **k):
+    return L.spec_attn_shared(c, k.get("q", P), k.get("qs", 256), 64, k.get("cu", P), k.get("lens", P), k.get("groups", P),
+                              k.get("ng", 1), k.get("shared", P), k.get("n", 1), k.get("m", 1), k.get("h", 4),
+                              k.get("scale", 0.0), k.get("out", P), 256, 64, None, k.get("ws"), k.get("wb", 0), None)
+
+
+def test_attention_refusals(L):
+    c = ctypes.byref(_cache())
+    for call in (_window, _shared):
+        for name in ("q", "cu", "lens", "out"):
+            assert call(L, c, **{name: None}) == -1, name
+        assert call(L, c, q=P + 2) == call(L, c, qs=260) == call(L, c, n=-1) == call(L, c, m=-1) == -1
+        assert call(L, c, ws=P + 4, wb=64) == call(L, c, ws=P, wb=-1) == call(L, c, scale=math.nan) == -1
+        assert call(L, c, scale=3e38) == call(L, c, scale=-1.0) == -1
+        assert call(L, c, h=3) == call(L, c, h=0) == -3
+        assert call(L, c, n=0) == call(L, c, m=0) == 0
+        assert call(L, None) == -1
+    for call in (lambda **k: _window(L, c, **k), lambda **k: _prompt(L, **k)):
+        assert call(window=-1) == call(sinks=-1) == -1
+    assert _shared(L, c, shared=None) == _shared(L, c, ng=0) == _shared(L, c, groups=None, ng=2) == -1
+    for name in ("q", "k", "v", "cu"):
+        assert _prompt(L, **{name: None}) == -1, name
+    assert _prompt(L, seqs=0) == _prompt(L, vs=132) == -1 and _prompt(L, h=3) == _prompt(L, hd=96) == -3
+    assert _prompt(L, n=0) == 0
+    assert L.spec_attn_shared_workspace(None, 1, 1, 1, 4) == 0
+    for bad in ((0, 1, 1, 4), (1, 0, 1, 4), (1, 1, 0, 4), (1, 1, 1, 3)):
+        assert L.spec_attn_shared_workspace(c, *bad) == 0
+
+
+@pytest.mark.parametrize("change,code", BAD_CACHE)
+def test_attention_cache_refusals(L, change, code):
+    c = ctypes.byref(_cache(**change))
+    assert _window(L, c) == _shared(L, c) == code
+
+
 def test_binding_refusals(L):
     sv._torch()
     plan, i, g = sv.rope_plan(64, 10000.0), torch.zeros(2, dtype=torch.int32), torch.ones(64)
@@ -96,3 +143,4 @@ def test_binding_refusals(L):
 def test_no_cpu_fallback(L):
     c = ctypes.byref(_cache())
     assert _reserve(L, c) == _release(L, c) == _qkv(L, c) == _norm(L) == -5
+    assert _window(L, c) == _shared(L, c) == _prompt(L) == -5
