@@ -532,12 +532,14 @@ SPEC_API int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_hea
  * of them.  Positions that no row of the call's chunk sees are not read where
  * whole pages (or a tile's rows) of them lie together, so their table entries need
  * not name pages that hold them any more; what else such a slot holds never
- * reaches an output.  The rest as for spec_attn_paged (which has no use for a
- * workspace here, NULL) and spec_attn_prompt. */
+ * reaches an output.  The rest, the workspace too, as for spec_attn_paged and
+ * spec_attn_prompt. */
 SPEC_API int spec_attn_paged_window(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
                     const int32_t* cu_q, const int32_t* kv_lens, int tokens, int max_q, int n_heads,
                     float scale, int window, int sinks, void* out, int64_t out_tok_stride, int64_t out_head_stride,
                     float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+SPEC_API int64_t spec_attn_paged_window_workspace(const spec_kv_cache* cache, int tokens, int max_q, int n_heads,
+                    int window, int sinks);
 SPEC_API int spec_attn_prompt_window(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* k,
                      int64_t k_tok_stride, int64_t k_head_stride, const void* v, int64_t v_tok_stride,
                      int64_t v_head_stride, const int32_t* cu, int seqs, int tokens, int max_len,

@@ -162,6 +162,7 @@ SIGNATURES = {
                                         _INT, _INT, _INT, _INT, ctypes.c_float, _VP, _I64, _I64, _VP, _VP]),
     "spec_attn_paged_window": (ctypes.c_int, [_VP, _VP, _I64, _I64, _VP, _VP, _INT, _INT, _INT, ctypes.c_float,
                                               _INT, _INT, _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
+    "spec_attn_paged_window_workspace": (ctypes.c_int64, [_VP, _INT, _INT, _INT, _INT, _INT]),
     "spec_attn_prompt_window": (ctypes.c_int, [_VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _INT, _INT,
                                                _INT, _INT, _INT, _INT, ctypes.c_float, _INT, _INT, _VP, _I64, _I64,
                                                _VP, _VP]),
@@ -845,11 +846,14 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
     if max_q is None:
         max_q = n
     if window or sinks:
-        out, lse, _ = _attn_out(q, shape, dev, out, lse, 0, stream)
+        window, sinks = min(window, 0x7fffffff), min(sinks, 0x7fffffff)
+        need = _ws_bytes(cache, (n, max_q, h, window, sinks), dev,
+                         lambda: lib().spec_attn_paged_window_workspace(cache._ref, n, max_q, h, window, sinks))
+        out, lse, ws = _attn_out(q, shape, dev, out, lse, need, stream)
         os_ = _rows3("out", out)
         _call(dev, stream, lib().spec_attn_paged_window, cache._ref, q.data_ptr(), qs[0], qs[1], cu_q.data_ptr(),
-              kv_lens.data_ptr(), n, max_q, h, scale, min(window, 0x7fffffff), min(sinks, 0x7fffffff),
-              out.data_ptr(), os_[0], os_[1], lse.data_ptr() if lse is not False else None, None, 0)
+              kv_lens.data_ptr(), n, max_q, h, scale, window, sinks, out.data_ptr(), os_[0], os_[1],
+              lse.data_ptr() if lse is not False else None, ws.data_ptr() if need else None, need)
         return out, (lse if lse is not False else None)
     need = _ws_bytes(cache, (n, max_q, h), dev, lambda: lib().spec_attn_paged_workspace(cache._ref, n, max_q, h))
     out, lse, ws = _attn_out(q, shape, dev, out, lse, need, stream)

@@ -40,7 +40,9 @@ bool row_aligned(const void* p, int64_t ts, int64_t hs) {
 // 24 rows, head dim 64: 64 x 4096 108 / 104, 4 x 8192 25 / 27, 1 x 16384 33 / 28.
 size_t td_bytes(const PAttn& a, int64_t rows, int sms) {
   if (!a.paged || rows < 1 || rows > kPaMaxRows || !pattn_td_supported(a)) return 0;
-  const int64_t keys = (int64_t)a.max_pages << a.page_shift, items = (int64_t)a.seqs * a.hkv * ((rows + 31) / 32);
+  int64_t keys = (int64_t)a.max_pages << a.page_shift;
+  if (a.window > 0) keys = std::min(keys, (int64_t)a.window + a.sinks + a.max_q);
+  const int64_t items = (int64_t)a.seqs * a.hkv * ((rows + 31) / 32);
   const int64_t units = items * ((keys + 127) / 128);
   if (units > 0x7fffffffLL) return 0;
   const bool wide = rows > 16;
@@ -104,17 +106,14 @@ int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
-  if (a.window > 0) {
-    e = choose_way(a, sms).tc ? launch_pattn_tc_window(a, sms, st) : launch_pa_window(a, sms, st);
-    return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
-  }
   if (const size_t need = a.shared ? shared_bytes(a, sms) : 0; need && a.ws && ws_bytes >= need) {
     e = launch_pattn_shared(a, sms, st);
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
   }
   const Way way = choose_way(a, sms);
-  if (way.tc) e = launch_pattn_tc(a, sms, st);
+  if (way.tc) e = a.window > 0 ? launch_pattn_tc_window(a, sms, st) : launch_pattn_tc(a, sms, st);
   else if (way.td_ws && a.ws && ws_bytes >= way.td_ws) e = launch_pattn_td(a, sms, st);
+  else if (a.window > 0) e = launch_pa_window(a, sms, st);
   else e = a.hd == 32 ? launch_pa_hd<32, kPaCausal>(a, sms, st) : a.hd == 64 ? launch_pa_hd<64, kPaCausal>(a, sms, st) : launch_pa_hd<128, kPaCausal>(a, sms, st);
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, w + cudaGetErrorString(e));
 }
@@ -132,14 +131,18 @@ void cache_fields(PAttn& a, const spec_kv_cache* cache) {
   while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
 }
 
-// A call's sizes alone, for what is asked of them (queries and outputs with strides that the
-// kernels take: others go to the register tiles).
-PAttn sized(const spec_kv_cache* cache, int tokens, int max_q, int n_heads) {
-  PAttn a{};
+// Workspace of a call of these sizes (queries and outputs with strides that the kernels take:
+// others go to the register tiles).  a: the window, or the number of groups.
+int64_t asked_workspace(PAttn a, const char* who, const spec_kv_cache* cache, int tokens, int max_q, int n_heads) {
+  if (check_cache(cache, who) || tokens < 1 || max_q < 1 || n_heads < 1 || n_heads % cache->n_kv_heads) return 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
   cache_fields(a, cache);
   a.hq = n_heads; a.tokens = tokens; a.max_q = max_q;
   a.q_hs = a.o_hs = a.hd; a.q_ts = a.o_ts = (int64_t)n_heads * a.hd;
-  return a;
+  const size_t own = a.n_groups > 0 ? shared_bytes(a, sms) : 0;
+  return own ? (int64_t)own : (int64_t)choose_way(a, sms).td_ws;
 }
 
 int window_fields(PAttn& a, int window, int sinks, const char* who) {
@@ -226,27 +229,21 @@ int spec_attn_shared(const spec_kv_cache* cache, const void* q, int64_t q_tok_st
                          out_tok_stride, out_head_stride, lse, workspace, workspace_bytes, stream);
 }
 
-int64_t spec_attn_shared_workspace(const spec_kv_cache* cache, int n_groups, int tokens, int max_q, int n_heads) {
-  if (check_cache(cache, "spec_attn_shared_workspace") || n_groups < 1 || tokens < 1 || max_q < 1 || n_heads < 1 ||
-      n_heads % cache->n_kv_heads)
-    return 0;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  PAttn a = sized(cache, tokens, max_q, n_heads);
-  a.n_groups = n_groups;
-  const size_t own = shared_bytes(a, sms);
-  return own ? (int64_t)own : (int64_t)choose_way(a, sms).td_ws;
+int64_t spec_attn_paged_workspace(const spec_kv_cache* cache, int tokens, int max_q, int n_heads) {
+  return asked_workspace(PAttn{}, "spec_attn_paged_workspace", cache, tokens, max_q, n_heads);
 }
 
-int64_t spec_attn_paged_workspace(const spec_kv_cache* cache, int tokens, int max_q, int n_heads) {
-  if (check_cache(cache, "spec_attn_paged_workspace") || tokens < 1 || max_q < 1 || n_heads < 1 ||
-      n_heads % cache->n_kv_heads)
-    return 0;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return (int64_t)choose_way(sized(cache, tokens, max_q, n_heads), sms).td_ws;
+int64_t spec_attn_paged_window_workspace(const spec_kv_cache* cache, int tokens, int max_q, int n_heads, int window,
+                                         int sinks) {
+  PAttn a{};
+  const char* who = "spec_attn_paged_window_workspace";
+  return window_fields(a, window, sinks, who) ? 0 : asked_workspace(a, who, cache, tokens, max_q, n_heads);
+}
+
+int64_t spec_attn_shared_workspace(const spec_kv_cache* cache, int n_groups, int tokens, int max_q, int n_heads) {
+  PAttn a{};
+  a.n_groups = n_groups;
+  return n_groups < 1 ? 0 : asked_workspace(a, "spec_attn_shared_workspace", cache, tokens, max_q, n_heads);
 }
 
 int spec_attn_prompt(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* k, int64_t k_tok_stride,

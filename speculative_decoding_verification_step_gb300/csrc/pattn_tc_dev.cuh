@@ -77,6 +77,7 @@ constexpr float kTaNone = -1e30f;
 
 struct TaArgs {
   TensorMap128 qm, km, vm;
+  TensorMap128 ks, vs;   // windows: the same in boxes of 16 rows
   PAttn a;
   int tpt;          // tokens of a tile: 128 / G
   uint32_t g_mul;   // ceil(2^16 / G): r * g_mul >> 16 = r / G for r < 128
@@ -86,6 +87,7 @@ struct TaArgs {
   int split;        // 2: clusters of two blocks share an item's keys
   int by_length;    // sequences in order of their lengths (paged, at most 32)
   int box_rows;     // key rows of a K / V box
+  int take;         // blocks take over further items
 };
 
 template <int HD, bool F8>
@@ -148,7 +150,7 @@ template <int Mode>
 struct TaItemOf : TaItemBase {};
 template <>
 struct TaItemOf<kPaWindow> : TaItemBase {
-  int lo, lead, gap;  // keys below lo (but the sinks) are seen by no row; steps in front of the gap, steps left out
+  int lo, lead, gap;  // keys below lo (but the sinks) are seen by no row; place p of the walk is key p, from `lead` on p + gap
 };
 template <>
 struct TaItemOf<kPaPrefix> : TaItemBase {
@@ -177,10 +179,12 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   const int G = a.hq / a.hkv, tpt = ta.tpt;
   const int rank = ta.split > 1 ? (int)ta_cluster_rank() : 0;
   const int sinks = Mode == kPaWindow ? a.sinks : 0;
-  // First key of the item's step j, of those left.
-  auto step_key = [&](const TaItem& it, int j) {
-    if constexpr (Mode == kPaWindow) return (it.beg + j + (it.beg + j < it.lead ? 0 : it.gap)) * kTaKeys;
-    else return (it.beg + j) * kTaKeys;
+  // Key at place p of the item's walk.  Windows walk the first tokens, in runs of 16,
+  // and the window close behind them, so that both may lie in one step.  What is left
+  // out between them is whole boxes of a paged cache: a box lies within one page.
+  auto key_at = [&](const TaItem& it, int p) {
+    if constexpr (Mode == kPaWindow) return p + (p < it.lead ? 0 : it.gap);
+    else return p;
   };
   // Some row of the item may see one of the n keys from `key` on.
   [[maybe_unused]] auto reached = [&](const TaItem& it, int64_t key, int n) {
@@ -256,20 +260,19 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     it.keys = keys;
     it.first_pos = keys - n;
     it.ntile = it.tok0 + tpt < it.toks ? 2 : 1;
+    if constexpr (Mode == kPaWindow) {
+      it.lo = max(0, max(0, it.first_pos + it.tok0) - a.window + 1);
+      it.lead = (min(sinks, keys) + 15) & ~15;
+      it.gap = max(0, it.lo - it.lead);
+      if (a.paged) it.gap -= it.gap & (ta.box_rows - 1);
+    }
     int all[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {             // key steps of each tile: what its last token sees
       const int last = min(it.toks, it.tok0 + (t + 1) * tpt) - 1;
-      const int see = min(keys, max(0, it.first_pos + last + 1));
+      int see = min(keys, max(0, it.first_pos + last + 1));
+      if constexpr (Mode == kPaWindow) see = max(0, see - it.gap);
       all[t] = t < it.ntile ? (see + kTaKeys - 1) / kTaKeys : 0;
-    }
-    if constexpr (Mode == kPaWindow) {         // steps between the sinks' and the first that a row's window reaches
-      it.lo = max(0, max(0, it.first_pos + it.tok0) - a.window + 1);
-      const int first = it.lo / kTaKeys, most = min(sinks, keys);
-      it.lead = min((most + kTaKeys - 1) / kTaKeys, first);
-      it.gap = first - it.lead;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) all[t] = max(0, all[t] - it.gap);
     }
     const int total = max(all[0], all[1]);
     it.beg = total * rank / ta.split;
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t code = s_scale[rs][r];
-          const int key = step_key(it, j / 2) + r;
+          const int key = key_at(it, (it.beg + j / 2) * kTaKeys + r);
           const bool live = key < it.keys && reached(it, key, 1);
           // a row past the length, or that no row sees, is zero whatever it holds
           const float f = !live ? 0.f : row_power(code);
@@ -396,7 +399,6 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     ta_regs_less<L::other_regs>();
     if (warp == 8) {
       // ---- producer ----
-      const int per = a.paged ? kTaKeys / ta.box_rows : 1;     // boxes of a step
       constexpr int kRing = F8 ? L::raws : kS;
       uint64_t* const full = F8 ? raw_full : kv_full;
       uint64_t* const empty = F8 ? raw_empty : kv_empty;
@@ -418,41 +420,56 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
         ++loads;
         const int32_t* table = a.paged ? a.table + it.b * a.table_stride : nullptr;
         const int npages = a.paged ? (int)(((int64_t)it.keys + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
-        auto page_of = [&](int j) {   // lane b: page of box b of step j; -1 (zero rows) past the length or outside the pool
-          const int64_t key = (int64_t)step_key(it, j) + lane * ta.box_rows;
-          const int pg = (int)(key >> a.page_shift);
-          // (a box lies within one page)
-          const int page = lane < per && j < it.nst && pg < npages && reached(it, key, ta.box_rows) ? __ldg(table + pg) : -1;
+        // rows of step j's boxes; small ones where it holds first tokens and window
+        auto box_of = [&](int j) {
+          if constexpr (Mode == kPaWindow) {
+            const int at = (it.beg + j) * kTaKeys;
+            return it.gap > 0 && at < it.lead && at + kTaKeys > it.lead ? 16 : ta.box_rows;
+          } else {
+            return ta.box_rows;
+          }
+        };
+        auto box_key = [&](int j) {   // first key of box `lane`
+          if constexpr (Mode == kPaWindow) return (int64_t)key_at(it, (it.beg + j) * kTaKeys + lane * box_of(j));
+          else return (int64_t)(it.beg + j) * kTaKeys + (a.paged ? lane * ta.box_rows : 0);
+        };
+        // lane b: page of box b of step j; -1 (zero rows) past the length, outside the pool or where no row sees it
+        auto page_of = [&](int j) {
+          const int64_t key = box_key(j);
+          const int pg = (int)(key >> a.page_shift), box = box_of(j);
+          const int page = lane < kTaKeys / box && j < it.nst && pg < npages && reached(it, key, box) ? __ldg(table + pg) : -1;
           return page >= a.pages ? -1 : page;
         };
         int next = a.paged ? page_of(0) : 0;
         for (int j = 0; j < it.nst && live; ++j) {
           const int page = next;
           if (a.paged) next = page_of(j + 1);
-          const int64_t key = (int64_t)step_key(it, j) + (a.paged ? lane * ta.box_rows : 0);
+          const int64_t key = box_key(j);
           const int row = a.paged ? (it.kvh << a.page_shift) + (int)(key & ((1 << a.page_shift) - 1)) : it.kvh;
+          const int box = box_of(j), per = Mode == kPaWindow || a.paged ? kTaKeys / box : 1;
+          const bool small = Mode == kPaWindow && box < ta.box_rows;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++i) {
             const int s = i % kRing;
             if (i >= kRing) live = live && ta_wait(&empty[s], (unsigned)((i / kRing - 1) & 1), &s_abort);
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
-            const void* map = kv ? &ta.vm : &ta.km;
+            const void* map = small ? (kv ? &ta.vs : &ta.ks) : kv ? &ta.vm : &ta.km;
             if constexpr (F8) {
               const bool in = lane < per && page >= 0;
               const unsigned some = __ballot_sync(0xffffffffu, in);
               if (lane < per && !in)
-                for (int e = 0; e < ta.box_rows; e += 4) *reinterpret_cast<uint32_t*>(&s_scale[s][lane * ta.box_rows + e]) = 0x7f7f7f7fu;
+                for (int e = 0; e < box; e += 4) *reinterpret_cast<uint32_t*>(&s_scale[s][lane * box + e]) = 0x7f7f7f7fu;
               __syncwarp();
               if (lane == 0) {
-                mbar_arrive_expect_tx(&full[s], L::raw + __popc(some) * ta.box_rows);
+                mbar_arrive_expect_tx(&full[s], L::raw + __popc(some) * box);
                 s_filled = i + 1;
               }
               __syncwarp();
               if (lane < per) {
-                ta_tma_3d(raw_at + s * L::raw + lane * ta.box_rows * HD, map, 0, row, page, &full[s]);
-                if (in) bulk_g2s(&s_scale[s][lane * ta.box_rows], (kv ? a.vs : a.ks) + (int64_t)page * a.scale_stride + row,
-                                 ta.box_rows, &full[s]);
+                ta_tma_3d(raw_at + s * L::raw + lane * box * HD, map, 0, row, page, &full[s]);
+                if (in) bulk_g2s(&s_scale[s][lane * box], (kv ? a.vs : a.ks) + (int64_t)page * a.scale_stride + row,
+                                 box, &full[s]);
               }
             } else {
               if (lane == 0) {
@@ -462,7 +479,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
               __syncwarp();
               if (lane < per) {
                 for (int h = 0; h < kHalf; ++h)
-                  ta_tma_3d(kv_at + s * kTile + h * (kTile / kHalf) + lane * ta.box_rows * 128, map, h * 64, row,
+                  ta_tma_3d(kv_at + s * kTile + h * (kTile / kHalf) + lane * box * 128, map, h * 64, row,
                             a.paged ? page : it.r_first + (int)key, &full[s]);
               }
             }
@@ -550,7 +567,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           if constexpr (Hook) ok = ok && (--hook != 0 || __all_sync(0xffffffffu, ta_wait(&drained, 0, &s_abort, 0)));
           if constexpr (!F8) {
             // V's rows past the length: p is zero there, but the slots may hold anything
-            const int key0 = step_key(it, j), rows = it.keys - key0;
+            const int at = (it.beg + j) * kTaKeys;
+            int rows = it.keys - at;
+            if constexpr (Mode == kPaWindow) rows -= it.gap;
             auto clear = [&](int from, int to) {
               for (int h = 0; h < kHalf; ++h)
                 for (int e = from * 8 + lane; e < to * 8; e += 32)
@@ -561,7 +580,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
             };
             if (ok && rows < kTaKeys) clear(rows, kTaKeys);
             if constexpr (Mode == kPaWindow) {  // and those between the sinks and the windows
-              const int from = min(max(sinks - key0, 0), kTaKeys), to = min(max(it.lo - key0, 0), kTaKeys);
+              const int from = min(max(sinks - at, 0), kTaKeys), to = min(max(it.lo - it.gap - at, 0), kTaKeys);
               if (ok && from < to) clear(from, to);
             }
           }
@@ -613,7 +632,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           const bool go = ok && !__any_sync(0xffffffffu, s_abort);
           it.valid = go && part_at(it.unit, it);
         }
-        while (Mode != kPaPrefix && ok && ta.split == 1 && !__any_sync(0xffffffffu, s_abort)) {
+        const bool take = Mode == kPaCausal ? ta.split == 1 : Mode == kPaWindow && ta.take;
+        while (take && ok && !__any_sync(0xffffffffu, s_abort)) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&taken, 16);
             ta_take(&s_taken, &taken);
@@ -654,8 +674,16 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       const bool row_ok = t < it.ntile && ti < tpt && tok < it.toks;
       const int seen = row_ok ? min(it.keys, max(0, it.first_pos + tok + 1)) : 0;
       const int tile_all = min(it.keys, max(0, it.first_pos + t_at + 1));   // keys that every row sees
-      // windows: from here on every row sees what is not past it
-      [[maybe_unused]] const int tile_lo = max(0, max(0, it.first_pos + min(it.toks, t_at + tpt) - 1) - a.window + 1);
+      // windows: places from here that the row sees, [low, high) and those below `first`
+      // (rows that are none of the item's see all: they are not written)
+      [[maybe_unused]] int high = 1 << 30, low = 0, first = 0;
+      if constexpr (Mode == kPaWindow) {
+        if (row_ok) {
+          high = seen - it.gap - it.beg * kTaKeys;
+          low = high - a.window;
+          first = min(sinks, seen) - it.beg * kTaKeys;
+        }
+      }
       float m = kTaNone, l = 0.f;
       const int my = it.steps[t];
       for (int j = 0; ok && j < my; ++j, ++np) {
@@ -667,20 +695,28 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
 #pragma unroll
         for (int c = 0; c < 4; ++c) ta_ld32(s_at + 32 * c, s + 32 * c);
         ta_wait_ld();
-        const int key0 = step_key(it, j);
         if constexpr (Mode == kPaWindow) {
-          if (key0 < tile_lo && key0 + kTaKeys > sinks) {
-            const int from = sinks - key0, to = seen - a.window - key0;
+          if (__any_sync(0xffffffffu, high < kTaKeys || low > 0)) {
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t see = (below(high - 32 * w) & ~below(low - 32 * w)) | below(first - 32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(see >> c & 1u)) s[32 * w + c] = neg_inf();
+            }
+          }
+          high -= kTaKeys;
+          low -= kTaKeys;
+          first -= kTaKeys;
+        } else {
+          const int key0 = (it.beg + j) * kTaKeys;
+          if (key0 + kTaKeys > tile_all) {
+            const int lim = seen - key0;
 #pragma unroll
             for (int c = 0; c < 128; ++c)
-              if (c >= from && c < to) s[c] = neg_inf();
+              if (c >= lim) s[c] = neg_inf();
           }
-        }
-        if (key0 + kTaKeys > tile_all) {
-          const int lim = seen - key0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= lim) s[c] = neg_inf();
         }
         float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
@@ -905,17 +941,19 @@ cudaError_t launch_ta_mode(const TaArgs& ta, cudaStream_t st) {
 // The arguments of a call, but for how its items are cut; false where no tensor map can be made.
 [[maybe_unused]] bool ta_args(TaArgs& ta, const PAttn& a) {
   ta.a = a;
-  const int G = a.hq / a.hkv;
+  const int G = a.hq / a.hkv, ps = a.paged ? 1 << a.page_shift : kTaKeys;
   ta.tpt = kTaRows / G;
   ta.g_mul = (65536u + G - 1) / G;
-  const int ps = a.paged ? 1 << a.page_shift : kTaKeys;
-  ta.box_rows = std::min(ps, kTaKeys);
-  if (!ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt)) return false;
-  if (a.paged)
-    return ta_map(ta.km, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, ta.box_rows, 1, a.f8) &&
-           ta_map(ta.vm, a.v, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, ta.box_rows, 1, a.f8);
-  return ta_map(ta.km, a.k, a.hd, a.hkv, a.tokens, a.k_hs, a.k_ts, 1, kTaKeys) &&
-         ta_map(ta.vm, a.v, a.hd, a.hkv, a.tokens, a.v_hs, a.v_ts, 1, kTaKeys);
+  ta.box_rows = std::min(ps, a.window > 0 && a.paged ? 64 : kTaKeys);   // (a window's first box may be mostly in front of it)
+  auto maps = [&](TensorMap128& k, TensorMap128& v, int rows) {
+    if (a.paged)
+      return ta_map(k, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, rows, 1, a.f8) &&
+             ta_map(v, a.v, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, rows, 1, a.f8);
+    return ta_map(k, a.k, a.hd, a.hkv, a.tokens, a.k_hs, a.k_ts, 1, rows) &&
+           ta_map(v, a.v, a.hd, a.hkv, a.tokens, a.v_hs, a.v_ts, 1, rows);
+  };
+  return ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt) && maps(ta.km, ta.vm, ta.box_rows) &&
+         (a.window == 0 || maps(ta.ks, ta.vs, 16));
 }
 // Items of a causal or windowed call.
 template <int Mode>
@@ -941,6 +979,9 @@ cudaError_t launch_ta_items(const PAttn& a, int num_sms, cudaStream_t st) {
   ta.split = most * (uneven ? 1 : 2) <= num_sms && max_keys >= 16 * kTaKeys ? 2 : 1;
   // new tokens few beside their contexts: a walk's length is its sequence's
   ta.by_length = Mode == kPaCausal && a.paged && a.seqs <= 32 && max_keys >= 2LL * a.max_q ? 1 : 0;
+  // Where blocks cover the items, each keeps to its own: one that starts early would take
+  // items whose blocks find free SMs (136 items of 18 steps in a grid of 256 65 -> %TAKE% us).
+  ta.take = ta.split == 1 && (Mode == kPaCausal || most > num_sms);
   return launch_ta_mode<Mode>(ta, st);
 }
 

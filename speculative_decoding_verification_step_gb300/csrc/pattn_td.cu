@@ -78,6 +78,21 @@ struct TdLayout {
 };
 
 // Units: 128 keys of one (sequence, KV head, row tile), in that order.
+// A windowed sequence is walked over its first tokens and then from the first key that
+// its first new token's window reaches, with whole boxes (pages, or halves of 256) left
+// out between them: place p of the walk is key p, from `lead` on p + gap.
+struct TdWalk {
+  int lo, lead, gap;   // keys below lo, but the sinks, are seen by no row
+};
+SV_DEV TdWalk td_walk(const PAttn& a, int keys, int first_pos) {
+  const int box = min(1 << a.page_shift, kTdKeys);
+  TdWalk w;
+  w.lo = max(0, max(0, first_pos) - a.window + 1);
+  w.lead = (min(a.sinks, keys) + box - 1) & -box;
+  w.gap = max(0, w.lo - w.lead) & -box;
+  return w;
+}
+template <int Mode>
 SV_DEV int td_seq_units(const PAttn& a, int tile_rows, int b, int* tiles) {
   const int r_first = __ldg(a.cu + b), n = __ldg(a.cu + b + 1) - r_first;
   int keys = __ldg(a.lens + b);
@@ -85,14 +100,16 @@ SV_DEV int td_seq_units(const PAttn& a, int tile_rows, int b, int* tiles) {
   if (r_first < 0 || n <= 0 || n > a.tokens - r_first) return 0;
   keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
   *tiles = (min(n, a.max_q) * (a.hq / a.hkv) + tile_rows - 1) / tile_rows;
+  if constexpr (Mode == kPaWindow) keys -= td_walk(a, keys, keys - n).gap;
   return max(1, (keys + kTdKeys - 1) / kTdKeys);   // a tile without keys is still written
 }
+template <int Mode>
 SV_DEV int td_total(const PAttn& a, int tile_rows) {   // units of the call; whole warps
   int sum = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 32) {
     const int b = b0 + (threadIdx.x & 31);
     int tiles = 0;
-    const int per = b < a.seqs ? td_seq_units(a, tile_rows, b, &tiles) : 0;
+    const int per = b < a.seqs ? td_seq_units<Mode>(a, tile_rows, b, &tiles) : 0;
     sum += per * tiles * a.hkv;
   }
 #pragma unroll
@@ -104,13 +121,14 @@ SV_DEV int td_begin(int total, int run, int runs) { return (int)((int64_t)total 
 struct TdUnit {
   int b, kvh, tile, off, upi;
 };
+template <int Mode>
 SV_DEV TdUnit td_find(const PAttn& a, int tile_rows, int u) {   // unit u; whole warps
   TdUnit w{};
   int before = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 32) {
     const int lane = threadIdx.x & 31, b = b0 + lane;
     int tiles = 0;
-    const int per = b < a.seqs ? td_seq_units(a, tile_rows, b, &tiles) : 0;
+    const int per = b < a.seqs ? td_seq_units<Mode>(a, tile_rows, b, &tiles) : 0;
     const int own = per * tiles * a.hkv;
     int sum = own;
 #pragma unroll
@@ -136,22 +154,37 @@ SV_DEV TdUnit td_find(const PAttn& a, int tile_rows, int u) {   // unit u; whole
 }
 
 // A part of a tile that a run holds: units off .. off + seg - 1 of upi.
-struct TdPart {
+struct TdPartBase {
   int b, kvh, tile, tiles, off, seg, upi;
   int r_first, rows, row0, keys, first_pos;
 };
-SV_DEV void td_seq(const PAttn& a, int tile_rows, TdPart& p) {   // sequence p.b
-  p.upi = td_seq_units(a, tile_rows, p.b, &p.tiles);
+template <int Mode>
+struct TdPartOf : TdPartBase {};
+template <>
+struct TdPartOf<kPaWindow> : TdPartBase {
+  TdWalk walk;
+};
+// Key at place p of the part's walk.
+template <int Mode>
+SV_DEV int td_key(const TdPartOf<Mode>& w, int p) {
+  if constexpr (Mode == kPaWindow) return p + (p < w.walk.lead ? 0 : w.walk.gap);
+  else return p;
+}
+template <int Mode>
+SV_DEV void td_seq(const PAttn& a, int tile_rows, TdPartOf<Mode>& p) {   // sequence p.b
+  p.upi = td_seq_units<Mode>(a, tile_rows, p.b, &p.tiles);
   p.r_first = __ldg(a.cu + p.b);
   const int n = __ldg(a.cu + p.b + 1) - p.r_first, keys = __ldg(a.lens + p.b);
   p.keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
   p.rows = min(n, a.max_q) * (a.hq / a.hkv);
   p.first_pos = p.keys - n;
+  if constexpr (Mode == kPaWindow) p.walk = td_walk(a, p.keys, p.first_pos);
 }
 // The run's first part (whole warps), and the one that starts at unit u behind p.
-SV_DEV TdPart td_first(const PAttn& a, int tile_rows, int u, int u_end) {
-  const TdUnit w = td_find(a, tile_rows, u);
-  TdPart p;
+template <int Mode>
+SV_DEV TdPartOf<Mode> td_first(const PAttn& a, int tile_rows, int u, int u_end) {
+  const TdUnit w = td_find<Mode>(a, tile_rows, u);
+  TdPartOf<Mode> p;
   p.b = w.b;
   td_seq(a, tile_rows, p);
   p.kvh = w.kvh;
@@ -161,7 +194,8 @@ SV_DEV TdPart td_first(const PAttn& a, int tile_rows, int u, int u_end) {
   p.seg = min(p.upi - p.off, u_end - u);
   return p;
 }
-SV_DEV void td_next(const PAttn& a, int tile_rows, TdPart& p, int u, int u_end) {
+template <int Mode>
+SV_DEV void td_next(const PAttn& a, int tile_rows, TdPartOf<Mode>& p, int u, int u_end) {
   if (u >= u_end) return;
   p.off = 0;
   if (++p.tile >= p.tiles) {
@@ -178,9 +212,10 @@ SV_DEV void td_next(const PAttn& a, int tile_rows, TdPart& p, int u, int u_end) 
   p.seg = min(p.upi, u_end - u);
 }
 
-template <int HD, int R>
+template <int HD, int R, int Mode>
 __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_constant__ TdArgs ta) {
   using L = TdLayout<HD, R>;
+  using TdPart = TdPartOf<Mode>;
   constexpr int C = L::cols, kHalf = HD / 64;
   constexpr int kSc = 8;                                   // K scales wait for the softmax, behind the ring
   extern __shared__ __align__(1024) unsigned char tsm[];
@@ -195,7 +230,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
   const PAttn& a = ta.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.hq / a.hkv;
-  const int total = td_total(a, ta.rows), runs = td_runs(total, ta.runs);
+  const int total = td_total<Mode>(a, ta.rows), runs = td_runs(total, ta.runs);
   if ((int)blockIdx.x >= runs || total == 0) return;
   const int u_beg = td_begin(total, blockIdx.x, runs), u_end = td_begin(total, blockIdx.x + 1, runs);
   const uint32_t base = (smem_u32(tsm) + 1023u) & ~1023u;
@@ -312,7 +347,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
     const int r = threadIdx.x & 127, s = (warp - 8) >> 2;   // a group of warps takes every other unit
     int i = 0, last = -1;                    // units of all parts, the last of this group
     bool ok = true;
-    TdPart w = td_first(a, ta.rows, u_beg, u_end);
+    TdPart w = td_first<Mode>(a, ta.rows, u_beg, u_end);
     int k = 0;
     ok = stage(w, 0, warp - 8);
     for (int u = u_beg; ok && u < u_end;) {
@@ -336,8 +371,10 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&v_empty[rs]);
         if (i >= 2) ok = __all_sync(0xffffffffu, ta_wait(&b_empty[s], (unsigned)((i / 2 - 1) & 1), &s_abort));
         if (!ok) break;
-        // a row past the length is zero whatever it holds
-        const bool dead = (w.off + j) * kTdKeys + r >= w.keys;
+        // a row past the length, or that no row sees, is zero whatever it holds
+        const int key = td_key(w, (w.off + j) * kTdKeys + r);
+        bool dead = key >= w.keys;
+        if constexpr (Mode == kPaWindow) dead = dead || (key < w.walk.lo && key >= a.sinks);
         if (__any_sync(0xffffffffu, dead)) {
 #pragma unroll
           for (int c = 0; c < HD / 16; ++c)
@@ -381,15 +418,20 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
       const int box_shift = min(a.page_shift, 7);       // keys of a unit from one page
       int i = 0;
       bool live = true;
-      TdPart w = td_first(a, ta.rows, u_beg, u_end);
+      TdPart w = td_first<Mode>(a, ta.rows, u_beg, u_end);
       for (int u = u_beg; live && u < u_end; td_next(a, ta.rows, w, u, u_end)) {
         u += w.seg;
         const int32_t* table = a.table + w.b * a.table_stride;
         const int npages = (int)(((int64_t)w.keys + (1 << a.page_shift) - 1) >> a.page_shift);
         auto page_of = [&](int j) {   // lane x: page of box x of unit j; -1 (zero rows) past the length or outside the pool
-          const int64_t key = (int64_t)(w.off + j) * kTdKeys + (lane << box_shift);
+          int64_t key = (int64_t)(w.off + j) * kTdKeys + (lane << box_shift);
+          bool some = true;                   // some row sees one of the box's keys
+          if constexpr (Mode == kPaWindow) {
+            key += key < w.walk.lead ? 0 : w.walk.gap;
+            some = key + (1 << box_shift) > w.walk.lo || key < a.sinks;
+          }
           const int pg = (int)(key >> a.page_shift);
-          const int page = lane < kTdKeys >> box_shift && j < w.seg && pg < npages ? __ldg(table + pg) : -1;
+          const int page = lane < kTdKeys >> box_shift && j < w.seg && pg < npages && some ? __ldg(table + pg) : -1;
           return page >= a.pages ? -1 : page;
         };
         int next = page_of(0);
@@ -399,7 +441,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
           if (i >= n) live = __all_sync(0xffffffffu, ta_wait(&empties[s], (unsigned)((i / n - 1) & 1), &s_abort));
           if (!live) break;
           const uint32_t dst = ring + s * L::tile;
-          const int row0 = (w.kvh << a.page_shift) + (int)(((int64_t)(w.off + j) * kTdKeys) & ((1 << a.page_shift) - 1));
+          const int row0 = (w.kvh << a.page_shift) + (td_key(w, (w.off + j) * kTdKeys) & ((1 << a.page_shift) - 1));
           if (lane == 0) mbar_arrive_expect_tx(&fulls[s], L::tile);
           __syncwarp();
           const int per = kTdKeys >> box_shift;
@@ -433,7 +475,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
       };
       int i = 0, k = 0;                         // units and tiles done
       bool ok = true;
-      TdPart w = td_first(a, ta.rows, u_beg, u_end);
+      TdPart w = td_first<Mode>(a, ta.rows, u_beg, u_end);
       for (int u = u_beg; ok && u < u_end; ++k, td_next(a, ta.rows, w, u, u_end)) {
         u += w.seg;
         if (warp == 5) {
@@ -495,7 +537,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
     };
     int i = 0, k = 0;
     bool ok = true;                           // the same in all softmax threads
-    TdPart w = td_first(a, ta.rows, u_beg, u_end);
+    TdPart w = td_first<Mode>(a, ta.rows, u_beg, u_end);
     for (int u = u_beg; u < u_end; ++k, td_next(a, ta.rows, w, u, u_end)) {
       const bool whole = w.off == 0 && w.seg == w.upi;
       const int piece = w.off > 0 ? 0 : 1;
@@ -511,6 +553,8 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
       }
       const int last_row = min(w.rows, w.row0 + ta.rows) - 1;
       const int see_all = w.first_pos + w.row0 / G + 1;       // keys that every row sees
+      // windows: from here on they see what is not past them
+      [[maybe_unused]] const int lo_all = max(0, max(0, w.first_pos + last_row / G) - a.window + 1);
       for (int j = 0; j < w.seg && ok; ++j, ++i) {
         got = __all_sync(0xffffffffu, got && ta_wait(&s_full[i & 3], (unsigned)((i / 4) & 1), &s_abort));
         ta_fence_after();
@@ -525,7 +569,18 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
           const uint64_t kk = ta_pair(kf, kf);
 #pragma unroll
           for (int r = 0; r < R; r += 2) ta_split(ta_mul2(ta_pair(s[r], s[r + 1]), kk), s[r], s[r + 1]);
-          if ((w.off + j + 1) * kTdKeys > see_all) {
+          if constexpr (Mode == kPaWindow) {
+            const int p = (w.off + j) * kTdKeys;
+            if (p + kTdKeys > see_all - w.walk.gap || p < lo_all - w.walk.gap) {
+              // row w.row0 + r sees the key from token key - first_pos on, until its window leaves it behind
+              const int key = td_key(w, p + tid), ago = key - w.first_pos;
+              const int from = key >= w.keys ? 0x7fffffff : max(ago, 0) * G - w.row0;
+              const int to = key < a.sinks ? 0x7fffffff : min(max(ago + a.window, 0), 1 << 16) * G - w.row0;
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+                if (r < from || r >= to) s[r] = neg_inf();
+            }
+          } else if ((w.off + j + 1) * kTdKeys > see_all) {
             // row w.row0 + r sees the key from token key - first_pos on
             const int key = (w.off + j) * kTdKeys + tid;
             const int from = key >= w.keys ? 0x7fffffff : (key - w.first_pos) * G - w.row0;
@@ -714,12 +769,12 @@ __global__ void __launch_bounds__(kTdThreads, 1) pattn_td_kernel(const __grid_co
 
 // Joins the parts of the tile that the border before run x + 1 cuts, if it is
 // the first border inside that tile.  A warp a row: rows 4 y .. 4 y + 3.
-template <int HD>
+template <int HD, int Mode>
 __global__ void __launch_bounds__(128) pattn_join_kernel(const __grid_constant__ PAttn a, int tile_rows, int cols, int most) {
-  const int total = td_total(a, tile_rows), runs = td_runs(total, most), c0 = blockIdx.x;
+  const int total = td_total<Mode>(a, tile_rows), runs = td_runs(total, most), c0 = blockIdx.x;
   if (c0 + 1 >= runs) return;
   const int u = td_begin(total, c0 + 1, runs);
-  const TdUnit w = td_find(a, tile_rows, u);
+  const TdUnit w = td_find<Mode>(a, tile_rows, u);
   if (w.off == 0) return;                      // the border lies between tiles
   const int first = u - w.off;
   if (td_begin(total, c0, runs) > first) return;   // an earlier border cuts it too
@@ -767,15 +822,24 @@ __global__ void __launch_bounds__(128) pattn_join_kernel(const __grid_constant__
     a.lse[(int64_t)(r_first + t) * a.hq + h] = ll == 0.f ? neg_inf() : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
-template <int HD, int R>
+template <int HD, int R, int Mode>
 cudaError_t launch_td(const TdArgs& ta, cudaStream_t st) {
   using L = TdLayout<HD, R>;
-  auto kern = pattn_td_kernel<HD, R>;
-  cudaError_t e = launch_rows_smem(std::integral_constant<int, HD * 100 + R>(), kern, dim3((unsigned)ta.runs),
+  auto kern = pattn_td_kernel<HD, R, Mode>;
+  cudaError_t e = launch_rows_smem(std::integral_constant<int, Mode * 100000 + HD * 100 + R>(), kern, dim3((unsigned)ta.runs),
                                    dim3(kTdThreads), L::smem, 1, st, ta);
   if (e != cudaSuccess || ta.runs < 2) return e;
-  return launch_rows(pattn_join_kernel<HD>, dim3((unsigned)ta.runs - 1, (ta.rows + 3) / 4), dim3(128), 0, 1, st, ta.a, ta.rows, R,
+  return launch_rows(pattn_join_kernel<HD, Mode>, dim3((unsigned)ta.runs - 1, (ta.rows + 3) / 4), dim3(128), 0, 1, st, ta.a, ta.rows, R,
                      ta.runs);
+}
+
+template <int Mode>
+cudaError_t launch_td_rows(const TdArgs& ta, int r, cudaStream_t st) {
+  if (ta.a.hd == 128)
+    return r == 16   ? launch_td<128, 16, Mode>(ta, st)
+           : r == 24 ? launch_td<128, 24, Mode>(ta, st)
+                     : launch_td<128, 32, Mode>(ta, st);
+  return r == 16 ? launch_td<64, 16, Mode>(ta, st) : r == 24 ? launch_td<64, 24, Mode>(ta, st) : launch_td<64, 32, Mode>(ta, st);
 }
 
 // Rows that a call's tiles are worked on with: even tiles of at most 32.
@@ -805,8 +869,7 @@ cudaError_t launch_pattn_td(const PAttn& a, int num_sms, cudaStream_t st) {
   if (!ta_map(ta.km, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, box, 1, 1) ||
       !ta_map(ta.vm, a.v, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, box, 1, 1))
     return cudaErrorInvalidValue;
-  if (a.hd == 128) return r == 16 ? launch_td<128, 16>(ta, st) : r == 24 ? launch_td<128, 24>(ta, st) : launch_td<128, 32>(ta, st);
-  return r == 16 ? launch_td<64, 16>(ta, st) : r == 24 ? launch_td<64, 24>(ta, st) : launch_td<64, 32>(ta, st);
+  return a.window > 0 ? launch_td_rows<kPaWindow>(ta, r, st) : launch_td_rows<kPaCausal>(ta, r, st);
 }
 
 }  // namespace sv

@@ -52,22 +52,20 @@ def _ref(q, ks, vs, see, scale):
 
 def _evict(cache, ns, ctx, window, sinks):
     """What no row of the chunks sees becomes NaN; whole pages of it leave the table."""
-    ps = cache.page_size
+    ps, c_table = cache.page_size, cache.table.long()
     for b, (n, c) in enumerate(zip(ns, ctx)):
         if not n or not c:
             continue
         lo = max(0, max(0, c - n) - window + 1)
-        for j in range(min(sinks, c), lo):
-            page = int(cache.table[b, j // ps])
-            if page < 0:
-                continue
-            if (j // ps) * ps >= sinks and (j // ps + 1) * ps <= lo:
-                cache.table[b, j // ps] = -1
-                continue
-            for t in (cache.k, cache.v):
-                t[page, :, j % ps] = math.nan if t.dtype is torch.bfloat16 else t[page, :, j % ps]
-            if cache.k_scale is not None:
-                cache.k_scale[page, :, j % ps] = cache.v_scale[page, :, j % ps] = 255
+        j = torch.arange(min(sinks, lo), lo, device="cuda")
+        page, slot = c_table[b, j // ps], j % ps
+        for t in (cache.k, cache.v):
+            if t.dtype is torch.bfloat16:
+                t[page, :, slot] = math.nan
+        if cache.k_scale is not None:
+            cache.k_scale[page, :, slot] = cache.v_scale[page, :, slot] = 255
+        p = torch.arange(cache.max_pages, device="cuda")
+        cache.table[b].masked_fill_((p * ps >= sinks) & ((p + 1) * ps <= lo), -1)
 
 
 def _window_check(c, q, cu, lens, ns, ctx, window, sinks, values, max_q=None):
@@ -124,6 +122,32 @@ def test_window_paged(hq, hk, hd, ps, ns, ctx, window, sinks, dtype):
     n = sum(ns)
     assert torch.equal(again[0][:n], b[0][:n]) and torch.equal(again[1][:n], b[1][:n])
     assert a[0].shape == b[0].shape
+
+
+LONG = [  # few rows over long windows of 8-bit keys
+    (32, 8, 128, 16, [6] * 24, [2500 + 37 * i for i in range(24)], 2100, 4),
+    (32, 8, 128, 64, [4, 6, 5, 1] * 6, [3000 - 41 * i for i in range(24)], 2048, 130),
+    (16, 4, 64, 32, [6, 3], [30000, 9000], 17000, 5),
+    (16, 4, 128, 16, [8], [40000], 20001, 0),
+    (4, 2, 128, 256, [16, 2], [20000, 18000], 17000, 300),
+    (16, 2, 64, 16, [1, 2], [40000, 16500], 16400, 1),
+]
+
+
+@pytest.mark.parametrize("hq,hk,hd,ps,ns,ctx,window,sinks", LONG)
+def test_window_few_rows_long(hq, hk, hd, ps, ns, ctx, window, sinks):
+    c, q, cu, lens = _paged_case(sum(ctx), hq, hk, hd, ps, "e4m3", ns, ctx, pad=1)
+    n = sum(ns)
+    assert sv.lib().spec_attn_paged_window_workspace(c._ref, n + 1, max(ns), hq, window, sinks) > 0
+    values = _all_values(c, ctx)
+    _evict(c, ns, ctx, window, sinks)
+    a = _window_check(c, q, cu, lens, ns, ctx, window, sinks, values, max_q=max(ns))
+    for _ in range(3):
+        again = sv.attn_paged(q, c, cu, lens, max_q=max(ns), window=window, sinks=sinks)
+        assert torch.equal(again[0][:n], a[0][:n]) and torch.equal(again[1][:n], a[1][:n])
+    if n < 30:
+        rows = q[:n]
+        _give_up(lambda o, l: sv.attn_paged(rows, c, cu, lens, max_q=max(ns), out=o, lse=l, window=window, sinks=sinks), rows, (1, 3))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
