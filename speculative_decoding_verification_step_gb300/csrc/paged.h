@@ -109,7 +109,8 @@ struct PAttn {
   int window, sinks;             // a row sees the last `window` keys up to its own (0: all) and keys below `sinks`
   const int32_t* groups;         // shared prefixes: [n_groups + 1] first sequences (null: one group of all)
   const int32_t* shared;         // [n_groups] positions whose pages a group's rows of the table all name
-  int n_groups;
+  int n_groups, runs;            // most runs that share a prefix's units
+  float* rest;                   // [tokens][hq] sums of head_dim, then references and sums of what lies behind the prefixes
   int give_up;                   // test hook: the step of a tensor-memory block that waits for what never comes (0: none)
 };
 // What a row of the attention kernels sees of the keys up to its own position.
@@ -120,7 +121,7 @@ enum PaMode {
   kPaPrefix = 3    // tensor memory only: parts of a group's shared prefix, seen whole by all of the group's rows
 };
 // A group of sequences as the prefix's kernels see it (worked out on the device).
-struct ShGroup {
+struct __align__(16) ShGroup {
   int eff;         // shared positions that all rows of the group see
   int unit0;       // its first unit: 128 keys of one (KV head, pair of row tiles)
   int tile0;       // its first (KV head, pair of row tiles)
@@ -128,20 +129,29 @@ struct ShGroup {
   int seq0;        // the sequence whose table row is read
   int pairs, steps;
 };
-// The prefix's workspace: the units and the runs that share them, the groups, then slots
-// [2][head_dim / 4][128] of four sums, [256] of a reference and a sum.  Run r's part of
+// What a sequence shares with its group (eff 0: nothing), for the rest and the join.
+struct __align__(16) ShSeq {
+  int eff, row0, unit0, tile0, pairs, steps, pad[2];
+};
+// The prefix's workspace: the units and the runs that share them, the groups, the sequences,
+// then slots [256 rows][head_dim] of sums, [256] of a reference and a sum.  Run r's part of
 // (KV head, pair) tile i lies in slot r + i: along the runs either grows by one.
-struct ShPlan {
+struct __align__(16) ShPlan {
   int units, runs, pad[6];
 };
-inline size_t sh_slots_at(int n_groups) { return (sizeof(ShPlan) + (size_t)n_groups * sizeof(ShGroup) + 255) & ~(size_t)255; }
-SV_DEV int sh_run(int unit, int units, int runs) {   // the run of a unit; run r begins at units * r / runs
-  return (int)((((int64_t)unit + 1) * runs - 1) / units);
+__host__ __device__ inline size_t sh_slots_at(int n_groups, int seqs) {
+  return (sizeof(ShPlan) + (size_t)n_groups * sizeof(ShGroup) + (size_t)seqs * sizeof(ShSeq) + 255) & ~(size_t)255;
 }
-SV_DEV const float* sh_slot(const float* ws, int n_groups, int hd, int slot) {
-  return reinterpret_cast<const float*>(reinterpret_cast<const unsigned char*>(ws) +
-                                        ((sizeof(ShPlan) + (size_t)n_groups * sizeof(ShGroup) + 255) & ~(size_t)255)) +
-         (size_t)slot * 256 * (hd + 2);
+SV_DEV int sh_run(int unit, int units, int runs) {   // the run of a unit; run r begins at units * r / runs
+  const uint64_t n = ((uint64_t)unit + 1) * runs - 1;
+  return n >> 32 ? (int)(n / (uint32_t)units) : (int)((uint32_t)n / (uint32_t)units);
+}
+SV_DEV ShGroup* sh_groups(const float* ws) {
+  return reinterpret_cast<ShGroup*>(reinterpret_cast<ShPlan*>(const_cast<float*>(ws)) + 1);
+}
+SV_DEV ShSeq* sh_seqs(const float* ws, int n_groups) { return reinterpret_cast<ShSeq*>(sh_groups(ws) + n_groups); }
+SV_DEV float* sh_slot(const float* ws, int n_groups, int seqs, int hd, int slot) {
+  return const_cast<float*>(ws) + sh_slots_at(n_groups, seqs) / sizeof(float) + (size_t)slot * 256 * (hd + 2);
 }
 // SPEC_FAULT_ATTN_TIMEOUT: give_up of the calls from now on.
 extern std::atomic<int> g_attn_give_up;
@@ -155,7 +165,7 @@ cudaError_t launch_pattn_tc(const PAttn& a, int num_sms, cudaStream_t st);
 cudaError_t launch_pattn_tc_window(const PAttn& a, int num_sms, cudaStream_t st);
 cudaError_t launch_pa_window(const PAttn& a, int num_sms, cudaStream_t st);
 // Sequences behind shared prefixes: the prefixes on tensor memory in equal runs over all SMs,
-// then each sequence's rest in register tiles, which join the parts.  Head dim 64 or 128, up to
+// each sequence's rest in register tiles, and a join of the parts.  Head dim 64 or 128, up to
 // kPaMaxRows rows per KV head of a sequence, a.ws of pattn_shared_workspace bytes (0: not supported).
 size_t pattn_shared_workspace(const PAttn& a, int num_sms);
 cudaError_t launch_pattn_shared(const PAttn& a, int num_sms, cudaStream_t st);

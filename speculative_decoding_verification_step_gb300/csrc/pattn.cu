@@ -78,11 +78,24 @@ Way choose_way(const PAttn& a, int sms) {
   return {false, td_bytes(a, rows, sms)};
 }
 
-// Workspace of launch_pattn_shared where it is taken, else 0.
+// Workspace of launch_pattn_shared where it is taken, else 0.  Its four launches cost
+// some 20 us, and sequences that read the same pages one by one find them in L2: it is
+// taken where they would read 800 thousand rows of keys (positions x KV heads) again, for
+// more than 8 rows per KV head, whose walk costs more, 260 thousand, 450 at head dim 64, and
+// beyond 32 rows, where what lies behind the prefix weighs more, 2048 positions at least.
+// The lengths being on the device, a table's width stands for them.  One by one / shared,
+// us, 8 KV heads, 100 positions behind the prefix.  4 rows, bf16, head dim 128: 8
+// sequences x 8192 26 / 29, 16 x 8192 39 / 29, 64 x 2048 51 / 28, 64 x 8192 168 / 37, 4 x
+// 32768 45 / 50; e4m3: 8 x 8192 29 / 36, 16 x 8192 50 / 35; head dim 64, bf16: 8 x 8192
+// 16 / 28, 16 x 8192 26 / 26.  24 rows, bf16, head dim 128: 4 x 8192 28 / 35, 8 x 8192
+// 47 / 39, 64 x 512 36 / 42, 64 x 2048 90 / 50; e4m3: 8 x 8192 58 / 42, 64 x 8192
+// 288 / 92; head dim 64, bf16: 8 x 8192 27 / 30, 16 x 8192 38 / 36.  64 rows, bf16: 4 x
+// 8192 46 / 43, 16 x 2048 36 / 38, 64 x 512 45 / 77, 64 x 2048 125 / 98.
 size_t shared_bytes(const PAttn& a, int sms) {
-  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv);
-  if (rows < 1 || rows > kPaMaxRows || a.seqs <= a.n_groups) return 0;
-  return pattn_shared_workspace(a, sms);
+  const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * (a.hq / a.hkv), keys = (int64_t)a.max_pages << a.page_shift;
+  if (rows < 1 || rows > kPaMaxRows || a.seqs <= a.n_groups || (rows > 32 && keys < 2048)) return 0;
+  const int64_t least = rows <= 8 ? 800000 : a.hd == 128 ? 260000 : 450000;
+  return (double)(a.seqs - a.n_groups) * (double)keys * a.hkv < (double)least ? 0 : pattn_shared_workspace(a, sms);
 }
 
 // All attention calls, after their own checks.

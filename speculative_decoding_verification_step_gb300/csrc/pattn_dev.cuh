@@ -58,7 +58,6 @@
 
 #include "common.cuh"
 #include "paged.h"
-#include "shared_dev.cuh"
 
 namespace sv {
 
@@ -167,56 +166,6 @@ SV_DEV float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
-// The group of sequence b, and the positions that its rows share with the group's others:
-// as many as the call says, cut to what all rows of the group see.  Called by whole blocks.
-struct ShOwn {
-  int eff, group, toks_end, row0;
-};
-SV_DEV ShOwn sh_own(const PAttn& a, int b, int r_first, int n) {
-  __shared__ int s_group, s_least;
-  if (threadIdx.x == 0) {
-    s_group = a.groups ? 0x7fffffff : 0;
-    s_least = 0x7fffffff;
-  }
-  __syncthreads();
-  if (a.groups)
-    for (int g = threadIdx.x; g < a.n_groups; g += blockDim.x)
-      if (__ldg(a.groups + g) <= b && b < __ldg(a.groups + g + 1)) atomicMin(&s_group, g);
-  __syncthreads();
-  ShOwn o{0, s_group, 0, 0};
-  if (o.group == 0x7fffffff) return o;
-  const int first = a.groups ? __ldg(a.groups + o.group) : 0, last = a.groups ? __ldg(a.groups + o.group + 1) : a.seqs;
-  const int least = sh_least(a, first, last);
-  if (least < 0x7fffffff) atomicMin(&s_least, least);
-  __syncthreads();
-  const ShRows r = sh_rows(a, first, last);
-  o.eff = r.toks > 0 ? sh_eff(a, o.group, s_least) : 0;
-  o.row0 = r.row0;
-  if (r_first < r.row0 || r_first + n > r.row0 + r.toks) o.eff = 0;   // (no order in cu)
-  return o;
-}
-// Adds the parts that the runs left of row `tok`, head `h` of KV head kvh (dims col .. col + 3).
-template <int HD>
-SV_DEV void sh_join(const PAttn& a, const ShOwn& own, int kvh, int tok, int h, int col, float4& x, float& mm, float& ll) {
-  if (own.eff == 0) return;
-  const volatile ShPlan* plan = reinterpret_cast<const volatile ShPlan*>(a.ws);
-  const volatile ShGroup* gr = reinterpret_cast<const volatile ShGroup*>(plan + 1) + own.group;
-  const int units = plan->units, runs = plan->runs, pairs = gr->pairs, steps = gr->steps;
-  if (steps == 0) return;
-  const int G = a.hq / a.hkv, tpt = 128 / G, t = tok - own.row0, pair = t / (2 * tpt), in = t - pair * 2 * tpt;
-  const int half = in / tpt, r = (in - half * tpt) * G + h, tile = kvh * pairs + pair, u0 = gr->unit0 + tile * steps;
-  const int last = sh_run(u0 + steps - 1, units, runs);
-  for (int run = sh_run(u0, units, runs); run <= last; ++run) {
-    const float* slot = sh_slot(a.ws, a.n_groups, HD, run + gr->tile0 + tile);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(slot) + (half * (HD / 4) + col / 4) * 128 + r);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot + 256 * HD) + half * 128 + r);
-    const float to = fmaxf(mm, ml.x), f1 = exp2_fast(mm - to), f2 = exp2_fast(ml.x - to);
-    x.x = x.x * f1 + y.x * f2; x.y = x.y * f1 + y.y * f2; x.z = x.z * f1 + y.z * f2; x.w = x.w * f1 + y.w * f2;
-    ll = ll * f1 + ml.y * f2;
-    mm = to;
-  }
-}
-
 // Block x: tile (x / C) % tpq of sequence (x / C) / tpq, share x % C of its
 // keys; y: KV head.
 template <int HD, bool F8, int NT, int Mode>
@@ -231,18 +180,27 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
   const int share = blockIdx.x % C, item = blockIdx.x / C;
   const int b = item / tpq, tile = item - b * tpq, kvh = blockIdx.y;
   const int G = a.hq / a.hkv;
+  if constexpr (Mode == kPaRest) {
+    pdl_trigger();
+    if (b >= a.seqs) {                         // (the last blocks of the grid)
+      // the prefix kernel in front is still at work: one block stays until it is done, so
+      // that what waits for this kernel waits for both
+      if (share == 0 && kvh == 0) pdl_wait();
+      return;
+    }
+  }
 
   // the sequence's rows and keys (every block of a cluster sees the same)
+  // (The plan is done: the prefix kernel waited for it before it let this one begin.)
+  [[maybe_unused]] const int shared = Mode == kPaRest ? __ldcg(&sh_seqs(a.ws, a.n_groups)[b].eff) : 0;
   const int r_first = __ldg(a.cu + b);
   const int n = __ldg(a.cu + b + 1) - r_first;
   int keys = a.paged ? __ldg(a.lens + b) : n;
-  // (a block that leaves early still waits for the kernel in front: the one behind may count on both)
-  const auto leave = [] { if constexpr (Mode == kPaRest) pdl_wait(); };
-  if (r_first < 0 || n <= 0 || n > a.tokens - r_first) return leave();
+  if (r_first < 0 || n <= 0 || n > a.tokens - r_first) return;
   if (a.paged) keys = keys < 0 ? 0 : (int)min((int64_t)keys, (int64_t)a.max_pages << a.page_shift);
   const int rows = min(n, a.max_q) * G;       // rows that are computed
   const int row0 = tile * kRows;
-  if (row0 >= rows) return leave();
+  if (row0 >= rows) return;
   const int first_pos = keys - n;             // position of the sequence's row 0
   const int last_row = min(rows, row0 + kRows) - 1;
   const int see_max = min(keys, max(0, first_pos + last_row / G + 1));   // keys that any row of the tile sees
@@ -251,7 +209,6 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
   // the `sinks` first; from lo_max on by all that are not behind them.
   int lo_min = 0, lo_max = 0, lead = 0, gap = 0;   // steps before the gap, steps left out
   const int sinks = Mode == kPaWindow ? a.sinks : 0;
-  [[maybe_unused]] ShOwn own{};
   if constexpr (Mode == kPaWindow) {
     lo_min = max(0, max(0, first_pos + row0 / G) - a.window + 1);
     lo_max = max(0, max(0, first_pos + last_row / G) - a.window + 1);
@@ -259,9 +216,8 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
     gap = lo_min / kPaStep - lead;
   }
   if constexpr (Mode == kPaRest) {
-    own = sh_own(a, b, r_first, n);
-    lo_min = lo_max = own.eff;
-    gap = own.eff / kPaStep;
+    lo_min = lo_max = shared;
+    gap = lo_min / kPaStep;
   }
   const auto step_key = [&](int s) { return (s + (s < lead ? 0 : gap)) * kPaStep; };
 
@@ -577,7 +533,12 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
   const int col = (tid % kLpr) * 4;
   auto write_row = [&](int r, float4 x, float mm, float ll) {
     const int R = row0 + r, t = R / G, h = kvh * G + R - t * G;
-    if constexpr (Mode == kPaRest) sh_join<HD>(a, own, kvh, r_first + t, R - t * G, col, x, mm, ll);
+    if constexpr (Mode == kPaRest) {           // sums as they are, for the join
+      const size_t at = (size_t)(r_first + t) * a.hq + h;
+      __stcg(reinterpret_cast<float4*>(a.rest + at * HD + col), x);
+      if (col == 0) __stcg(reinterpret_cast<float2*>(a.rest + (size_t)a.tokens * a.hq * HD) + at, make_float2(mm, ll));
+      return;
+    }
     const float f = ll > 0.f || !(ll == ll) ? 1.f / ll : 0.f;
     bf16* d = (bf16*)a.out + (int64_t)(r_first + t) * a.o_ts + (int64_t)h * a.o_hs + col;
     *reinterpret_cast<uint2*>(d) = make_uint2(pa_pack(x.x * f, x.y * f), pa_pack(x.z * f, x.w * f));
@@ -585,7 +546,6 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
       a.lse[(int64_t)(r_first + t) * a.hq + h] = ll == 0.f ? neg_inf() : (mm + log2f(ll)) * 0.6931471805599453f;
   };
   const int live = min(kRows, rows - row0);
-  if constexpr (Mode == kPaRest) pdl_wait();   // the prefix's parts
   for (int r = tid / kLpr; r < live; r += kPaThreads / kLpr) {
     float mm = kPaNone, ll = 0.f;
 #pragma unroll
@@ -644,8 +604,9 @@ cudaError_t launch_pa(const PAttn& a, int64_t rows, int tpq, int num_sms, cudaSt
   int C = 1;
   while (C < 8 && C * 2 <= room && max_keys >= 128 * C) C *= 2;
   if (C == 2 && room >= 3 && max_keys >= 192) C = 3;
-  if (items * C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_rows_smem<Mode == kPaRest>(std::integral_constant<int, Mode * 100000 + NT * 1000 + HD * 2 + F8>(), kern, dim3((unsigned)(items * C), a.hkv),
+  const int64_t blocks = (items + (Mode == kPaRest ? 1 : 0)) * C;   // (one waits for the prefix)
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_rows_smem<Mode == kPaRest>(std::integral_constant<int, Mode * 100000 + NT * 1000 + HD * 2 + F8>(), kern, dim3((unsigned)blocks, a.hkv),
                           dim3(kPaThreads), L::smem, C, st, a, tpq, C);
 }
 template <int HD, bool F8, int Mode>

@@ -64,7 +64,6 @@
 #include "kernels.h"
 #include "pa_dev.cuh"
 #include "paged.h"
-#include "shared_dev.cuh"
 
 namespace sv {
 
@@ -282,12 +281,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     return true;
   };
   TaItem mine;
-  if constexpr (Mode == kPaPrefix) {
-    pdl_wait();                                // the plan
-    pdl_trigger();
-  }
-  mine.valid = item_at(Mode == kPaPrefix ? -1 : (int)blockIdx.x / ta.split, mine);
-  if (!mine.valid) return;                    // (all blocks of a cluster)
+  mine.valid = Mode != kPaPrefix && item_at((int)blockIdx.x / ta.split, mine);
+  if (Mode != kPaPrefix && !mine.valid) return;                    // (all blocks of a cluster)
 
   const uint32_t base = (smem_u32(tsm) + 1023u) & ~1023u;
   const uint32_t q_at = base + L::q, kv_at = base + L::kv, raw_at = base + L::raw_at;
@@ -334,6 +329,11 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
   ta_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   constexpr uint32_t o_at = 256;
+  if constexpr (Mode == kPaPrefix) {           // begun early: what the launch in front left is read from here on
+    pdl_wait();
+    pdl_trigger();
+    mine.valid = part_at(-1, mine);
+  }
 
   // Next item of the queue (the k-th of this block); false at the end or, but for
   // `last`, when a wait gave up.  The softmax warps take all that is handed out:
@@ -797,14 +797,29 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       }
       if constexpr (Mode == kPaPrefix) {        // sums as they are, for the join
         if (!ok) l = __uint_as_float(0x7fffffffu);
-        if (row_ok) {
-          float* const slot = const_cast<float*>(sh_slot(a.ws, a.n_groups, HD, it.slot));
-          float4* const at = reinterpret_cast<float4*>(slot) + t * (HD / 4) * kTaRows + r;
+        float* const slot = sh_slot(a.ws, a.n_groups, a.seqs, HD, it.slot);
+        const int c16 = lane & 7, first = t * kTaRows + (warp & 3) * 32, rows = min(tpt, it.toks - t_at) * G;
 #pragma unroll
-          for (int c = 0; c < HD / 4; ++c)
-            __stcg(at + c * kTaRows, make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
-          __stcg(reinterpret_cast<float2*>(slot + 256 * HD) + t * kTaRows + r, make_float2(m, l));
+        for (int h = 0; h < HD / 32; ++h) {     // 32 dims of the warp's rows at a time, out as whole lines
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(stage + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) << 4))), "f"(o[32 * h + 4 * c]),
+                           "f"(o[32 * h + 4 * c + 1]), "f"(o[32 * h + 4 * c + 2]), "f"(o[32 * h + 4 * c + 3]) : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const int r2 = i + (lane >> 3);
+            float4 x;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                         : "r"(stage + (uint32_t)(r2 * 128 + ((c16 ^ (r2 & 7)) << 4))) : "memory");
+            if ((warp & 3) * 32 + r2 < rows)
+              __stcg(reinterpret_cast<float4*>(slot + (size_t)(first + r2) * HD + 32 * h) + c16, x);
+          }
+          __syncwarp();
         }
+        if (row_ok) __stcg(reinterpret_cast<float2*>(slot + 256 * HD) + t * kTaRows + r, make_float2(m, l));
         continue;
       }
       if (ta.split > 1) {
@@ -892,7 +907,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     if constexpr (Mode == kPaPrefix) {         // a wait gave up: the parts of the run that were not handed out are NaN
       if (__any_sync(0xffffffffu, s_abort))
         while (part_at(it.unit, it)) {
-          float* const slot = const_cast<float*>(sh_slot(a.ws, a.n_groups, HD, it.slot));
+          float* const slot = sh_slot(a.ws, a.n_groups, a.seqs, HD, it.slot);
           __stcg(reinterpret_cast<float2*>(slot + 256 * HD) + t * kTaRows + r, make_float2(0.f, __uint_as_float(0x7fffffffu)));
         }
     }

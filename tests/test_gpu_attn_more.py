@@ -263,6 +263,21 @@ def _shared_case(seed, hq, hk, hd, ps, dtype, ns, first, shared, rests, pad=0):
     return cache, q, _i32(cu), _i32(lens), lens
 
 
+def _wide(c):
+    """The cache with a table whose width makes sharing pay for any of these batches (the lengths are
+    the device's own; entries past them name nothing)."""
+    t = torch.full((c.seqs, max(c.max_pages, 900000 // c.page_size)), -1, dtype=torch.int32, device="cuda")
+    t[:, :c.max_pages] = c.table
+    return sv.KVCache(c.k, c.v, t, c.k_scale, c.v_scale)
+
+
+def _shares(c, groups, n, max_q, hq):
+    """Whether a call of these sizes shares anything: the prefixes' parts need room of their own."""
+    L = sv.lib()
+    return (L.spec_attn_shared_workspace(c._ref, groups, n, max_q, hq)
+            > L.spec_attn_paged_workspace(c._ref, n, max_q, hq) + 256 * n)
+
+
 def _shared_check(c, q, cu, lens, ns, ctx, shared, groups, max_q):
     hd = q.shape[2]
     out = torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
@@ -288,7 +303,9 @@ SHARED = [  # hq, hk, hd, page, new tokens, groups, shared, positions behind the
     (16, 2, 128, 16, [8] * 5, [0, 1, 5], [100, 2000], [8, 8, 9, 10, 300]),        # a group of one
     (8, 8, 64, 16, [1, 60, 2], [0, 3], [300], [1, 60, 300]),                      # 60 rows a KV head
     (32, 8, 64, 16, [2] * 40, [0, 10, 20, 30, 40], [400, 16, 0, 2000], [2 + i for i in range(40)]),
-    (128, 1, 128, 16, [1] * 6, [0, 6], [700], [1, 9, 20, 33, 1, 64]),             # a tile holds one token
+    (128, 1, 128, 16, [1] * 6, [0, 6], [700], [1, 9, 20, 33, 1, 64]),             # too many rows a KV head
+    (64, 1, 128, 16, [1] * 6, [0, 6], [700], [1, 9, 20, 33, 1, 64]),              # a tile holds two tokens
+    (120, 2, 64, 32, [1] * 5, [0, 5], [900], [1, 9, 20, 33, 1]),                  # 60 rows: a tile of 120
     (4, 4, 128, 16, [1] * 300, [0, 300], [256], [1 + i % 40 for i in range(300)]),  # two row pairs a head
     (6, 2, 64, 16, [1, 1], [0, 2], [-5], [30, 40]),
 ]
@@ -299,6 +316,8 @@ SHARED = [  # hq, hk, hd, page, new tokens, groups, shared, positions behind the
 def test_shared(hq, hk, hd, ps, ns, first, shared, rests, dtype):
     c, q, cu, lens, ctx = _shared_case(sum(rests) + hd, hq, hk, hd, ps, dtype, ns, first, shared, rests, pad=3)
     sh, gr = _i32(shared), _i32(first)
+    c = _wide(c)
+    assert _shares(c, len(shared), q.shape[0], max(ns), hq) == (max(ns) * hq // hk <= 64)
     a = _shared_check(c, q, cu, lens, ns, ctx, sh, gr, max(ns))
     if first == [0, len(ns)]:
         b = sv.attn_shared(q, c, cu, lens, sh, max_q=max(ns))
@@ -320,6 +339,8 @@ def test_shared_is_cut_to_what_rows_see(dtype, hd):
     c.table.copy_(c.table[:1].expand_as(c.table).clone())
     pos = torch.arange(900, device="cuda").int()
     sv.kv_append(c, _randn(g, 900, 2, hd), _randn(g, 900, 2, hd), torch.zeros_like(pos), pos)
+    c = _wide(c)
+    assert _shares(c, 1, 6, 3, 8)
     q = _randn(g, 6, 8, hd).bfloat16()
     cu, lens = _i32([0, 2, 3, 6, 6]), _i32(ctx)
     for shared in (399, 400, 900, 2 ** 31 - 1, 384, 1, 0):
@@ -333,6 +354,8 @@ def test_shared_bad_indices(dtype):
     groups are as they were."""
     ns, first, shared = [4] * 6, [0, 3, 6], [600, 300]
     c, q, cu, lens, ctx = _shared_case(5, 16, 4, 128, 16, dtype, ns, first, shared, [20] * 6, pad=2)
+    c = _wide(c)
+    assert _shares(c, 2, 26, 4, 16)
     ref, _ = sv.attn_shared(q, c, cu, lens, _i32(shared), groups=_i32(first), max_q=4)
     call = lambda g, cu=cu, t=None: sv.attn_shared(q, c, cu, lens, _i32(shared), groups=_i32(g), max_q=4,
                                                    out=torch.full_like(ref, 7.0))[0]
@@ -355,6 +378,9 @@ def test_shared_streams_graphs_workspaces(dtype):
     workspace that holds anything; without one the call is attn_paged."""
     ns, first, shared = [3] * 8, [0, 5, 8], [2000, 900]
     c, q, cu, lens, ctx = _shared_case(9, 32, 8, 128, 16, dtype, ns, first, shared, [30, 200] * 4)
+    narrow = c
+    c = _wide(c)
+    assert _shares(c, 2, 24, 3, 32)
     sh, gr = _i32(shared), _i32(first)
     q2 = q.flip(0).contiguous()
     call = lambda x, **kw: sv.attn_shared(x, c, cu, lens, sh, groups=gr, max_q=3, **kw)
@@ -373,6 +399,10 @@ def test_shared_streams_graphs_workspaces(dtype):
     need = L.spec_attn_shared_workspace(c._ref, 2, n, 3, 32)
     ws = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
     plain = sv.attn_paged(q, c, cu, lens, max_q=3)
+    # where sharing does not pay the call is attn_paged
+    assert not _shares(narrow, 2, n, 3, 32)
+    for x, y in zip(sv.attn_shared(q, narrow, cu, lens, sh, groups=gr, max_q=3), sv.attn_paged(q, narrow, cu, lens, max_q=3)):
+        assert torch.equal(x, y)
     for size in (0, max(0, need - 16), need):
         out, lse = torch.zeros(n, 32, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 32, device="cuda")
         assert L.spec_attn_shared(c._ref, q.data_ptr(), q.stride(0), q.stride(1), cu.data_ptr(), lens.data_ptr(),
@@ -402,6 +432,8 @@ def test_shared_waits_that_run_out(dtype, hd):
     did not come to."""
     ns, first, shared = [4] * 40, [0, 30, 40], [3000, 900]
     c, q, cu, lens, ctx = _shared_case(19, 16, 4, hd, 16, dtype, ns, first, shared, [9] * 40)
+    c = _wide(c)
+    assert _shares(c, 2, 160, 4, 16)
     sh, gr = _i32(shared), _i32(first)
     _give_up(lambda o, l: sv.attn_shared(q, c, cu, lens, sh, groups=gr, max_q=4, out=o, lse=l), q, (1, 2))
 
@@ -416,7 +448,7 @@ def test_serving_loop(dtype, hd, ps):
     hq, hk, seqs, width = 8, 2, 5, 640 // ps + 2
     prompt = 512
     shared_pages = prompt // ps
-    table = torch.full((seqs, width), -1, dtype=torch.int32, device="cuda")
+    table = torch.full((seqs, 250000 // ps), -1, dtype=torch.int32, device="cuda")   # (wide: sharing pays)
     pool = shared_pages + seqs * (width - shared_pages)
     c = sv.KVCache.empty(pool, ps, hk, hd, table, dtype)
     table[:, :shared_pages] = torch.arange(shared_pages, device="cuda").int()
