@@ -763,15 +763,12 @@ def kv_reserve(cache, kv_lens, counts, free, n_free, tokens, stream=None):
     _stack(cache, free, n_free)
     if tokens < 0:
         _refuse("tokens: a bound on the step's tokens")
-    up = (seqs + 4) & ~3, (tokens + 3) & ~3            # one allocation, its parts on 16-byte boundaries
-    buf = _alloc(stream, cache.device, lambda: _t.empty(2 * up[0] + 2 * up[1] + 4, dtype=_t.int32, device=cache.device))
-    at = buf.data_ptr()
-    cu, lens = buf[:seqs + 1], buf[up[0]:up[0] + seqs]
-    o = 2 * up[0]
-    seq, pos, lacking = buf[o:o + tokens], buf[o + up[1]:o + up[1] + tokens], buf[o + 2 * up[1]:o + 2 * up[1] + 1]
+    where = cache.device
+    cu, lens, seq, pos, lacking = _alloc(stream, where, lambda: [
+        _t.empty(n, dtype=_t.int32, device=where) for n in (seqs + 1, seqs, tokens, tokens, 1)])
     _call(dev, stream, lib().spec_kv_reserve, cache._ref, kv_lens.data_ptr(), counts.data_ptr(), free.data_ptr(),
-          n_free.data_ptr(), free.shape[0], tokens, at, at + 4 * up[0], at + 4 * o, at + 4 * (o + up[1]),
-          at + 4 * (o + 2 * up[1]))
+          n_free.data_ptr(), free.shape[0], tokens, cu.data_ptr(), lens.data_ptr(), seq.data_ptr(), pos.data_ptr(),
+          lacking.data_ptr())
     return cu, lens, seq, pos, lacking
 
 

@@ -288,6 +288,25 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
     }
     cp_async_commit();
   };
+  // the warp's rows of Q on their way, all at once and ahead of the page ids that the copies wait for
+  constexpr int kPer = HD / 32, kOwn = kRows / kPaWarps;   // elements of a lane (kPer lane ..), rows of a warp
+  uint32_t raw[kOwn][kPer > 1 ? kPer / 2 : 1];
+#pragma unroll
+  for (int ri = 0; ri < kOwn; ++ri) {
+    const int R = row0 + warp + ri * kPaWarps, t = R / G;
+    const bool ok = R < rows;
+    const bf16* qr = (const bf16*)a.q + (int64_t)(r_first + (ok ? t : 0)) * a.q_ts +
+                     (int64_t)(kvh * G + (ok ? R - t * G : 0)) * a.q_hs + kPer * lane;
+    if constexpr (kPer == 4) {
+      const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(qr)) : make_uint2(0, 0);
+      raw[ri][0] = v.x;
+      raw[ri][1] = v.y;
+    } else if constexpr (kPer == 2) {
+      raw[ri][0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qr)) : 0u;
+    } else {
+      raw[ri][0] = ok ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(qr)) : 0u;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < D; ++j) {
     issue(j, 0);
@@ -298,16 +317,12 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
   // bytes (two 16-element k slices of two words).  A lane's words hold
   // elements 2 q, 2 q + 1 and 8 more; with 8-bit keys, whose four neighbours
   // come in one word, elements 4 q .. 4 q + 3.
-  for (int r = warp; r < kRows; r += kPaWarps) {
-    const int R = row0 + r, t = R / G;
-    const bool ok = R < rows;
-    constexpr int kPer = HD / 32;             // elements of a lane: kPer lane .. + kPer - 1
-    const int k = kPer * lane;
-    const bf16* qr = (const bf16*)a.q + (int64_t)(r_first + (ok ? t : 0)) * a.q_ts +
-                     (int64_t)(kvh * G + (ok ? R - t * G : 0)) * a.q_hs + k;
+#pragma unroll
+  for (int ri = 0; ri < kOwn; ++ri) {
+    const int r = warp + ri * kPaWarps, k = kPer * lane;
     float x[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = ok ? __bfloat162float(qr[i]) : 0.f;
+    for (int i = 0; i < kPer; ++i) x[i] = i & 1 ? bf16hi(raw[ri][i / 2]) : bf16lo(raw[ri][i / 2]);
     if constexpr (F8) {
       uint32_t m = 0;
 #pragma unroll

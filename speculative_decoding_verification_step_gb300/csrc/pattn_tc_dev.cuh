@@ -89,19 +89,24 @@ struct TaArgs {
   int take;         // blocks take over further items
 };
 
-template <int HD, bool F8>
+template <int HD, bool F8, int Mode>
 struct TaLayout {
-  static constexpr int threads = F8 ? 512 : 384;
+  // 8-bit prefixes leave as sums, a row by its thread, in whole sectors: the room where other rows
+  // wait on their way out holds more codes in flight, and eight warps convert them.
+  static constexpr bool deep = F8 && Mode == kPaPrefix;
+  static constexpr int convert = deep ? 8 : 4;             // warps that convert codes
+  static constexpr int threads = F8 ? 384 + 32 * convert : 384;
   static constexpr int stages = F8 ? 3 : 4;                // bf16 K / V tiles
-  static constexpr int raws = F8 ? 2 : 0;                  // tiles of codes
+  static constexpr int raws = !F8 ? 0 : !deep ? 2 : HD == 128 ? 4 : 6;   // tiles of codes
   static constexpr uint32_t tile = kTaKeys * HD * 2;
   static constexpr uint32_t raw = kTaKeys * HD;
   static constexpr uint32_t q = 0, kv = 2 * tile, raw_at = kv + stages * tile, stage_at = raw_at + raws * raw;
   static constexpr uint32_t stage = 32 * 128;              // a warp's rows on their way out, 64 dims at a time
-  static constexpr int smem = (int)(stage_at + 8 * stage) + 1024;
+  static constexpr int smem = (int)(stage_at + (deep ? 0 : 8 * stage)) + 1024;
   static_assert(smem <= 227 * 1024 - 1536, "with the barriers and queues, one block's shared memory");
-  // registers (multiples of 8): softmax, others, 8-bit conversion; 2 x 216 + 56 <= 3 x 168, 2 x 184 + 56 + 88 <= 4 x 128
-  static constexpr int soft_regs = F8 ? 184 : 216, other_regs = 56;
+  // registers (multiples of 8): softmax, others, 8-bit conversion; 2 x 216 + 56 <= 3 x 168, 2 x 184 + 56 + 88 <= 4 x 128,
+  // 2 x 176 + 48 + 2 x 40 <= 5 x 96
+  static constexpr int soft_regs = deep ? 176 : F8 ? 184 : 216, other_regs = deep ? 48 : 56, convert_regs = deep ? 40 : 88;
 };
 
 SV_DEV uint32_t ta_cluster_rank() {
@@ -158,8 +163,8 @@ struct TaItemOf<kPaPrefix> : TaItemBase {
 
 // Hook: the form of SPEC_FAULT_ATTN_TIMEOUT, whose a.give_up-th step waits for what never comes.
 template <int HD, bool F8, bool Hook, int Mode>
-__global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
-  using L = TaLayout<HD, F8>;
+__global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
+  using L = TaLayout<HD, F8, Mode>;
   using TaItem = TaItemOf<Mode>;
   constexpr int kHalf = HD / 64;                       // 64-dim halves of a row
   constexpr uint32_t kTile = L::tile;
@@ -297,15 +302,15 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
     mbar_init(&taken, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_empty[s], F8 ? 14 : 10);   // one arrival per warp that works on items
+      mbar_init(&item_empty[s], F8 ? 10 + L::convert : 10);   // one arrival per warp that works on items
     }
     for (int s = 0; s < kS; ++s) {
-      mbar_init(&kv_full[s], F8 ? 4 : 1);    // converted by four warps, or copied
+      mbar_init(&kv_full[s], F8 ? L::convert : 1);   // converted by so many warps, or copied
       mbar_init(&kv_empty[s], 1);
     }
     for (int s = 0; s < kR; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], 4);
+      mbar_init(&raw_empty[s], L::convert);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -350,9 +355,10 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
 
   if (warp >= 12) {
     if constexpr (F8) {
-      // ---- 8-bit rows to bf16: thread = key row ----
-      ta_regs_less<88>();
-      const int r = threadIdx.x - 384;
+      // ---- 8-bit rows to bf16: thread = key row, or half of one ----
+      constexpr int kChunks = HD / 16 * 4 / L::convert;
+      ta_regs_less<L::convert_regs>();
+      const int r = (threadIdx.x - 384) & 127, c0 = (threadIdx.x - 384) / 128 * kChunks;
       int i = 0;                               // tile: K and V of the steps of all items in turn
       bool ok = true;
       TaItem it;
@@ -371,8 +377,9 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
           const uint64_t scale = ta_pair(f, f);
           const uint32_t src = raw_at + rs * L::raw + r * HD, dst = kv_at + s * kTile + r * 128;
 #pragma unroll
-          for (int c = 0; c < HD / 16; ++c) {
+          for (int ci = 0; ci < kChunks; ++ci) {
             uint32_t w[4], o[8];
+            const int c = c0 + ci;
             const int sw = HD == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src + (sw << 4)) : "memory");
@@ -798,26 +805,36 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
       if constexpr (Mode == kPaPrefix) {        // sums as they are, for the join
         if (!ok) l = __uint_as_float(0x7fffffffu);
         float* const slot = sh_slot(a.ws, a.n_groups, a.seqs, HD, it.slot);
-        const int c16 = lane & 7, first = t * kTaRows + (warp & 3) * 32, rows = min(tpt, it.toks - t_at) * G;
+        if constexpr (L::deep) {
+          float* const at = slot + (size_t)(t * kTaRows + r) * HD;
+          if (row_ok)
 #pragma unroll
-        for (int h = 0; h < HD / 32; ++h) {     // 32 dims of the warp's rows at a time, out as whole lines
+            for (int c = 0; c < HD; c += 8)
+              asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                           ::"l"(at + c), "f"(o[c]), "f"(o[c + 1]), "f"(o[c + 2]), "f"(o[c + 3]), "f"(o[c + 4]), "f"(o[c + 5]),
+                             "f"(o[c + 6]), "f"(o[c + 7]) : "memory");
+        } else {
+          const int c16 = lane & 7, first = t * kTaRows + (warp & 3) * 32, rows = min(tpt, it.toks - t_at) * G;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
-                         ::"r"(stage + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) << 4))), "f"(o[32 * h + 4 * c]),
-                           "f"(o[32 * h + 4 * c + 1]), "f"(o[32 * h + 4 * c + 2]), "f"(o[32 * h + 4 * c + 3]) : "memory");
-          __syncwarp();
+          for (int h = 0; h < HD / 32; ++h) {     // 32 dims of the warp's rows at a time, out as whole lines
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const int r2 = i + (lane >> 3);
-            float4 x;
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                         : "r"(stage + (uint32_t)(r2 * 128 + ((c16 ^ (r2 & 7)) << 4))) : "memory");
-            if ((warp & 3) * 32 + r2 < rows)
-              __stcg(reinterpret_cast<float4*>(slot + (size_t)(first + r2) * HD + 32 * h) + c16, x);
+            for (int c = 0; c < 8; ++c)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                           ::"r"(stage + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) << 4))), "f"(o[32 * h + 4 * c]),
+                             "f"(o[32 * h + 4 * c + 1]), "f"(o[32 * h + 4 * c + 2]), "f"(o[32 * h + 4 * c + 3]) : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const int r2 = i + (lane >> 3);
+              float4 x;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                           : "r"(stage + (uint32_t)(r2 * 128 + ((c16 ^ (r2 & 7)) << 4))) : "memory");
+              if ((warp & 3) * 32 + r2 < rows)
+                __stcg(reinterpret_cast<float4*>(slot + (size_t)(first + r2) * HD + 32 * h) + c16, x);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (row_ok) __stcg(reinterpret_cast<float2*>(slot + 256 * HD) + t * kTaRows + r, make_float2(m, l));
         continue;
@@ -938,7 +955,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8>::threads, 1) pattn_tc_kernel(
 
 template <int HD, bool F8, bool Hook, int Mode>
 cudaError_t launch_ta_hook(const TaArgs& ta, cudaStream_t st) {
-  using L = TaLayout<HD, F8>;
+  using L = TaLayout<HD, F8, Mode>;
   auto kern = pattn_tc_kernel<HD, F8, Hook, Mode>;
   return launch_rows_smem<Mode == kPaPrefix>(std::integral_constant<int, Mode * 1000 + HD * 4 + F8 * 2 + Hook>(), kern,
                                              dim3((unsigned)(ta.split * ta.items)), dim3(L::threads), L::smem, ta.split, st, ta);
@@ -995,7 +1012,7 @@ cudaError_t launch_ta_items(const PAttn& a, int num_sms, cudaStream_t st) {
   // new tokens few beside their contexts: a walk's length is its sequence's
   ta.by_length = Mode == kPaCausal && a.paged && a.seqs <= 32 && max_keys >= 2LL * a.max_q ? 1 : 0;
   // Where blocks cover the items, each keeps to its own: one that starts early would take
-  // items whose blocks find free SMs (136 items of 18 steps in a grid of 256 65 -> %TAKE% us).
+  // items whose blocks find free SMs (136 items of 18 steps in a grid of 256: 65 -> 36 us).
   ta.take = ta.split == 1 && (Mode == kPaCausal || most > num_sms);
   return launch_ta_mode<Mode>(ta, st);
 }
