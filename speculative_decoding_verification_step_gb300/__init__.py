@@ -761,8 +761,8 @@ def kv_reserve(cache, kv_lens, counts, free, n_free, tokens, stream=None):
     _index("kv_lens", kv_lens, seqs, dev)
     _index("counts", counts, seqs, dev)
     _stack(cache, free, n_free)
-    if tokens < 0:
-        _refuse("tokens: a bound on the step's tokens")
+    if not 0 <= tokens <= 0x7fffff00:
+        _refuse("tokens: a bound on the step's tokens, up to 2^31 - 256")
     where = cache.device
     cu, lens, seq, pos, lacking = _alloc(stream, where, lambda: [
         _t.empty(n, dtype=_t.int32, device=where) for n in (seqs + 1, seqs, tokens, tokens, 1)])
@@ -804,6 +804,12 @@ def _attn_out(q, shape, dev, out, lse, need, stream):
         _t.empty(need, dtype=_t.uint8, device=where) if need else None))
 
 
+def _window(window, sinks):
+    if window < 0 or sinks < 0:
+        _refuse("window and sinks must not be negative")
+    return min(window, 0x7fffffff), min(sinks, 0x7fffffff)
+
+
 def _paged_args(q, cache, cu_q, kv_lens):
     """(strides, shape, device) of an attention call over the cache."""
     qs = _rows3("q", q)
@@ -843,7 +849,7 @@ def attn_paged(q, cache, cu_q, kv_lens, max_q=None, scale=0.0, out=None, lse=Non
     if max_q is None:
         max_q = n
     if window or sinks:
-        window, sinks = min(window, 0x7fffffff), min(sinks, 0x7fffffff)
+        window, sinks = _window(window, sinks)
         need = _ws_bytes(cache, (n, max_q, h, window, sinks), dev,
                          lambda: lib().spec_attn_paged_window_workspace(cache._ref, n, max_q, h, window, sinks))
         out, lse, ws = _attn_out(q, shape, dev, out, lse, need, stream)
@@ -912,9 +918,10 @@ def attn_prompt(q, k, v, cu, max_len=None, scale=0.0, out=None, lse=None, stream
     out, lse, _ = _attn_out(q, shape, dev, out, lse, 0, stream)
     os_ = _rows3("out", out)
     if window or sinks:
+        window, sinks = _window(window, sinks)
         _call(dev, stream, lib().spec_attn_prompt_window, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
               v.data_ptr(), vs[0], vs[1], cu.data_ptr(), seqs, n, n if max_len is None else max_len, h, kshape[1], d,
-              scale, min(window, 0x7fffffff), min(sinks, 0x7fffffff), out.data_ptr(), os_[0], os_[1],
+              scale, window, sinks, out.data_ptr(), os_[0], os_[1],
               lse.data_ptr() if lse is not False else None)
         return out, (lse if lse is not False else None)
     _call(dev, stream, lib().spec_attn_prompt, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],

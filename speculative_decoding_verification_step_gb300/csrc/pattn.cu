@@ -24,6 +24,12 @@ bool row_aligned(const void* p, int64_t ts, int64_t hs) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ts % 8 == 0 && hs % 8 == 0;
 }
 
+// A window that holds every position of the call is none.
+void settle_window(PAttn& a) {
+  const int64_t most = a.paged ? (int64_t)a.max_pages << a.page_shift : std::min(a.max_q, a.tokens);
+  if (a.window >= most) a.window = 0;
+}
+
 // Workspace of launch_pattn_td where it is taken, else 0.  It costs 5 us a tile
 // and 10 us for its start and join, and saves up to a third of a long context's
 // time.  It is taken at head dim 128 for more than 16 rows, tables of 2048
@@ -112,6 +118,7 @@ int run_attention(PAttn& a, size_t ws_bytes, const char* who, cudaStream_t st) {
   if (!a.q || !a.out || !a.cu) return fail(SPEC_E_ARG, w + "null pointer");
   if (!row_aligned(a.q, a.q_ts, a.q_hs) || !row_aligned(a.out, a.o_ts, a.o_hs))
     return fail(SPEC_E_ARG, w + "q and out must be 16-byte aligned with strides multiples of 8");
+  settle_window(a);
   if (a.scale_log2 == 0.f) a.scale_log2 = 1.f / std::sqrt((float)a.hd);
   a.scale_log2 *= kLog2e;
   a.give_up = g_attn_give_up.load(std::memory_order_relaxed);
@@ -154,13 +161,14 @@ int64_t asked_workspace(PAttn a, const char* who, const spec_kv_cache* cache, in
   cache_fields(a, cache);
   a.hq = n_heads; a.tokens = tokens; a.max_q = max_q;
   a.q_hs = a.o_hs = a.hd; a.q_ts = a.o_ts = (int64_t)n_heads * a.hd;
+  settle_window(a);
   const size_t own = a.n_groups > 0 ? shared_bytes(a, sms) : 0;
   return own ? (int64_t)own : (int64_t)choose_way(a, sms).td_ws;
 }
 
 int window_fields(PAttn& a, int window, int sinks, const char* who) {
   if (window < 0 || sinks < 0) return fail(SPEC_E_ARG, std::string(who) + ": window and sinks must not be negative");
-  a.window = std::min(window, 1 << 30);      // (differences of positions stay within 32 bits)
+  a.window = window;
   a.sinks = sinks;
   return SPEC_OK;
 }

@@ -192,7 +192,7 @@ int64_t most_tiles(const PAttn& a) {
 }  // namespace
 
 size_t pattn_shared_workspace(const PAttn& a, int num_sms) {
-  if (!a.paged || !pattn_tc_supported(a)) return 0;
+  if (!a.paged || a.seqs > 1 << 24 || !pattn_tc_supported(a)) return 0;
   const int64_t keys = (int64_t)a.max_pages << a.page_shift, tiles = most_tiles(a);
   const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * a.hq;
   if (tiles * ((keys + kTaKeys - 1) / kTaKeys) > 0x3fffffffLL || (rows + 7) / 8 * a.seqs > 0x7fffffffLL) return 0;
@@ -205,7 +205,7 @@ cudaError_t launch_pattn_shared(const PAttn& call, int num_sms, cudaStream_t st)
   a.rest = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(a.ws) + sh_slots_at(a.n_groups, a.seqs)) +
            (size_t)(num_sms + most_tiles(a)) * 256 * (a.hd + 2);
   TaArgs ta{};
-  if (!ta_args(ta, a)) return cudaErrorInvalidValue;
+  if (!ta_args<kPaPrefix>(ta, a)) return cudaErrorInvalidValue;
   ta.items = num_sms;
   ta.split = 1;
   cudaError_t e = launch_rows(shared_plan_kernel, dim3(1), dim3(kShThreads), 0, 1, st, a, sh_cost(a));

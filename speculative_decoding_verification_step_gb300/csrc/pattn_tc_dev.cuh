@@ -59,6 +59,7 @@
 
 #include <algorithm>
 #include <cstdlib>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -76,7 +77,6 @@ constexpr float kTaNone = -1e30f;
 
 struct TaArgs {
   TensorMap128 qm, km, vm;
-  TensorMap128 ks, vs;   // windows: the same in boxes of 16 rows
   PAttn a;
   int tpt;          // tokens of a tile: 128 / G
   uint32_t g_mul;   // ceil(2^16 / G): r * g_mul >> 16 = r / G for r < 128
@@ -86,8 +86,14 @@ struct TaArgs {
   int split;        // 2: clusters of two blocks share an item's keys
   int by_length;    // sequences in order of their lengths (paged, at most 32)
   int box_rows;     // key rows of a K / V box
-  int take;         // blocks take over further items
 };
+
+struct TaWindowArgs : TaArgs {
+  TensorMap128 ks, vs;   // K and V in boxes of 16 rows
+  int take;              // blocks take over further items
+};
+template <int Mode>
+using TaArgsOf = std::conditional_t<Mode == kPaWindow, TaWindowArgs, TaArgs>;
 
 template <int HD, bool F8, int Mode>
 struct TaLayout {
@@ -163,7 +169,7 @@ struct TaItemOf<kPaPrefix> : TaItemBase {
 
 // Hook: the form of SPEC_FAULT_ATTN_TIMEOUT, whose a.give_up-th step waits for what never comes.
 template <int HD, bool F8, bool Hook, int Mode>
-__global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_kernel(const __grid_constant__ TaArgs ta) {
+__global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_kernel(const __grid_constant__ TaArgsOf<Mode> ta) {
   using L = TaLayout<HD, F8, Mode>;
   using TaItem = TaItemOf<Mode>;
   constexpr int kHalf = HD / 64;                       // 64-dim halves of a row
@@ -406,6 +412,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
     ta_regs_less<L::other_regs>();
     if (warp == 8) {
       // ---- producer ----
+      const int per_step = a.paged ? kTaKeys / ta.box_rows : 1;   // boxes of a step
       constexpr int kRing = F8 ? L::raws : kS;
       uint64_t* const full = F8 ? raw_full : kv_full;
       uint64_t* const empty = F8 ? raw_empty : kv_empty;
@@ -427,24 +434,28 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
         ++loads;
         const int32_t* table = a.paged ? a.table + it.b * a.table_stride : nullptr;
         const int npages = a.paged ? (int)(((int64_t)it.keys + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
-        // rows of step j's boxes; small ones where it holds first tokens and window
-        auto box_of = [&](int j) {
+        // small boxes where a step holds first tokens and window
+        auto is_small = [&](int j) {
           if constexpr (Mode == kPaWindow) {
             const int at = (it.beg + j) * kTaKeys;
-            return it.gap > 0 && at < it.lead && at + kTaKeys > it.lead ? 16 : ta.box_rows;
+            return it.gap > 0 && at < it.lead && at + kTaKeys > it.lead;
           } else {
-            return ta.box_rows;
+            return false;
           }
         };
         auto box_key = [&](int j) {   // first key of box `lane`
-          if constexpr (Mode == kPaWindow) return (int64_t)key_at(it, (it.beg + j) * kTaKeys + lane * box_of(j));
+          if constexpr (Mode == kPaWindow) return (int64_t)key_at(it, (it.beg + j) * kTaKeys + lane * (is_small(j) ? 16 : ta.box_rows));
           else return (int64_t)(it.beg + j) * kTaKeys + (a.paged ? lane * ta.box_rows : 0);
         };
         // lane b: page of box b of step j; -1 (zero rows) past the length, outside the pool or where no row sees it
         auto page_of = [&](int j) {
           const int64_t key = box_key(j);
-          const int pg = (int)(key >> a.page_shift), box = box_of(j);
-          const int page = lane < kTaKeys / box && j < it.nst && pg < npages && reached(it, key, box) ? __ldg(table + pg) : -1;
+          const int pg = (int)(key >> a.page_shift);
+          const bool small = is_small(j);
+          const int page = lane < (small ? kTaKeys / 16 : per_step) && j < it.nst && pg < npages &&
+                                   reached(it, key, small ? 16 : ta.box_rows)
+                               ? __ldg(table + pg)
+                               : -1;
           return page >= a.pages ? -1 : page;
         };
         int next = a.paged ? page_of(0) : 0;
@@ -453,15 +464,17 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
           if (a.paged) next = page_of(j + 1);
           const int64_t key = box_key(j);
           const int row = a.paged ? (it.kvh << a.page_shift) + (int)(key & ((1 << a.page_shift) - 1)) : it.kvh;
-          const int box = box_of(j), per = Mode == kPaWindow || a.paged ? kTaKeys / box : 1;
-          const bool small = Mode == kPaWindow && box < ta.box_rows;
+          const bool small = is_small(j);
+          const int box = small ? 16 : ta.box_rows, per = small ? kTaKeys / 16 : per_step;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++i) {
             const int s = i % kRing;
             if (i >= kRing) live = live && ta_wait(&empty[s], (unsigned)((i / kRing - 1) & 1), &s_abort);
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
-            const void* map = small ? (kv ? &ta.vs : &ta.ks) : kv ? &ta.vm : &ta.km;
+            const void* map = kv ? &ta.vm : &ta.km;
+            if constexpr (Mode == kPaWindow)
+              if (small) map = kv ? &ta.vs : &ta.ks;
             if constexpr (F8) {
               const bool in = lane < per && page >= 0;
               const unsigned some = __ballot_sync(0xffffffffu, in);
@@ -639,7 +652,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
           const bool go = ok && !__any_sync(0xffffffffu, s_abort);
           it.valid = go && part_at(it.unit, it);
         }
-        const bool take = Mode == kPaCausal ? ta.split == 1 : Mode == kPaWindow && ta.take;
+        bool take = Mode == kPaCausal && ta.split == 1;
+        if constexpr (Mode == kPaWindow) take = ta.take;
         while (take && ok && !__any_sync(0xffffffffu, s_abort)) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&taken, 16);
@@ -687,8 +701,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
       if constexpr (Mode == kPaWindow) {
         if (row_ok) {
           high = seen - it.gap - it.beg * kTaKeys;
-          low = high - a.window;
-          first = min(sinks, seen) - it.beg * kTaKeys;
+          low = (int)max((int64_t)0, (int64_t)high - a.window);   // (below 0 is as good as 0)
+          first = max(min(sinks, seen) - it.beg * kTaKeys, 0);
         }
       }
       float m = kTaNone, l = 0.f;
@@ -714,8 +728,8 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
             }
           }
           high -= kTaKeys;
-          low -= kTaKeys;
-          first -= kTaKeys;
+          low = max(low - kTaKeys, 0);
+          first = max(first - kTaKeys, 0);
         } else {
           const int key0 = (it.beg + j) * kTaKeys;
           if (key0 + kTaKeys > tile_all) {
@@ -954,7 +968,7 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
 }
 
 template <int HD, bool F8, bool Hook, int Mode>
-cudaError_t launch_ta_hook(const TaArgs& ta, cudaStream_t st) {
+cudaError_t launch_ta_hook(const TaArgsOf<Mode>& ta, cudaStream_t st) {
   using L = TaLayout<HD, F8, Mode>;
   auto kern = pattn_tc_kernel<HD, F8, Hook, Mode>;
   return launch_rows_smem<Mode == kPaPrefix>(std::integral_constant<int, Mode * 1000 + HD * 4 + F8 * 2 + Hook>(), kern,
@@ -962,21 +976,22 @@ cudaError_t launch_ta_hook(const TaArgs& ta, cudaStream_t st) {
 }
 
 template <int HD, bool F8, int Mode>
-cudaError_t launch_ta(const TaArgs& ta, cudaStream_t st) {
+cudaError_t launch_ta(const TaArgsOf<Mode>& ta, cudaStream_t st) {
   return ta.a.give_up > 0 ? launch_ta_hook<HD, F8, true, Mode>(ta, st) : launch_ta_hook<HD, F8, false, Mode>(ta, st);
 }
 template <int Mode>
-cudaError_t launch_ta_mode(const TaArgs& ta, cudaStream_t st) {
+cudaError_t launch_ta_mode(const TaArgsOf<Mode>& ta, cudaStream_t st) {
   if (ta.a.f8) return ta.a.hd == 64 ? launch_ta<64, true, Mode>(ta, st) : launch_ta<128, true, Mode>(ta, st);
   return ta.a.hd == 64 ? launch_ta<64, false, Mode>(ta, st) : launch_ta<128, false, Mode>(ta, st);
 }
 // The arguments of a call, but for how its items are cut; false where no tensor map can be made.
-[[maybe_unused]] bool ta_args(TaArgs& ta, const PAttn& a) {
+template <int Mode>
+bool ta_args(TaArgsOf<Mode>& ta, const PAttn& a) {
   ta.a = a;
   const int G = a.hq / a.hkv, ps = a.paged ? 1 << a.page_shift : kTaKeys;
   ta.tpt = kTaRows / G;
   ta.g_mul = (65536u + G - 1) / G;
-  ta.box_rows = std::min(ps, a.window > 0 && a.paged ? 64 : kTaKeys);   // (a window's first box may be mostly in front of it)
+  ta.box_rows = std::min(ps, Mode == kPaWindow && a.paged ? 64 : kTaKeys);   // (a window's first box may be mostly in front of it)
   auto maps = [&](TensorMap128& k, TensorMap128& v, int rows) {
     if (a.paged)
       return ta_map(k, a.k, a.hd, (int64_t)a.hkv * ps, a.pages, a.hd, a.page_stride, rows, 1, a.f8) &&
@@ -984,14 +999,15 @@ cudaError_t launch_ta_mode(const TaArgs& ta, cudaStream_t st) {
     return ta_map(k, a.k, a.hd, a.hkv, a.tokens, a.k_hs, a.k_ts, 1, rows) &&
            ta_map(v, a.v, a.hd, a.hkv, a.tokens, a.v_hs, a.v_ts, 1, rows);
   };
-  return ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt) && maps(ta.km, ta.vm, ta.box_rows) &&
-         (a.window == 0 || maps(ta.ks, ta.vs, 16));
+  if constexpr (Mode == kPaWindow)
+    if (!maps(ta.ks, ta.vs, 16)) return false;
+  return ta_map(ta.qm, a.q, a.hd, a.hq, a.tokens, a.q_hs, a.q_ts, G, ta.tpt) && maps(ta.km, ta.vm, ta.box_rows);
 }
 // Items of a causal or windowed call.
 template <int Mode>
 cudaError_t launch_ta_items(const PAttn& a, int num_sms, cudaStream_t st) {
-  TaArgs ta{};
-  if (!ta_args(ta, a)) return cudaErrorInvalidValue;
+  TaArgsOf<Mode> ta{};
+  if (!ta_args<Mode>(ta, a)) return cudaErrorInvalidValue;
   ta.pairs = (std::min(a.max_q, a.tokens) + 2 * ta.tpt - 1) / (2 * ta.tpt);
   // A block reads all the keys that its rows see, so blocks of one KV head
   // run together and share them in L2: as many heads at a time as give the
@@ -1011,9 +1027,9 @@ cudaError_t launch_ta_items(const PAttn& a, int num_sms, cudaStream_t st) {
   ta.split = most * (uneven ? 1 : 2) <= num_sms && max_keys >= 16 * kTaKeys ? 2 : 1;
   // new tokens few beside their contexts: a walk's length is its sequence's
   ta.by_length = Mode == kPaCausal && a.paged && a.seqs <= 32 && max_keys >= 2LL * a.max_q ? 1 : 0;
-  // Where blocks cover the items, each keeps to its own: one that starts early would take
+  // (Windows:) where blocks cover the items, each keeps to its own: one that starts early would take
   // items whose blocks find free SMs (136 items of 18 steps in a grid of 256: 65 -> 36 us).
-  ta.take = ta.split == 1 && (Mode == kPaCausal || most > num_sms);
+  if constexpr (Mode == kPaWindow) ta.take = ta.split == 1 && most > num_sms;
   return launch_ta_mode<Mode>(ta, st);
 }
 

@@ -230,6 +230,48 @@ def test_window_waits_that_run_out(hd, dtype):
     _give_up(lambda o, l: sv.attn_paged(q, c, cu, lens, max_q=256, out=o, lse=l, window=1500, sinks=4), q, (1, 2, 5))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 6, 40, 200])
+def test_window_far_past_everything(dtype, n):
+    """The longest table there is, and windows and first tokens near 2^31: no place of a walk leaves 32 bits."""
+    ns, ctx = [n, n], [700, 513]
+    c, q, cu, lens = _paged_case(78, 16, 4, 128, 256, dtype, ns, ctx)
+    t = torch.full((2, 0x7fffff00 // 256), -1, dtype=torch.int32, device="cuda")
+    t[:, :c.max_pages] = c.table
+    values = _all_values(c, ctx)
+    far = sv.KVCache(c.k, c.v, t, c.k_scale, c.v_scale)
+    for window, sinks in ((0x7ffffeff, 0x7fffffff), (2 ** 30 + 1, 0), (2 ** 30 + 1, 2 ** 31 + 7), (0x7ffffeff, 5)):
+        _window_check(far, q, cu, lens, ns, ctx, window, sinks, values, max_q=n)
+    _window_check(far, q, cu, lens, ns, ctx, 100, 2 ** 31 - 1, values, max_q=n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_more_past_32_bit_offsets(dtype):
+    """Pages that lie past 2^31 elements: written by qkv_append, read in a window and behind a shared prefix."""
+    hk, ps, hd, hq = 8, 256, 128, 32
+    pages = 2 ** 31 // (hk * ps * hd) + 12
+    if torch.cuda.mem_get_info()[0] < 4 * pages * hk * ps * hd * (2 if dtype == "bf16" else 1):
+        pytest.skip("not enough memory")
+    g = _gen(17)
+    table = torch.full((3, 4000), -1, dtype=torch.int32, device="cuda")
+    table[:, :4] = pages - 12 + torch.randperm(12, generator=g, device="cuda").int().view(3, 4)
+    table[1:, :2] = table[0, :2]
+    c = sv.KVCache.empty(pages, ps, hk, hd, table, dtype)
+    ctx, ns = [900, 700, 1000], [6, 6, 6]
+    plan, gain = sv.rope_plan(hd, 500000.0), torch.exp(0.3 * _randn(g, hd))
+    for b, m in enumerate(ctx):
+        pos = torch.arange(m, device="cuda").int()
+        x = _randn(g, m, hq + 2 * hk, hd).bfloat16()
+        live = pos if b == 0 else torch.where(pos < 2 * ps, -1, pos)     # (the shared pages are written once)
+        sv.qkv_append(c, x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], torch.full_like(pos, b), live, plan, gain, gain)
+    q = _randn(g, 18, hq, hd).bfloat16()
+    cu, lens, values = _i32([0, 6, 12, 18]), _i32(ctx), _all_values(c, ctx)
+    assert all(v.abs().amax() > 0 for kv in values for v in kv)
+    _window_check(c, q, cu, lens, ns, ctx, 300, 4, values, max_q=6)
+    assert _shares(c, 1, 18, 6, hq)
+    _shared_check(c, q, cu, lens, ns, ctx, _i32([2 * ps]), None, 6)
+
+
 # ------------------------------------------------------------ shared prefixes
 def _shared_case(seed, hq, hk, hd, ps, dtype, ns, first, shared, rests, pad=0):
     """Sequences whose rows of the table begin alike within a group; slots past the lengths hold NaN.

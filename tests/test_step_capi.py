@@ -52,6 +52,8 @@ def test_page_refusals(L):
     for name in ("lens", "counts", "free", "left", "cu", "out", "seq", "pos", "lacking"):
         assert _reserve(L, c, **{name: None}) == -1, name
     assert _reserve(L, c, cap=-1) == _reserve(L, c, n=-1) == _reserve(L, c, n=2 ** 31 - 1) == -1
+    many = ctypes.byref(_cache(seqs=2 ** 30 + 1))
+    assert _reserve(L, many) == _release(L, many) == -1
     assert _reserve(L, c, out=P) == -1                       # the new lengths over the old
     assert _reserve(L, None) == _release(L, None) == -1
     for name in ("lens", "keep", "free", "left"):
@@ -137,6 +139,10 @@ def test_binding_refusals(L):
             sv._gain("gain", bad, (64,), -1)
     with pytest.raises(sv.SpecError, match="requires grad"):
         sv._gain("gain", torch.ones(64, requires_grad=True), (64,), -1)
+    for bad in ((-1, 0), (0, -1), (-2 ** 40, 5)):
+        with pytest.raises(sv.SpecError, match="negative"):
+            sv._window(*bad)
+    assert sv._window(2 ** 40, 7) == (0x7fffffff, 7)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
