@@ -142,6 +142,10 @@ struct __align__(16) ShPlan {
 __host__ __device__ inline size_t sh_slots_at(int n_groups, int seqs) {
   return (sizeof(ShPlan) + (size_t)n_groups * sizeof(ShGroup) + (size_t)seqs * sizeof(ShSeq) + 255) & ~(size_t)255;
 }
+SV_DEV int sh_begin(int run, int units, int runs) {
+  const uint64_t n = (uint64_t)units * run;
+  return n >> 32 ? (int)(n / (uint32_t)runs) : (int)((uint32_t)n / (uint32_t)runs);
+}
 SV_DEV int sh_run(int unit, int units, int runs) {   // the run of a unit; run r begins at units * r / runs
   const uint64_t n = ((uint64_t)unit + 1) * runs - 1;
   return n >> 32 ? (int)(n / (uint32_t)units) : (int)((uint32_t)n / (uint32_t)units);

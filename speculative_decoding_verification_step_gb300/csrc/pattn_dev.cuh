@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kPaThreads, PaLayout<HD, F8, NT>::blocks)
 
   // this block's steps, and the warp's: s0 + 4 j
   const int steps = (see_max + kPaStep - 1) / kPaStep - gap;
-  const int s_beg = (int)((int64_t)steps * share / C), s_end = (int)((int64_t)steps * (share + 1) / C);
+  const int s_beg = steps * share / C, s_end = steps * (share + 1) / C;   // (up to 2^27 steps, 8 shares)
   const int s0 = s_beg + warp;
   const int nj = s_end > s0 ? (s_end - s0 + kPaWarps - 1) / kPaWarps : 0;
   unsigned char* ring = sm + L::q_bytes + (size_t)warp * D * L::stage;

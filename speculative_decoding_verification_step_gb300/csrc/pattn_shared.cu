@@ -55,6 +55,8 @@ __global__ void __launch_bounds__(kShThreads) shared_plan_kernel(const __grid_co
   ShGroup* groups = sh_groups(a.ws);
   int unit = 0, tile = 0, seq_end = 0, row_end = 0;
   float rest = 0.f;
+  // the thread's first sequence, on its way
+  int r0 = (int)threadIdx.x < a.seqs ? __ldg(a.cu + threadIdx.x) : 0, r1 = (int)threadIdx.x < a.seqs ? __ldg(a.cu + threadIdx.x + 1) : 0;
   for (int g0 = 0; g0 < a.n_groups; g0 += kWarps) {
     const int g = g0 + warp;
     if (g < a.n_groups) {
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kShThreads) shared_plan_kernel(const __grid_co
         unit += a.hkv * o.pairs * o.steps;
         tile += a.hkv * o.pairs;
         rest += s_rest[w];
-        groups[g0 + w] = o;
+        groups[g0 + w] = s_group[w] = o;
       }
     __syncthreads();
   }
@@ -104,8 +106,11 @@ __global__ void __launch_bounds__(kShThreads) shared_plan_kernel(const __grid_co
       else end = mid;
     }
     ShSeq o{};
-    const ShGroup& gr = groups[g];
-    const int r0 = __ldg(a.cu + s), r1 = __ldg(a.cu + s + 1);
+    const ShGroup gr = a.n_groups <= kWarps ? s_group[g] : groups[g];
+    if (s >= kShThreads) {
+      r0 = __ldg(a.cu + s);
+      r1 = __ldg(a.cu + s + 1);
+    }
     if ((!a.groups || (__ldg(a.groups + g) <= s && s < __ldg(a.groups + g + 1))) && r0 >= gr.row0 && r1 <= gr.row0 + gr.toks)
       o = ShSeq{gr.eff, gr.row0, gr.unit0, gr.tile0, gr.pairs, gr.steps, {0, 0}};   // (else there is no order in cu)
     sh_seqs(a.ws, a.n_groups)[s] = o;

@@ -204,33 +204,39 @@ __global__ void __launch_bounds__(TaLayout<HD, F8, Mode>::threads, 1) pattn_tc_k
   // Prefixes: the part of this block's run that starts at unit u; false at its end.
   [[maybe_unused]] auto part_at = [&](int u, TaItem& it) {
     if constexpr (Mode == kPaPrefix) {
-      const volatile ShPlan* plan = reinterpret_cast<const volatile ShPlan*>(a.ws);
-      const volatile ShGroup* groups = reinterpret_cast<const volatile ShGroup*>(plan + 1);
-      const int units = plan->units, runs = plan->runs, run = (int)blockIdx.x;
+      // the plan and the first groups' records, one a lane, in one round of loads
+      const int4* at = reinterpret_cast<const int4*>(sh_groups(a.ws));
+      const int4 plan = __ldcg(reinterpret_cast<const int4*>(a.ws));      // units, runs
+      int4 x = __ldcg(at + 2 * min(lane, a.n_groups - 1)), y = __ldcg(at + 2 * min(lane, a.n_groups - 1) + 1);   // a ShGroup
+      const int units = plan.x, runs = plan.y, run = (int)blockIdx.x;
       if (run >= runs) return false;
-      const int end = (int)((int64_t)units * (run + 1) / runs);
-      if (u < 0) u = (int)((int64_t)units * run / runs);
+      const int end = sh_begin(run + 1, units, runs);
+      if (u < 0) u = sh_begin(run, units, runs);
       if (u >= end) return false;
       int g = 0;                                 // the last group that begins at or before u: one that holds units
       for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
-        const unsigned in = __ballot_sync(0xffffffffu, g0 + lane < a.n_groups && groups[min(g0 + lane, a.n_groups - 1)].unit0 <= u);
+        const int first = g0 == 0 ? x.y : __ldcg(&sh_groups(a.ws)[min(g0 + lane, a.n_groups - 1)].unit0);
+        const unsigned in = __ballot_sync(0xffffffffu, g0 + lane < a.n_groups && first <= u);
         if (in) g = g0 + 31 - __clz(in);
       }
-      const volatile ShGroup& gr = groups[g];
-      const int in = u - gr.unit0, steps = gr.steps, tile = in / steps, off = in - tile * steps;
-      it.kvh = tile / gr.pairs;
-      it.b = gr.seq0;
-      it.r_first = gr.row0;
-      it.toks = gr.toks;
-      it.keys = gr.eff;
-      it.first_pos = gr.eff;
-      it.tok0 = (tile - it.kvh * gr.pairs) * 2 * tpt;
+      if (g >= 32) {
+        x = __ldcg(at + 2 * g);
+        y = __ldcg(at + 2 * g + 1);
+      }
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, g & 31); };
+      const int in = u - of(x.y), steps = of(y.w), pairs = of(y.z), tile = in / steps, off = in - tile * steps;
+      it.kvh = tile / pairs;
+      it.b = of(y.y);
+      it.r_first = of(x.w);
+      it.toks = of(y.x);
+      it.keys = it.first_pos = of(x.x);
+      it.tok0 = (tile - it.kvh * pairs) * 2 * tpt;
       it.ntile = it.tok0 + tpt < it.toks ? 2 : 1;
       it.beg = off;
       it.nst = min(steps - off, end - u);
       it.steps[0] = it.nst;
       it.steps[1] = it.ntile == 2 ? it.nst : 0;
-      it.slot = run + gr.tile0 + tile;
+      it.slot = run + of(x.z) + tile;
       it.unit = u + it.nst;
       return true;
     } else {

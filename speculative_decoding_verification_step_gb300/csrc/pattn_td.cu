@@ -117,7 +117,7 @@ SV_DEV int td_total(const PAttn& a, int tile_rows) {   // units of the call; who
   return sum;
 }
 SV_DEV int td_runs(int total, int most) { return max(1, min(most, total)); }
-SV_DEV int td_begin(int total, int run, int runs) { return (int)((int64_t)total * run / runs); }
+SV_DEV int td_begin(int total, int run, int runs) { return sh_begin(run, total, runs); }
 struct TdUnit {
   int b, kvh, tile, off, upi;
 };
