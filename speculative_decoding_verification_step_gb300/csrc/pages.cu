@@ -12,9 +12,12 @@
 // Sequences come in chunks of kPgThreads, a chunk's sums in shared memory.  One block is
 // enough for a verify step; where there is more to write, a cluster of eight shares the
 // writes: every block sums for itself (the inputs are a few KB and lie in L2), and the
-// stack's count changes behind a barrier of the cluster, when all have read it.  No
-// atomics: the pages that a sequence gets depend on the arguments alone.
-// Bound by latency: loads, two scans, searches, stores.
+// stack's count changes behind a barrier of the cluster, when all have read it.  Beyond
+// 64 thousand tokens the blocks are as many as the writes need, and the count changes in a
+// launch behind them (960 thousand tokens and the release of their pages 61 -> 22 us).
+// No atomics: the pages that a sequence gets depend on the arguments alone.
+// Bound by latency: loads, two scans, searches, stores.  64 sequences x 6 tokens and their
+// release 7.9 us replayed from a graph; as calls 25 us of host time, 8 of them the results.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -72,11 +75,6 @@ SV_DEV int find_run(const int* at, int n, int i) {
   }
   return lo;
 }
-SV_DEV uint32_t pg_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 SV_DEV void pg_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -96,14 +94,14 @@ struct PageArgs {
   int32_t* seq;
   int32_t* pos;
   int32_t* lacking;
-  int blocks;                    // 1, or the cluster's
+  int blocks;                    // 1, the cluster's, or more without a cluster
   int vec;                       // seq and pos take 16-byte stores
 };
 
 __global__ void __launch_bounds__(kPgThreads) reserve_kernel(const __grid_constant__ PageArgs a) {
   __shared__ Sums warps[kPgThreads / 32];
   __shared__ int s_tok[kPgThreads + 1], s_page[kPgThreads + 1], s_len[kPgThreads], s_had[kPgThreads];
-  const int tid = threadIdx.x, rank = a.blocks > 1 ? (int)pg_rank() : 0;
+  const int tid = threadIdx.x, rank = (int)blockIdx.x;
   const int me = rank * kPgThreads + tid, all = a.blocks * kPgThreads;
   const int left = max(0, min(ld_volatile_i32(a.n_free), a.free_cap)), ps1 = (1 << a.shift) - 1;
   const int64_t cap = (int64_t)a.max_pages << a.shift;
@@ -168,19 +166,30 @@ __global__ void __launch_bounds__(kPgThreads) reserve_kernel(const __grid_consta
     __syncthreads();                           // the chunk's sums are read
   }
   for (int64_t i = given.toks + me; i < a.tokens; i += all) a.seq[i] = a.pos[i] = -1;
-  if (a.blocks > 1) pg_cluster_sync();         // all have read the count
+  if (a.blocks == kPgCluster) pg_cluster_sync();   // all have read the count
   else __syncthreads();
   if (rank == 0 && tid == 0) {
     a.cu[0] = 0;
-    *a.n_free = left - (int)given.pages;
+    if (a.blocks <= kPgCluster) *a.n_free = left - (int)given.pages;
     *a.lacking = (int)min((int64_t)0x7fffffff, max((int64_t)0, asked.pages - left));
   }
+}
+
+// The stack's count behind blocks that share no barrier: less the pages that the lengths grew by.
+__global__ void __launch_bounds__(kPgThreads) reserve_end_kernel(const __grid_constant__ PageArgs a) {
+  __shared__ Sums warps[kPgThreads / 32];
+  const int ps1 = (1 << a.shift) - 1;
+  Sums mine{0, 0}, total;
+  for (int b = threadIdx.x; b < a.seqs; b += kPgThreads)
+    mine.pages += (((int64_t)__ldg(a.lens_out + b) + ps1) >> a.shift) - (((int64_t)__ldg(a.lens + b) + ps1) >> a.shift);
+  block_sums(mine, warps, total);
+  if (threadIdx.x == 0) *a.n_free = max(0, min(*a.n_free, a.free_cap)) - (int)total.pages;
 }
 
 __global__ void __launch_bounds__(kPgThreads) release_kernel(const __grid_constant__ PageArgs a) {
   __shared__ Sums warps[kPgThreads / 32];
   __shared__ int s_page[kPgThreads + 1], s_beg[kPgThreads];
-  const int tid = threadIdx.x, rank = a.blocks > 1 ? (int)pg_rank() : 0;
+  const int tid = threadIdx.x, rank = (int)blockIdx.x;
   const int me = rank * kPgThreads + tid, all = a.blocks * kPgThreads;
   const int left = max(0, min(ld_volatile_i32(a.n_free), a.free_cap)), ps1 = (1 << a.shift) - 1, room = a.free_cap - left;
   const int64_t cap = (int64_t)a.max_pages << a.shift;
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(kPgThreads) release_kernel(const __grid_consta
     done += count;
     __syncthreads();
   }
-  if (a.blocks > 1) pg_cluster_sync();
+  if (a.blocks == kPgCluster) pg_cluster_sync();
   else __syncthreads();
   if (rank == 0 && tid == 0) *a.n_free = left + (int)min((int64_t)room, done);
 }
@@ -251,8 +260,12 @@ int spec_kv_reserve(const spec_kv_cache* cache, const int32_t* kv_lens, const in
   if (kv_lens_out == kv_lens) return fail(SPEC_E_ARG, std::string(who) + ": kv_lens_out must not be kv_lens");
   a.tokens = tokens; a.cu = cu_q; a.lens_out = kv_lens_out; a.seq = seq; a.pos = pos; a.lacking = lacking;
   a.vec = ((reinterpret_cast<uintptr_t>(seq) | reinterpret_cast<uintptr_t>(pos)) & 15u) == 0;
-  a.blocks = tokens > 8 * kPgThreads ? kPgCluster : 1;
-  return done(launch_rows(reserve_kernel, dim3(a.blocks), dim3(kPgThreads), 0, a.blocks, (cudaStream_t)stream, a), who);
+  const bool many = tokens > 65536;
+  a.blocks = many ? std::min(296, tokens / 1024) : tokens > 8 * kPgThreads ? kPgCluster : 1;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = launch_rows(reserve_kernel, dim3(a.blocks), dim3(kPgThreads), 0, many ? 1 : a.blocks, st, a);
+  if (e == cudaSuccess && many) e = launch_rows(reserve_end_kernel, dim3(1), dim3(kPgThreads), 0, 1, st, a);
+  return done(e, who);
 }
 
 int spec_kv_release(const spec_kv_cache* cache, const int32_t* kv_lens, const int32_t* keep, int32_t* free_pages,

@@ -40,14 +40,24 @@
 // and merges through distributed shared memory in a fixed order (no scratch
 // memory, no second launch, no atomics): blocks merge their four warps, then
 // block j of the cluster finishes the rows j, j + C, ...
+// What a row sees of the keys up to its own is the kernel's Mode (paged.h).  A window's
+// tile walks the steps of the first tokens and then those that its rows' windows reach;
+// within them keys that no row sees are not read, others are masked as those past
+// the length are.  The rest behind a shared prefix is a walk that starts there, and
+// leaves sums for the join.
 // Bound: by the copies for a few rows (64 sequences x 4096 keys of 8 heads of
-// 128, 16-bit, one token each: 129 us, 91% of a copy's rate; 16 x 16384 of 64
-// dims 66 us, 89%; 64 x 4096 8-bit of 128 dims 86 us, 71%), by the latencies of a
+// 128, 16-bit, one token each: 128 us, 92% of a copy's rate; 16 x 16384 of 64
+// dims 65 us, 90%; 64 x 4096 8-bit of 128 dims 84 us, 73%), by the latencies of a
 // step's instructions (three warps a partition) for more: 24 rows of 64 x 4096
-// 164 us (75%), 8-bit 153 us (40%), which is why long 8-bit contexts go to tensor
+// 151 us (81%), 8-bit 153 us (40%), which is why long 8-bit contexts go to tensor
 // memory.  8-bit rows of 64 dims hold half the bytes for the same conversions a
-// step: 64 x 4096 65 us of one token (49%), 108 us of 24 rows (29%).  One sequence of 512 keys and 24 rows takes 9 us, most of it the
-// start, one walk of a few steps and two merges.
+// step: 64 x 4096 63 us of one token (51%), 99 us of 24 rows (32%).  One sequence of
+// 512 keys and 24 rows takes 7.7 us, most of it the start, one walk of a few steps
+// and two merges.  (A warp's rows of Q are loaded at once, ahead of the page ids: one
+// after another behind them they were 1.4 us of 9.)
+// A window of 1024 in contexts of 16384: 64 sequences of one token 51 us (78%), 8-bit 30
+// (67%), of six 68 us (60%); 16 of one token and 64 dims 9 us (55%): a walk is a few steps
+// a warp, and its start and merges do not shrink with it.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

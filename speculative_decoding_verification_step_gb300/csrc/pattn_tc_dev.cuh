@@ -54,6 +54,18 @@
 // four chunks of up to 512 tokens over up to 16384 keys 164 us (1.1 PFLOP/s), four
 // of 512 over 16384 364 us (78%), with 8-bit keys 514 us (56%); head dim 64, four
 // prompts of 4096 349 us (42%).
+// Windows (Mode, paged.h).  An item walks the first tokens and, close behind them, the keys
+// from the first that its first token's window reaches, so that four first tokens are 16 keys
+// of a step and not a step of their own (six prompts in a window of 1024 173 -> 158 us); boxes
+// are then 16 rows where a step holds both, else pages or 128 rows of a prompt.  A row's
+// mask is 128 bits, from three bounds that go down by a step's keys.  Of nine steps an item
+// takes in that window 8.25 would do, and the fixed time of an item is a third of its time:
+// 158 us is 1.05 PFLOP/s of what the rows see (55%).  Four chunks of up to 512 in a window
+// of 2048 36 us: 136 items of 18 steps, fewer than SMs, 1.4 us a step and 10 around them.
+// Prefixes (pattn_shared.cu): no mask; a block's items are the parts of its run, and their sums
+// leave as they are.  8-bit ones keep four tiles of codes in flight, where the other modes keep
+// rows on their way out, and have eight warps to convert them: either alone gained 2%,
+// both 6% of 96 us (64 x 6 tokens behind four prompts).
 #pragma once
 #include <cuda_runtime.h>
 
@@ -97,8 +109,8 @@ using TaArgsOf = std::conditional_t<Mode == kPaWindow, TaWindowArgs, TaArgs>;
 
 template <int HD, bool F8, int Mode>
 struct TaLayout {
-  // 8-bit prefixes leave as sums, a row by its thread, in whole sectors: the room where other rows
-  // wait on their way out holds more codes in flight, and eight warps convert them.
+  // 8-bit prefixes: sums leave by the thread that holds the row, in whole sectors, the room where
+  // other rows wait on their way out holds more codes in flight, and eight warps convert them.
   static constexpr bool deep = F8 && Mode == kPaPrefix;
   static constexpr int convert = deep ? 8 : 4;             // warps that convert codes
   static constexpr int threads = F8 ? 384 + 32 * convert : 384;

@@ -104,7 +104,8 @@ def test_reserve(ps, width, lens, counts, left, tokens):
 
 
 @pytest.mark.parametrize("seqs,most,left", [(511, 9, 10 ** 6), (512, 40, 700), (513, 300, 10 ** 6), (1500, 7, 900),
-                                            (2, 20000, 10 ** 6), (40, 1500, 2000)])
+                                            (2, 20000, 10 ** 6), (40, 1500, 2000), (5, 60000, 10 ** 6), (600, 400, 5000),
+                                            (9, 30000, 9000)])
 def test_reserve_and_release_many(seqs, most, left):
     """More sequences than a block sums at once, more writes than a block makes, stacks that run short."""
     g = torch.Generator().manual_seed(seqs)
