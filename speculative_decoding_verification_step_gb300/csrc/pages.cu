@@ -227,7 +227,7 @@ int page_args(PageArgs& a, const spec_kv_cache* cache, const int32_t* lens, cons
   const std::string w = std::string(who) + ": ";
   const int rc = check_cache(cache, who);
   if (rc) return rc;
-  if (!lens || !change || !free_pages || !n_free) return fail(SPEC_E_ARG, w + "null pointer");
+  if (!lens || !change || (!free_pages && free_cap > 0) || !n_free) return fail(SPEC_E_ARG, w + "null pointer");
   if (cache->seqs > 1 << 30) return fail(SPEC_E_ARG, w + "too many sequences");
   if (free_cap < 0) return fail(SPEC_E_ARG, w + "bad capacity of the free stack");
   a.table = const_cast<int32_t*>(cache->table);

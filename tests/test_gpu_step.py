@@ -140,6 +140,34 @@ def test_release(ps, width, lens, keep, stack, left):
     assert (c.table.tolist(), f.tolist(), n.tolist()) == (want[0], want[1], [want[2]])
 
 
+def test_pages_without_a_stack():
+    """A stack of no entries: what needs no page is served, what does gets nothing, dropped pages are lost."""
+    c = _pages(2, 4, 16, 64, torch.arange(8, device="cuda").int().view(2, 4))
+    free, n = torch.empty(0, dtype=torch.int32, device="cuda"), _i32([5])
+    cu, lens, seq, pos, lacking = sv.kv_reserve(c, _i32([3, 15]), _i32([4, 2]), free, n, 9)
+    assert (cu.tolist(), lens.tolist(), lacking.tolist(), n.tolist()) == ([0, 4, 4], [7, 15], [1], [0])
+    assert seq.tolist() == [0] * 4 + [-1] * 5 and pos.tolist() == [3, 4, 5, 6] + [-1] * 5
+    sv.kv_release(c, _i32([64, 64]), _i32([0, 17]), free, n)
+    assert c.table.tolist() == [[-1] * 4, [4, 5, -1, -1]] and n.tolist() == [0]
+
+
+def test_no_tokens():
+    """A step of nothing writes nothing and returns what has no rows."""
+    c = _pages(2, 4, 16, 8)
+    x = torch.zeros(0, 6, 32, dtype=torch.bfloat16, device="cuda")
+    none, plan = torch.empty(0, dtype=torch.int32, device="cuda"), sv.rope_plan(32, 10000.0)
+    gain = torch.ones(32, device="cuda")
+    assert sv.qkv_append(c, x[:, :4], x[:, 4:5], x[:, 5:], none, none, plan, gain, gain).shape == (0, 4, 32)
+    assert sv.rope_norm_rows(x, none, plan, gain).shape == (0, 6, 32)
+    zero, n = _i32([0, 0]), _i32([3])
+    cu, lens, seq, pos, lacking = sv.kv_reserve(c, zero, zero, _i32([1, 2, 3]), n, 0)
+    assert cu.tolist() == [0, 0, 0] and lens.tolist() == [0, 0] and seq.numel() == pos.numel() == 0
+    q = torch.zeros(0, 4, 32, dtype=torch.bfloat16, device="cuda")
+    for out, lse in (sv.attn_paged(q, c, cu, lens, window=5, sinks=1), sv.attn_shared(q, c, cu, lens, _i32([3])),
+                     sv.attn_prompt(q, q[:, :1], q[:, :1], cu, window=5)):
+        assert out.shape == (0, 4, 32) and lse.shape == (0, 4)
+
+
 def test_pages_replayed_and_strided():
     """A captured step, replayed: the stack, the table and the lengths move on from where they are."""
     ps, seqs, width = 16, 3, 8

@@ -56,6 +56,7 @@ def test_page_refusals(L):
     assert _reserve(L, many) == _release(L, many) == -1
     assert _reserve(L, c, out=P) == -1                       # the new lengths over the old
     assert _reserve(L, None) == _release(L, None) == -1
+    assert _reserve(L, c, free=None, cap=1) == _release(L, c, free=None, cap=1) == -1
     for name in ("lens", "keep", "free", "left"):
         assert _release(L, c, **{name: None}) == -1, name
     assert _release(L, c, cap=-1) == -1
