@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
     if (pass == 0) {   // the first loads are on their way while the angles are worked out
       for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
         const int tt = i / np, k = i - tt * np;
-        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), a.sign, cs + tt * pad + k, si + tt * pad + k);
+        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), a.sign, cs + tt * pad + angle_at<V>(k, pad),
+                     si + tt * pad + angle_at<V>(k, pad));
       }
       __syncthreads();
     }
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
       float xa[V], xb[V];
       ra.get(xa);
       rb.get(xb);
-      unit_rotate<V>(xa, xb, u, rot, a.r.interleaved, cs + t * pad, si + t * pad);
+      unit_rotate<V>(xa, xb, u, rot, a.r.interleaved, cs + t * pad, si + t * pad, pad);
       store_v<TO, V>(y + ca * V, xa);
       store_v<TO, V>(y + cb * V, xb);
     }
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
         slot[threadIdx.x] = cache_slot(a.c, __ldg(a.seq + t0 + threadIdx.x), __ldg(a.pos + t0 + threadIdx.x));
       for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
         const int tt = i / np, k = i - tt * np;
-        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), 1.f, cs + tt * pad + k, si + tt * pad + k);
+        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), 1.f, cs + tt * pad + angle_at<V>(k, pad),
+                     si + tt * pad + angle_at<V>(k, pad));
       }
       __syncthreads();
     }
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
     for (int j = 0; j < kUpl; ++j) {
       ra[q][j].get(xa[j]);
       rb[q][j].get(xb[j]);
-      if (rot) unit_rotate<V>(xa[j], xb[j], j * kLanes + lane, rot, a.r.interleaved, cs + t * pad, si + t * pad);
+      if (rot) unit_rotate<V>(xa[j], xb[j], j * kLanes + lane, rot, a.r.interleaved, cs + t * pad, si + t * pad, pad);
     }
     const size_t base = (size_t)(h << a.c.shift) + s.y;
     if constexpr (!F8) {

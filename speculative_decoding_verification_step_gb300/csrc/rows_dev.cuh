@@ -117,9 +117,16 @@ SV_DEV void unit_chunks(int u, int rot, int inter, int* a, int* b) {
     *b = 2 * u + 1;
   }
 }
+// Place of angle k among a token's `pad` in shared memory.  Units of eight read theirs as two
+// quads: first quads lie side by side, then the second, so that adjacent lanes find them in
+// distinct banks.
+template <int V>
+SV_DEV int angle_at(int k, int pad) {
+  return V == 1 ? k : (k & 4 ? pad / 2 : 0) + ((k >> 3) << 2) + (k & 3);
+}
 // Rotates the two chunks of unit u (xa, xb) by the token's cosines and sines.
 template <int V>
-SV_DEV void unit_rotate(float (&xa)[V], float (&xb)[V], int u, int rot, int inter, const float* co, const float* si) {
+SV_DEV void unit_rotate(float (&xa)[V], float (&xb)[V], int u, int rot, int inter, const float* co, const float* si, int pad) {
   if constexpr (V == 1) {
     if (u >= rot / 2) return;
     const float c = co[u], n = si[u], p = xa[0], q = xb[0];
@@ -131,7 +138,8 @@ SV_DEV void unit_rotate(float (&xa)[V], float (&xb)[V], int u, int rot, int inte
     float c[8], n[8];
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(co + u * 8 + i), y = *reinterpret_cast<const float4*>(si + u * 8 + i);
+      const int at = u * 4 + (i ? pad / 2 : 0);
+      const float4 x = *reinterpret_cast<const float4*>(co + at), y = *reinterpret_cast<const float4*>(si + at);
       c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
       n[i] = y.x; n[i + 1] = y.y; n[i + 2] = y.z; n[i + 3] = y.w;
     }
