@@ -10,16 +10,17 @@
 // one rounding at the store.  Angles and 8-bit rows as in kvrows.cu.
 //
 // Bound by HBM for prompts, by launch and dependent loads for a verify step's rows.
-// Blocks of q, of k and of v lie side by side in one grid, 512 threads' work each (256:
-// 72 us, 1024: 70 below).
-// Measured: 4 x 4000 rows of 32 + 8 + 8 bf16 heads of 128 to an e4m3 cache 68.5 us (5.3 TB/s,
-// 78% of a copy's rate), to a bf16 one 67 us (87%), from fp32 rows 87 us (100%); 16381 rows of
-// 40 heads of 64 32.7 us (5.1 TB/s); a step's 6 tokens 3.2 us.  Beside its 32 bytes of a
-// bf16 row a lane reads 64 of cosines and sines and 64 of gains from shared memory and
-// L1, whose pipe is busy for 75% of the time.  Keeping them in registers over several
-// heads (or gains over several tokens) took 94 registers a thread for 56, and with the
-// fewer rows in flight 74 us (69) for 68.5; three rows of a thread in flight 91, the
-// compiler held to 48 registers 71.
+// Blocks of q, of k and of v lie side by side in one grid, 1024 threads' work each (512: 2%
+// more for 40 heads of 64).
+// Measured: 4 x 4000 rows of 32 + 8 + 8 bf16 heads of 128 to an e4m3 cache 64 us (5.6 TB/s,
+// 83% of a copy's rate), to a bf16 one 65 us (90%), from fp32 rows 88 us (99%); 16381 rows of
+// 40 heads of 64 30 us (5.6 TB/s, 83%); a step's 6 tokens 3.0 us.  Beside its 32 bytes of a
+// bf16 row a lane reads 64 of cosines and sines from shared memory and 64 of gains from L1,
+// whose pipe was busy for 75% of the time while lanes met in banks and gains came in
+// fours (69 and 33 us), and is for 57% now; issue slots are at 68%.  Angles in registers
+// over several heads (or gains over several tokens) took 94 registers a thread for 56, and
+// with the fewer rows in flight 74 us (69) for 68.5; three rows of a thread in flight 91, the
+// compiler held to 48 registers 71; packed fp32 arithmetic in the norm changes nothing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -286,7 +287,7 @@ cudaError_t launch_qkv(QkvArgs& a, bool vec, cudaStream_t st) {
       continue;
     }
     const int64_t units = (int64_t)p.heads * per;
-    p.tpb = few ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokBlock, 4 * kRowThreads / units));
+    p.tpb = few ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokBlock, 8 * kRowThreads / units));
     p.hpb = few ? std::min(p.heads, std::max(1, kRowThreads / per)) : p.heads;
     p.hblocks = (p.heads + p.hpb - 1) / p.hpb;
     const int64_t n = (int64_t)((a.tokens + p.tpb - 1) / p.tpb) * p.hblocks;
