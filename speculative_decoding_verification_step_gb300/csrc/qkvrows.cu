@@ -12,8 +12,8 @@
 // Bound by HBM for prompts, by launch and dependent loads for a verify step's rows.
 // Blocks of q, of k and of v lie side by side in one grid, 1024 threads' work each (512: 2%
 // more for 40 heads of 64).
-// Measured: 4 x 4000 rows of 32 + 8 + 8 bf16 heads of 128 to an e4m3 cache 64 us (5.6 TB/s,
-// 83% of a copy's rate), to a bf16 one 65 us (90%), from fp32 rows 88 us (99%); 16381 rows of
+// Measured: 4 x 4000 rows of 32 + 8 + 8 bf16 heads of 128 to an e4m3 cache 65 us (5.5 TB/s,
+// 82% of a copy's rate), to a bf16 one 65 us (90%), from fp32 rows 88 us (99%); 16381 rows of
 // 40 heads of 64 30 us (5.6 TB/s, 83%); a step's 6 tokens 3.0 us.  Beside its 32 bytes of a
 // bf16 row a lane reads 64 of cosines and sines from shared memory and 64 of gains from L1,
 // whose pipe was busy for 75% of the time while lanes met in banks and gains came in
@@ -72,6 +72,25 @@ SV_DEV uint32_t lanes_max(uint32_t m) {
   return m;
 }
 
+// Rows without a norm turn by the same angles, to the bit, as in rope_rows and kv_append; of normed
+// ones those whose rounding is fp32's, or so coarse that its neighbours count (codes), turn by the
+// finer ones (16381 rows to fp32 off by 6.4e-8 of their size for 7.6e-8, PyTorch 6.9e-8).
+template <typename TO, bool F8>
+SV_DEV bool fine_angles(const QkvPart& p, int kind) {
+  return p.gain && (kind ? F8 : sizeof(TO) == 4);
+}
+SV_DEV void row_cos_sin(const spec_rope& r, bool fine, int i, int pos, float* c, float* s) {
+  if (fine) turn_cos_sin_fine(r, i, pos, c, s);
+  else turn_cos_sin(r, i, pos, 1.f, c, s);
+}
+// 1 / sqrt(m) with one correction: the function is off by up to two units, as a factor of the
+// whole row.
+SV_DEV float inverse_root(float m) {
+  const float y = rsqrtf(m);
+  if (!(y > 0.f && y < 3e38f)) return y;       // of 0, infinity or NaN
+  const float h = m * y, l = fmaf(m, y, -h);   // m y, exactly
+  return fmaf(0.5f * y, fmaf(-l, y, fmaf(-h, y, 1.f)), y);
+}
 // Eight gains in one load: two of four, 32 bytes apart from lane to lane, take L1 twice as long.
 SV_DEV void load_gain8(float (&x)[8], const float* p) {
   asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -117,7 +136,8 @@ __global__ void __launch_bounds__(kRowThreads) qkv_kernel(const __grid_constant_
         slot[threadIdx.x] = cache_slot(a.c, __ldg(a.seq + t0 + threadIdx.x), __ldg(a.pos + t0 + threadIdx.x));
       for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
         const int tt = i / np, k = i - tt * np;
-        turn_cos_sin(a.r, k, __ldg(a.pos + t0 + tt), 1.f, cs + tt * pad + angle_at<V>(k, pad), si + tt * pad + angle_at<V>(k, pad));
+        row_cos_sin(a.r, fine_angles<TO, F8>(p, kind), k, __ldg(a.pos + t0 + tt), cs + tt * pad + angle_at<V>(k, pad),
+                    si + tt * pad + angle_at<V>(k, pad));
       }
       __syncthreads();
     }
@@ -133,7 +153,7 @@ __global__ void __launch_bounds__(kRowThreads) qkv_kernel(const __grid_constant_
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-        const float inv = rsqrtf(lanes_sum<kLanes>(ss) * (1.f / HD) + a.eps);
+        const float inv = inverse_root(lanes_sum<kLanes>(ss) * (1.f / HD) + a.eps);
         const float* g = p.gain + (h0 + h) * p.gain_hs;
         float ga[V], gb[V];
         load_gain8(ga, g + ca * V);
@@ -204,7 +224,7 @@ __global__ void __launch_bounds__(kRowThreads) qkv_any_kernel(const __grid_const
     ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
   }
   if (p.gain) {
-    const float inv = rsqrtf(warp_sum(ss) / (float)a.hd + a.eps);
+    const float inv = inverse_root(warp_sum(ss) / (float)a.hd + a.eps);
     const float* g = p.gain + h * p.gain_hs;
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) {
@@ -222,7 +242,7 @@ __global__ void __launch_bounds__(kRowThreads) qkv_any_kernel(const __grid_const
     const int u = lane + 32 * j;
     if (u < p.rot / 2) {
       float c, n;
-      turn_cos_sin(a.r, u, pos, 1.f, &c, &n);
+      row_cos_sin(a.r, fine_angles<TO, F8>(p, kind), u, pos, &c, &n);
       const float e = xa[j], f = xb[j];
       xa[j] = e * c - f * n;
       xb[j] = f * c + e * n;

@@ -27,6 +27,17 @@ SV_DEV void turn_cos_sin(const spec_rope& r, int i, int pos, float sign, float* 
   *cos_out = c * r.mscale;
   *sin_out = s * r.mscale * sign;
 }
+// The same with what the fraction's rounding to fp32 leaves (up to 9e-8 of a radian) put back by
+// the sine's and cosine's slopes: normed rows, whose 8-bit codes are as often the wrong
+// neighbour as the row before the rounding is off.
+SV_DEV void turn_cos_sin_fine(const spec_rope& r, int i, int pos, float* cos_out, float* sin_out) {
+  const int turn = (int)((r.turn[i] * (uint64_t)(int64_t)pos) >> 32);
+  const float f = (float)turn, left = (float)(turn - __float2int_rz(f)) * (4.656612873077393e-10f * 3.1415927f);
+  float s, c;
+  sincospif(f * 4.656612873077393e-10f, &s, &c);
+  *cos_out = fmaf(-s, left, c) * r.mscale;
+  *sin_out = fmaf(c, left, s) * r.mscale;
+}
 // n / d for n * d < 2^32, by m = ceil(2^32 / d) (0 for d = 1).
 SV_DEV int quick_div(int n, uint32_t m) { return m ? (int)__umulhi((uint32_t)n, m) : n; }
 [[maybe_unused]] uint32_t div_magic(int64_t d) { return d <= 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); }
