@@ -467,14 +467,33 @@ def sample_rows(logits, temperature, seed, step_base=0, position=1, stream=None,
 # refused while grad mode is on (a Function of one's own runs with it off:
 # rope_rows with `inverse` is the gradient of rope_rows).
 _t = None
+_packed = None
 
 
 def _torch():
-    global _t
+    global _t, _packed
     if _t is None:
         import torch
+        # torch.empty on the current device without its parsing and dispatch, where torch has it:
+        # between launches an allocation costs 1 us for 3
+        guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+        _packed = getattr(guards, "_empty_strided_cuda", None)
         _t = torch
     return _t
+
+
+def _empty(dev, shape, dtype):
+    """A packed tensor on CUDA device `dev`."""
+    if _packed is None or _t._C._cuda_getDevice() != dev:
+        return _t.empty(shape, dtype=dtype, device=_t.device("cuda", dev))
+    shape = tuple(shape)                     # (no torch.Size)
+    n = len(shape)
+    if n == 1:
+        return _packed(shape, (1,), dtype)
+    if n == 2:
+        return _packed(shape, (max(shape[1], 1), 1), dtype)
+    d = max(shape[2], 1)
+    return _packed(shape, (max(shape[1], 1) * d, d, 1), dtype)
 
 
 def _refuse(msg):
@@ -626,7 +645,7 @@ def rope_rows(x, pos, plan, out=None, dtype=None, inverse=False, stream=None):
     dev = x.get_device()
     _index("pos", pos, n, dev)
     if out is None:
-        out = _alloc(stream, x.device, lambda: _t.empty(shape, dtype=x.dtype if dtype is None else dtype, device=x.device))
+        out = _alloc(stream, x.device, lambda: _empty(dev, shape, x.dtype if dtype is None else dtype))
         ys = out.stride()
     else:
         if out.shape != shape or out.get_device() != dev or (dtype is not None and dtype is not out.dtype):
@@ -665,9 +684,7 @@ def kv_gather(cache, seq, pos, dtype=None, stream=None):
     shape = (n, cache.n_kv_heads, cache.head_dim)
     if dtype is None:
         dtype = _t.bfloat16
-    where = cache.device
-    k, v = _alloc(stream, where, lambda: (_t.empty(shape, dtype=dtype, device=where),
-                                          _t.empty(shape, dtype=dtype, device=where)))
+    k, v = _alloc(stream, cache.device, lambda: (_empty(dev, shape, dtype), _empty(dev, shape, dtype)))
     _call(dev, stream, lib().spec_kv_gather, cache._ref, seq.data_ptr(), pos.data_ptr(), n, k.data_ptr(),
           v.data_ptr(), _io_dtype(k))
     return k, v
@@ -692,7 +709,7 @@ def rope_norm_rows(x, pos, plan, gain, eps=1e-5, out=None, dtype=None, stream=No
     _index("pos", pos, n, dev)
     _gain("gain", gain, shape[2:] if gain.dim() == 1 else shape[1:], dev)
     if out is None:
-        out = _alloc(stream, x.device, lambda: _t.empty(shape, dtype=x.dtype if dtype is None else dtype, device=x.device))
+        out = _alloc(stream, x.device, lambda: _empty(dev, shape, x.dtype if dtype is None else dtype))
         ys = out.stride()
     else:
         if out.shape != shape or out.get_device() != dev or (dtype is not None and dtype is not out.dtype):
@@ -726,7 +743,7 @@ def qkv_append(cache, q, k, v, seq, pos, plan=None, q_norm=None, k_norm=None, ep
         if g is not None:
             _gain(name, g, shape[2:], dev)
     if out is None:
-        out = _alloc(stream, cache.device, lambda: _t.empty(qshape, dtype=_t.bfloat16, device=cache.device))
+        out = _alloc(stream, cache.device, lambda: _empty(dev, qshape, _t.bfloat16))
         os_ = out.stride()
     else:
         if out.shape != qshape or out.dtype is not _t.bfloat16 or out.get_device() != dev:
@@ -763,9 +780,8 @@ def kv_reserve(cache, kv_lens, counts, free, n_free, tokens, stream=None):
     _stack(cache, free, n_free)
     if not 0 <= tokens <= 0x7fffff00:
         _refuse("tokens: a bound on the step's tokens, up to 2^31 - 256")
-    where = cache.device
-    cu, lens, seq, pos, lacking = _alloc(stream, where, lambda: [
-        _t.empty(n, dtype=_t.int32, device=where) for n in (seqs + 1, seqs, tokens, tokens, 1)])
+    cu, lens, seq, pos, lacking = _alloc(stream, cache.device, lambda: [
+        _empty(dev, (n,), _t.int32) for n in (seqs + 1, seqs, tokens, tokens, 1)])
     _call(dev, stream, lib().spec_kv_reserve, cache._ref, kv_lens.data_ptr(), counts.data_ptr(), free.data_ptr(),
           n_free.data_ptr(), free.shape[0], tokens, cu.data_ptr(), lens.data_ptr(), seq.data_ptr(), pos.data_ptr(),
           lacking.data_ptr())
@@ -797,11 +813,10 @@ def _attn_out(q, shape, dev, out, lse, need, stream):
         _refuse("lse: contiguous fp32 [tokens, heads]")
     if out is not None and lse is not None and not need:
         return out, lse, None
-    where = q.device
-    return _alloc(stream, where, lambda: (
-        _t.empty(shape, dtype=_t.bfloat16, device=where) if out is None else out,
-        _t.empty(shape[:2], dtype=_t.float32, device=where) if lse is None else lse,
-        _t.empty(need, dtype=_t.uint8, device=where) if need else None))
+    return _alloc(stream, q.device, lambda: (
+        _empty(dev, shape, _t.bfloat16) if out is None else out,
+        _empty(dev, shape[:2], _t.float32) if lse is None else lse,
+        _empty(dev, (need,), _t.uint8) if need else None))
 
 
 def _window(window, sinks):
