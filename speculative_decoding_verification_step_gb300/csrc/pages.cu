@@ -17,7 +17,7 @@
 // launch behind them (960 thousand tokens and the release of their pages 61 -> 22 us).
 // No atomics: the pages that a sequence gets depend on the arguments alone.
 // Bound by latency: loads, two scans, searches, stores.  64 sequences x 6 tokens and their
-// release 7.9 us replayed from a graph; as calls 25 us of host time, 8 of them the results.
+// release 7.9 us replayed from a graph; as calls 19 to 23 us of host time, 3 of them the results.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -371,3 +371,25 @@ def test_qkv_append_in_place_and_streams():
         sv.qkv_append(c, x[:, :8], x[:, 8:10], x[:, 10:], seq, pos, plan, gain[:32], gain)
     with pytest.raises(sv.SpecError):
         sv.qkv_append(c, x[:, :8].float(), x[:, 8:10], x[:, 10:], seq, pos, plan, gain, gain)
+
+
+# ------------------------------------------------------- results' allocation
+@pytest.mark.parametrize("shape", [(0,), (7,), (5, 3), (0, 3), (4, 0), (6, 5, 64), (0, 5, 64), (6, 0, 64), (6, 5, 0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.int32, torch.uint8])
+def test_results_are_packed_like_torchs_own(shape, dtype, monkeypatch):
+    sv._torch()
+    fast = sv._empty(0, torch.Size(shape), dtype)
+    monkeypatch.setattr(sv, "_packed", None)       # torch without the short call
+    slow = sv._empty(0, torch.Size(shape), dtype)
+    for t in (fast, slow):
+        assert t.shape == torch.Size(shape) and t.dtype == dtype and t.device == torch.device("cuda", 0)
+        assert t.stride() == torch.empty(shape, dtype=dtype).stride()
+    assert not fast.requires_grad
+
+
+def test_calls_without_the_short_allocation(monkeypatch):
+    x, pos = _randn(_gen(5), 9, 4, 64), _i32(list(range(9)))
+    plan = sv.rope_plan(64, 10000.0)
+    with_it = sv.rope_rows(x, pos, plan)
+    monkeypatch.setattr(sv, "_packed", None)
+    assert torch.equal(sv.rope_rows(x, pos, plan), with_it)
