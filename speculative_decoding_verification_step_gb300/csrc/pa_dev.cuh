@@ -175,7 +175,9 @@ SV_DEV void ta_regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" 
 template <int N>
 SV_DEV void ta_regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 // Four codes times a pair of equal powers of two as bf16 pairs: exact where bf16
-// holds the value; a NaN code is NaN.
+// holds the value; a NaN code is NaN.  A tile of 128 x 128 codes takes eight warps 586
+// clocks this way; moving the bits by shifts and masks under one bf16x2 product, with a
+// check for NaN codes, gave the same bits in 733.
 SV_DEV void ta_codes(uint32_t w, uint64_t scale, uint32_t& lo, uint32_t& hi) {
   uint32_t h[2];
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
