@@ -202,6 +202,10 @@ int64_t most_tiles(const PAttn& a) {
   return (int64_t)a.hkv * (a.tokens / (2 * tpt) + std::min<int64_t>(a.n_groups, a.tokens));
 }
 
+// The parts of 8-bit prefixes leave in 32-byte stores and slots lie at multiples of 32 bytes from the
+// workspace's start, which callers align to 16: the start moves up to 32, in room asked for that.
+constexpr size_t kShAlign = 32;
+
 }  // namespace
 
 size_t pattn_shared_workspace(const PAttn& a, int num_sms) {
@@ -209,12 +213,13 @@ size_t pattn_shared_workspace(const PAttn& a, int num_sms) {
   const int64_t keys = (int64_t)a.max_pages << a.page_shift, tiles = most_tiles(a);
   const int64_t rows = (int64_t)std::min(a.max_q, a.tokens) * a.hq;
   if (tiles * ((keys + kTaKeys - 1) / kTaKeys) > 0x3fffffffLL || (rows + 7) / 8 * a.seqs > 0x7fffffffLL) return 0;
-  return sh_slots_at(a.n_groups, a.seqs) + ((size_t)(num_sms + tiles) * 256 + (size_t)a.tokens * a.hq) * (a.hd + 2) * sizeof(float);
+  return kShAlign - 16 + sh_slots_at(a.n_groups, a.seqs) + ((size_t)(num_sms + tiles) * 256 + (size_t)a.tokens * a.hq) * (a.hd + 2) * sizeof(float);
 }
 
 cudaError_t launch_pattn_shared(const PAttn& call, int num_sms, cudaStream_t st) {
   PAttn a = call;
   a.runs = num_sms;
+  a.ws = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(a.ws) + kShAlign - 1) & ~(uintptr_t)(kShAlign - 1));
   a.rest = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(a.ws) + sh_slots_at(a.n_groups, a.seqs)) +
            (size_t)(num_sms + most_tiles(a)) * 256 * (a.hd + 2);
   TaArgs ta{};

@@ -519,3 +519,27 @@ def test_serving_loop(dtype, hd, ps):
         assert n_free.item() == held - pages
     sv.kv_release(c, lens, _i32([prompt] * seqs), free, n_free)
     assert n_free.item() == held and sorted(free.tolist()) == list(range(shared_pages, pool))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_shared_workspace_alignment(dtype, hd):
+    """Workspaces at any multiple of 16 bytes: the same bits, and nothing outside the bytes asked for."""
+    ns, first, shared = [3] * 6, [0, 4, 6], [1500, 333]
+    c, q, cu, lens, ctx = _shared_case(29, 16, 4, hd, 32, dtype, ns, first, shared, [7, 300] * 3)
+    c = _wide(c)
+    assert _shares(c, 2, 18, 3, 16)
+    sh, gr, n = _i32(shared), _i32(first), 18
+    ref = sv.attn_shared(q, c, cu, lens, sh, groups=gr, max_q=3)
+    L = sv.lib()
+    need = L.spec_attn_shared_workspace(c._ref, 2, n, 3, 16)
+    ws = torch.empty(need + 512, dtype=torch.uint8, device="cuda")
+    assert ws.data_ptr() % 256 == 0
+    for at in (16, 32, 48, 112, 0):
+        ws.fill_(0xff)
+        out, lse = torch.zeros(n, 16, hd, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 16, device="cuda")
+        assert L.spec_attn_shared(c._ref, q.data_ptr(), q.stride(0), q.stride(1), cu.data_ptr(), lens.data_ptr(),
+                                  gr.data_ptr(), 2, sh.data_ptr(), n, 3, 16, 0.0, out.data_ptr(), 16 * hd, hd,
+                                  lse.data_ptr(), ws.data_ptr() + at, need, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+        assert (ws[:at] == 0xff).all() and (ws[at + need:] == 0xff).all()
