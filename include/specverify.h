@@ -552,10 +552,12 @@ SPEC_API int spec_attn_prompt_window(const void* q, int64_t q_tok_stride, int64_
  * 1], ascending; NULL with n_groups 1: all), and the caller says that their rows
  * of the table name the same pages for the first shared[g] positions (device int32;
  * any number, it need not end with a page and is cut to what every row of the group
- * sees).  Sequences outside every group share nothing.  The result is that
+ * sees).  Sequences outside every group share nothing; neither length nor table of a
+ * sequence without rows in the call is used.  The result is that
  * of spec_attn_paged, some roundings apart: the sums over the prefix and over the
  * rest of a row are fp32 and joined in fp32.  Which row of the table the prefix
- * is read by is not said, so where the rows name other pages the result is neither's.
+ * is read by (of a sequence with rows) is not said, so where the rows name other
+ * pages the result is neither's.
  * Groups or cu_q out of order give rows without meaning, and no access outside
  * the buffers.  A value row that is not finite within the prefix reaches
  * the rows of the whole group.

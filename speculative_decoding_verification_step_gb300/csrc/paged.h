@@ -126,7 +126,7 @@ struct __align__(16) ShGroup {
   int unit0;       // its first unit: 128 keys of one (KV head, pair of row tiles)
   int tile0;       // its first (KV head, pair of row tiles)
   int row0, toks;  // first row, rows
-  int seq0;        // the sequence whose table row is read
+  int seq0;        // the sequence whose table row is read: the group's first with rows
   int pairs, steps;
 };
 // What a sequence shares with its group (eff 0: nothing), for the rest and the join.

@@ -56,6 +56,7 @@ ShCost sh_cost(const PAttn& a) {
 __global__ void __launch_bounds__(kShThreads) shared_plan_kernel(const __grid_constant__ PAttn a, ShCost cost) {
   constexpr int kWarps = kShThreads / 32;
   __shared__ ShGroup s_group[kWarps];
+  __shared__ int s_first[kWarps];
   __shared__ float s_rest[kWarps];             // keys behind the prefixes, and as many as a block's start costs
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tpt = kTaRows / (a.hq / a.hkv);
@@ -73,15 +74,15 @@ __global__ void __launch_bounds__(kShThreads) shared_plan_kernel(const __grid_co
       ShGroup o{};
       float keys;
       int seqs;
-      o.eff = sh_eff(a, g, first, last, &keys, &seqs);
+      o.eff = sh_eff(a, g, first, last, &keys, &seqs, &o.seq0);
       if (r.toks == 0) o.eff = 0;
       o.row0 = r.row0;
       o.toks = r.toks;
-      o.seq0 = first;
       o.pairs = (r.toks + 2 * tpt - 1) / (2 * tpt);
       o.steps = (o.eff + kTaKeys - 1) / kTaKeys;
       if (lane == 0) {
         s_group[warp] = o;
+        s_first[warp] = first;
         s_rest[warp] = keys + (float)seqs * (cost.block - (float)o.eff);
       }
     }
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kShThreads) shared_plan_kernel(const __grid_co
       for (int w = 0; w < kWarps && g0 + w < a.n_groups; ++w) {
         ShGroup o = s_group[w];
         // (groups or rows out of order hold nothing: the tiles stay within what the workspace has room for)
-        if (o.seq0 < seq_end || o.row0 < row_end) o.eff = o.toks = 0;
+        if (s_first[w] < seq_end || o.row0 < row_end) o.eff = o.toks = 0;
         if (o.eff == 0) o.pairs = o.steps = 0;
         if (o.toks > 0) {
           seq_end = a.groups ? __ldg(a.groups + g0 + w + 1) : a.seqs;

@@ -543,3 +543,24 @@ def test_shared_workspace_alignment(dtype, hd):
                                   lse.data_ptr(), ws.data_ptr() + at, need, torch.cuda.current_stream().cuda_stream) == 0
         assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
         assert (ws[:at] == 0xff).all() and (ws[at + need:] == 0xff).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd,ns,first,shared", [
+    (128, [0, 2, 1, 0, 3], [0, 5], [400]),
+    (64, [0, 0, 4, 4, 0, 0, 0, 1, 2], [0, 4, 9], [640, 77]),
+    (128, [0, 1] + [0] * 40 + [1, 1], [0, 1, 44], [300, 512]),       # the second of the group; a group of none
+])
+def test_shared_behind_idle_sequences(dtype, hd, ns, first, shared):
+    """Sequences without new tokens whose pages were given back (no length, cleared entries), the groups'
+    first ones among them: the prefix is that of the others."""
+    c, q, cu, lens, ctx = _shared_case(23 + hd, 16, 4, hd, 16, dtype, ns, first, shared, [n + 9 for n in ns], pad=2)
+    for b, n in enumerate(ns):
+        if n == 0:
+            c.table[b], lens[b], ctx[b] = -1, 0, 0
+    c = _wide(c)
+    sh, gr = _i32(shared), _i32(first)
+    assert _shares(c, len(shared), q.shape[0], max(ns), 16)
+    _shared_check(c, q, cu, lens, ns, ctx, sh, gr, max(ns))
+    c.table[torch.tensor(ns, device="cuda") == 0] = 2 ** 30
+    _shared_check(c, q, cu, lens, ns, ctx, sh, gr, max(ns))
