@@ -458,8 +458,10 @@ SPEC_API int spec_rope_norm_rows(const void* x, int x_dtype, int64_t x_tok_strid
  * spec_kv_release: sequence b keeps the first keep[b] of its kv_lens[b] positions
  * (both cut to 0 .. the table's room, keep to the length); the pages past them
  * go back to the stack in order of sequences and positions, and their entries
- * become -1.  A page that several rows name (a shared prefix) must not be
- * dropped by more than one of them.  What the stack has no room for is lost.
+ * become -1.  Entries that are negative already (pages in front of a window, which
+ * the caller has given back itself) are left out.  A page that several rows name
+ * (a shared prefix) must not be dropped by more than one of them.  What the stack
+ * has no room for is lost.
  *
  * The cache's pools are not touched.  Both read and write n_free, the stack and
  * the table in place: calls on one cache go one behind the other. */

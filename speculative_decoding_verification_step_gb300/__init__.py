@@ -791,8 +791,10 @@ def kv_reserve(cache, kv_lens, counts, free, n_free, tokens, stream=None):
 def kv_release(cache, kv_lens, keep, free, n_free, stream=None):
     """The pages of positions keep[b] .. kv_lens[b] - 1 of every sequence b
     (int32 [seqs]: the lengths with the tokens that are dropped, and without)
-    back to the stack free[: n_free]; their entries of the table become -1.  A
-    page that several sequences name must not be dropped by more than one."""
+    back to the stack free[: n_free]; their entries of the table become -1.
+    Entries that are negative already (given back by the caller, as pages in
+    front of a window) are left out.  A page that several sequences name must
+    not be dropped by more than one."""
     _torch()
     dev = cache._dev
     _index("kv_lens", kv_lens, cache.seqs, dev)

@@ -8,16 +8,21 @@
 //   reserve  the i-th page needed, in order of sequences and positions, is the i-th from
 //            the top of the free stack; token i of the step finds its sequence by a
 //            search in the sums, four tokens a thread.
-//   release  the i-th page dropped goes to place n_free + i of the stack.
+//   release  the i-th page dropped goes to place n_free + i of the stack.  Entries that a
+//            program has cleared itself (negative: the pages in front of a window) are no
+//            pages, so the places follow from what the table holds: a block takes its run of
+//            the dropped entries into shared memory, and the blocks of a cluster tell each
+//            other how many pages are among them (64 prompts' release 1.3 us of 11.4; a step's
+//            few entries are the first block's, 0.3).
 // Sequences come in chunks of kPgThreads, a chunk's sums in shared memory.  One block is
 // enough for a verify step; where there is more to write, a cluster of eight shares the
 // writes: every block sums for itself (the inputs are a few KB and lie in L2), and the
 // stack's count changes behind a barrier of the cluster, when all have read it.  Beyond
 // 64 thousand tokens the blocks are as many as the writes need, and the count changes in a
-// launch behind them (960 thousand tokens and the release of their pages 61 -> 22 us).
+// launch behind them (960 thousand tokens and the release of their pages 61 -> 21 us).
 // No atomics: the pages that a sequence gets depend on the arguments alone.
 // Bound by latency: loads, two scans, searches, stores.  64 sequences x 6 tokens and their
-// release 7.9 us replayed from a graph; as calls 19 to 23 us of host time, 3 of them the results.
+// release 8.2 us replayed from a graph; as calls 19 to 23 us of host time, 3 of them the results.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,6 +38,8 @@ namespace {
 
 constexpr int kPgThreads = 512;
 constexpr int kPgCluster = 8;
+constexpr int kPgBatch = 4;        // dropped entries of a thread on their way
+constexpr int kPgHeld = 8192;      // dropped entries of a block at a time
 
 struct Sums {
   int64_t pages, toks;
@@ -77,6 +84,13 @@ SV_DEV int find_run(const int* at, int n, int i) {
 }
 SV_DEV void pg_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *at of block `rank` of the cluster.
+SV_DEV int pg_peer(const int* at, int rank) {
+  int v;
+  asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %1, %2;\n ld.shared::cluster.u32 %0, [p];\n}"
+               : "=r"(v) : "r"(smem_u32(at)), "r"(rank) : "memory");
+  return v;
 }
 
 struct PageArgs {
@@ -188,37 +202,89 @@ __global__ void __launch_bounds__(kPgThreads) reserve_end_kernel(const __grid_co
 
 __global__ void __launch_bounds__(kPgThreads) release_kernel(const __grid_constant__ PageArgs a) {
   __shared__ Sums warps[kPgThreads / 32];
-  __shared__ int s_page[kPgThreads + 1], s_beg[kPgThreads];
+  __shared__ int s_page[kPgThreads + 1], s_beg[kPgThreads], s_held[kPgHeld], s_kept[2];
   const int tid = threadIdx.x, rank = (int)blockIdx.x;
-  const int me = rank * kPgThreads + tid, all = a.blocks * kPgThreads;
   const int left = max(0, min(ld_volatile_i32(a.n_free), a.free_cap)), ps1 = (1 << a.shift) - 1, room = a.free_cap - left;
   const int64_t cap = (int64_t)a.max_pages << a.shift;
-  int64_t done = 0;
-  for (int b0 = 0; b0 < a.seqs; b0 += kPgThreads) {
+  int64_t done = 0, solo = 0;                  // pages that went before: of runs that all know of, of the block's since
+  for (int b0 = 0, odd = 0; b0 < a.seqs; b0 += kPgThreads) {
     const int b = b0 + tid, n = min(kPgThreads, a.seqs - b0);
     const int64_t len = b < a.seqs ? min(cap, (int64_t)max(0, __ldg(a.lens + b))) : 0;
     const int64_t keep = b < a.seqs ? min(len, (int64_t)max(0, __ldg(a.change + b))) : 0;
     const int beg = (int)((keep + ps1) >> a.shift), end = (int)((len + ps1) >> a.shift);
     Sums total;
     const Sums at = block_sums(Sums{end - beg, 0}, warps, total);
-    // (a stack cannot hold more than free_cap: what would lie past it is dropped)
     s_page[tid + 1] = (int)min((int64_t)0x7fffffff, at.pages);
     s_beg[tid] = beg;
     if (tid == 0) s_page[0] = 0;
     __syncthreads();
-    const int count = (int)min((int64_t)0x7fffffff, total.pages);
-    for (int64_t i = me; i < count; i += all) {
-      const int r = find_run(s_page, n, (int)i);
-      int32_t* entry = a.table + (b0 + r) * a.tstride + s_beg[r] + ((int)i - s_page[r]);
-      if (done + i < room) a.free_pages[left + done + i] = *entry;
-      *entry = -1;
+    const unsigned count = (unsigned)min((int64_t)0x7fffffff, total.pages), most = (unsigned)a.blocks * kPgHeld;
+    for (unsigned t0 = 0; t0 < count; t0 += most) {
+      // the block's run of the next entries (few of them are the first block's): out of the table, and counted
+      const unsigned in = min(most, count - t0);
+      const bool split = a.blocks == kPgCluster && in > kPgThreads;
+      const unsigned i_beg = t0 + (split ? in * rank >> 3 : rank ? in : 0), i_end = t0 + (split ? in * (rank + 1) >> 3 : in);
+      const unsigned run = i_end - i_beg;
+      int sound = 0, mine = 0;
+      for (unsigned i0 = tid; i0 < run; i0 += kPgBatch * kPgThreads) {
+        int32_t* e[kPgBatch];
+        int page[kPgBatch];
+#pragma unroll
+        for (int k = 0; k < kPgBatch; ++k) {   // (all on their way: the entries written are not those read)
+          const unsigned i = i0 + k * kPgThreads;
+          e[k] = nullptr;
+          if (i < run) {
+            const int at = (int)(i_beg + i), r = find_run(s_page, n, at);
+            e[k] = a.table + (b0 + r) * a.tstride + s_beg[r] + (at - s_page[r]);
+            page[k] = *e[k];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kPgBatch; ++k)
+          if (e[k]) {
+            *e[k] = -1;
+            s_held[i0 + k * kPgThreads] = page[k];
+            sound += page[k] >= 0;
+            ++mine;
+          }
+      }
+      unsigned kept = run;
+      if (!__syncthreads_and(sound == mine)) {
+        block_sums(Sums{sound, 0}, warps, total);
+        kept = (unsigned)total.pages;
+      }
+      int64_t place = done + solo;             // of the run's first page in the stack, from n_free on
+      solo += kept;
+      if (split) {
+        if (tid == 0) s_kept[odd] = (int)solo;
+        __syncwarp();
+        pg_cluster_sync();
+        for (int c = 0; c < kPgCluster; ++c) {
+          const int k = pg_peer(&s_kept[odd], c);
+          if (c < rank) place += k;
+          done += k;
+        }
+        solo = 0;
+        odd ^= 1;
+      }
+      // (a stack cannot hold more than free_cap: what would lie past it is dropped)
+      if (kept == run) {
+        for (unsigned i = tid; i < run; i += kPgThreads)
+          if (place + i < room) a.free_pages[left + place + i] = s_held[i];
+      } else {
+        for (unsigned i0 = 0; i0 < run; i0 += kPgThreads) {
+          const int page = i0 + tid < run ? s_held[i0 + tid] : -1;
+          const Sums before = block_sums(Sums{page >= 0, 0}, warps, total);
+          const int64_t to = place + before.pages - 1;
+          if (page >= 0 && to < room) a.free_pages[left + to] = page;
+          place += total.pages;
+        }
+      }
+      __syncthreads();                         // s_held is read
     }
-    done += count;
-    __syncthreads();
   }
-  if (a.blocks == kPgCluster) pg_cluster_sync();
-  else __syncthreads();
-  if (rank == 0 && tid == 0) *a.n_free = left + (int)min((int64_t)room, done);
+  if (a.blocks == kPgCluster) pg_cluster_sync();   // all have read the count, and each other's
+  if (rank == 0 && tid == 0) *a.n_free = left + (int)min((int64_t)room, done + solo);
 }
 
 // The checks that both calls share.

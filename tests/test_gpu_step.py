@@ -393,3 +393,82 @@ def test_calls_without_the_short_allocation(monkeypatch):
     with_it = sv.rope_rows(x, pos, plan)
     monkeypatch.setattr(sv, "_packed", None)
     assert torch.equal(sv.rope_rows(x, pos, plan), with_it)
+
+
+# ------------------------------------------------------- cleared entries
+def _release_sound_ref(table, ps, lens, keep, free, left):
+    """_release_ref over rows some of whose entries are cleared (negative) already: those are no pages."""
+    table, free = [list(r) for r in table], list(free)
+    left = max(0, min(left, len(free)))
+    for b, (n, k) in enumerate(zip(lens, keep)):
+        n = min(max(0, n), len(table[b]) * ps)
+        k = min(max(0, k), n)
+        for j in range(-(-k // ps), -(-n // ps)):
+            if table[b][j] >= 0 and left < len(free):
+                free[left] = table[b][j]
+                left += 1
+            table[b][j] = -1
+    return table, free, left
+
+
+@pytest.mark.parametrize("seqs,width,cleared,stack,left", [
+    (1, 4, 0.5, 4, 0), (3, 40, 0.3, 200, 7), (3, 40, 1.0, 200, 7), (3, 400, 0.01, 2000, 100), (7, 300, 0.5, 900, 0),
+    (1, 30000, 0.5, 40000, 17), (5, 9000, 0.002, 50000, 0), (9, 7000, 0.9, 3000, 1000), (513, 20, 0.2, 20000, 5),
+    (1200, 9, 0.5, 4000, 3990), (1600, 40, 0.4, 70000, 1), (2, 8000, 0.0, 20000, 3),
+])
+def test_release_of_cleared_entries(seqs, width, cleared, stack, left):
+    """What a program cleared itself, as the pages in front of a window, is not taken for a page; the others
+    lie in the stack in order, in rows of one and of many blocks' work, in stacks with room and without."""
+    g = torch.Generator().manual_seed(seqs + width)
+    ps = 16
+    table = torch.randperm(seqs * width, generator=g).int().view(seqs, width)
+    gone = torch.rand(seqs, width, generator=g) < cleared
+    table[gone] = torch.randint(-2 ** 31, 0, (int(gone.sum()),), generator=g).int()
+    lens = torch.randint(width * ps // 2, width * ps + 40, (seqs,), generator=g).tolist()
+    keep = [x if i % 5 == 3 else int(x * (i % 4) / 5) for i, x in enumerate(lens)]
+    want = _release_sound_ref(table.tolist(), ps, lens, keep, list(range(stack)), left)
+    c = _pages(seqs, width, ps, 64, table.cuda())
+    f, n = _i32(list(range(stack))), _i32([left])
+    sv.kv_release(c, _i32(lens), _i32(keep), f, n)
+    assert n.tolist() == [want[2]] and f.tolist() == want[1] and c.table.tolist() == want[0]
+    sv.kv_release(c, _i32(lens), _i32(keep), f, n)             # again: nothing is left to give back
+    assert n.tolist() == [want[2]] and f.tolist() == want[1] and c.table.tolist() == want[0]
+
+
+def test_pages_left_behind_by_a_window():
+    """A program clears the entries in front of its window and gives their pages back itself; the sequence's
+    release then leaves every page in the stack once, and what is reserved from it holds rows."""
+    ps, pages = 16, 24
+    table = torch.full((2, 64), -1, dtype=torch.int32, device="cuda")
+    c = sv.KVCache.empty(pages, ps, 1, 32, table)
+    free, n = torch.arange(pages, device="cuda").int(), _i32([pages])
+    _, lens, *_ = sv.kv_reserve(c, _i32([0, 0]), _i32([200, 150]), free, n, 400)
+    behind = table[0, :7].tolist()                             # positions in front of a window of 80
+    left = n.item()
+    free[left:left + 7] = _i32(behind)
+    n.fill_(left + 7)
+    table[0, :7] = -1
+    sv.kv_release(c, lens, _i32([0, 0]), free, n)
+    assert n.item() == pages and sorted(free.tolist()) == list(range(pages)) and (table == -1).all()
+    cu, lens, seq, pos, lacking = sv.kv_reserve(c, _i32([0, 0]), _i32([190, 190]), free, n, 380)
+    assert lacking.item() == 0 and n.item() == 0
+    x = _randn(_gen(1), 380, 1, 32).bfloat16()
+    sv.kv_append(c, x, x, seq, pos)
+    k, v = sv.kv_gather(c, seq, pos)
+    assert torch.equal(k, x) and torch.equal(v, x)
+
+
+def test_release_of_few_and_many_by_turns():
+    """Few dropped entries, then many, and again: what one block placed alone moves the others' places."""
+    g = torch.Generator().manual_seed(11)
+    ps, seqs, width, stack = 16, 2100, 30, 70000
+    table = torch.randperm(seqs * width, generator=g).int().view(seqs, width)
+    table[torch.rand(seqs, width, generator=g) < 0.3] = -1
+    lens = [width * ps] * seqs
+    drops = lambda b: b // 512 % 2 == 1 or b % 512 in (7, 100, 101)
+    keep = [17 * (b % 20) if drops(b) else lens[b] for b in range(seqs)]
+    want = _release_sound_ref(table.tolist(), ps, lens, keep, list(range(stack)), 40)
+    c = _pages(seqs, width, ps, 64, table.cuda())
+    f, n = _i32(list(range(stack))), _i32([40])
+    sv.kv_release(c, _i32(lens), _i32(keep), f, n)
+    assert n.tolist() == [want[2]] and f.tolist() == want[1] and c.table.tolist() == want[0]
