@@ -472,3 +472,57 @@ def test_release_of_few_and_many_by_turns():
     f, n = _i32(list(range(stack))), _i32([40])
     sv.kv_release(c, _i32(lens), _i32(keep), f, n)
     assert n.tolist() == [want[2]] and f.tolist() == want[1] and c.table.tolist() == want[0]
+
+
+@pytest.mark.parametrize("det", [False, True])
+def test_results_under_deterministic_algorithms(det):
+    """Torch fills what it allocates while deterministic algorithms are asked for: so with the results' rows
+    that a call leaves as they were."""
+    c = _pages(1, 4, 16, 8, _i32([[0, 1, 2, 3]]))
+    q = torch.ones(5, 4, 32, dtype=torch.bfloat16, device="cuda")
+    on, fill = torch.are_deterministic_algorithms_enabled(), torch.utils.deterministic.fill_uninitialized_memory
+    try:
+        torch.use_deterministic_algorithms(True)
+        torch.utils.deterministic.fill_uninitialized_memory = det
+        for _ in range(3):
+            junk = [torch.full((5, 4, 32), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 4), 3.0, device="cuda")]
+            del junk                                     # (what the memory holds when the results take it)
+            out, lse = sv.attn_paged(q, c, _i32([0, 2]), _i32([9]))
+            assert torch.isfinite(out[:2].float()).all() and torch.isfinite(lse[:2]).all()
+            if det:
+                assert out[2:].isnan().all() and lse[2:].isnan().all()
+    finally:
+        torch.use_deterministic_algorithms(on)
+        torch.utils.deterministic.fill_uninitialized_memory = fill
+
+
+def test_results_under_modes():
+    """Dispatch and function modes and profilers see the results' allocation, and a result made in inference mode is one."""
+    from torch.overrides import TorchFunctionMode
+    from torch.utils._python_dispatch import TorchDispatchMode
+    seen = []
+
+    class Dispatch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            seen.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    class Function(TorchFunctionMode):
+        def __torch_function__(self, func, types, args=(), kwargs=None):
+            seen.append(getattr(func, "__name__", ""))
+            return func(*args, **(kwargs or {}))
+
+    x, pos, plan = _randn(_gen(5), 9, 4, 64), _i32(list(range(9))), sv.rope_plan(64, 10000.0)
+    ref = sv.rope_rows(x, pos, plan)
+    for mode in (Dispatch, Function):
+        seen.clear()
+        with mode():
+            y = sv.rope_rows(x, pos, plan)
+        assert any("empty" in s for s in seen), mode
+        assert torch.equal(y, ref)
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as prof:
+        sv.rope_rows(x, pos, plan)
+    assert any(e.key == "aten::empty" for e in prof.key_averages())
+    with torch.inference_mode():
+        y = sv.rope_rows(x, pos, plan)
+    assert y.is_inference() and not ref.is_inference() and torch.equal(y, ref)
