@@ -452,7 +452,8 @@ SPEC_API int spec_rope_norm_rows(const void* x, int x_dtype, int64_t x_tok_strid
  * the table's new entries (the i-th page needed is the i-th from the top),
  * *n_free, the new lengths, cu_q [seqs + 1], of every token its sequence and
  * position (seq, pos [tokens]; -1 past the last token, which the row calls
- * skip), and *lacking, the pages asked for beyond the stack's (0: none).
+ * skip), and *lacking, the pages asked for beyond the stack's (0: none; a request
+ * without room in the table or in `tokens` shows in its length alone).
  * kv_lens_out must not overlap kv_lens.
  *
  * spec_kv_release: sequence b keeps the first keep[b] of its kv_lens[b] positions
@@ -564,9 +565,12 @@ SPEC_API int spec_attn_prompt_window(const void* q, int64_t q_tok_stride, int64_
  * the buffers.  A value row that is not finite within the prefix reaches
  * the rows of the whole group.
  * workspace as for spec_attn_paged; with fewer bytes than
- * spec_attn_shared_workspace says, and where sharing does not pay (more than 64
- * rows max_q * n_heads / n_kv_heads, head_dim 32, few or short sequences),
- * nothing is shared and the call is spec_attn_paged. */
+ * spec_attn_shared_workspace says, and where sharing is not taken (more than 64
+ * rows max_q * n_heads / n_kv_heads, head_dim 32, few sequences or a narrow table),
+ * nothing is shared and the call is spec_attn_paged.  The lengths being on the
+ * device, the choice goes by the table's width (max_pages * page_size): a program
+ * whose contexts are short in a wide table should call spec_attn_paged while they
+ * are, which then takes half the time. */
 SPEC_API int spec_attn_shared(const spec_kv_cache* cache, const void* q, int64_t q_tok_stride, int64_t q_head_stride,
                     const int32_t* cu_q, const int32_t* kv_lens, const int32_t* groups, int n_groups,
                     const int32_t* shared, int tokens, int max_q, int n_heads, float scale, void* out,

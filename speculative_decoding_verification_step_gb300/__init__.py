@@ -789,7 +789,8 @@ def kv_reserve(cache, kv_lens, counts, free, n_free, tokens, stream=None):
     attention calls take them; `tokens` bounds the step's tokens, and entries
     past them are -1.  Requests are served in order and whole; one that does
     not fit gets nothing (its length is as before), and lacking counts the
-    pages that were missing."""
+    pages that were missing (want of room in the table or in `tokens` shows in
+    the lengths alone)."""
     _torch()
     dev, seqs = cache._dev, cache.seqs
     _index("kv_lens", kv_lens, seqs, dev)
@@ -909,7 +910,9 @@ def attn_shared(q, cache, cu_q, kv_lens, shared, groups=None, max_q=None, scale=
     pages at their beginning: the first shared[g] positions (int32 [groups]) of
     the sequences groups[g] .. groups[g+1]-1 (int32 [groups + 1]; default: one
     group of all) are read once for the group.  Any number of positions; it is
-    cut to what every row of the group sees."""
+    cut to what every row of the group sees.  Whether sharing pays is judged by
+    the sizes given and the table's width: for short contexts in a wide table
+    attn_paged takes half the time."""
     _torch()
     qs, shape, dev = _paged_args(q, cache, cu_q, kv_lens)
     n, h, d = shape

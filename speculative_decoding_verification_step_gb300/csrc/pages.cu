@@ -22,7 +22,7 @@
 // launch behind them (960 thousand tokens and the release of their pages 61 -> 21 us).
 // No atomics: the pages that a sequence gets depend on the arguments alone.
 // Bound by latency: loads, two scans, searches, stores.  64 sequences x 6 tokens and their
-// release 8.2 us replayed from a graph; as calls 19 to 23 us of host time, 3 of them the results.
+// release 8.2 us replayed from a graph; as calls 21 us of host time, 6 of them the results.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kPgThreads = 512;
 constexpr int kPgCluster = 8;
+constexpr int kPgMost = 296;       // blocks of a step of many tokens (304, two an SM: 21.7 us for 21.4)
 constexpr int kPgBatch = 4;        // dropped entries of a thread on their way
 constexpr int kPgHeld = 8192;      // dropped entries of a block at a time
 
@@ -327,7 +328,7 @@ int spec_kv_reserve(const spec_kv_cache* cache, const int32_t* kv_lens, const in
   a.tokens = tokens; a.cu = cu_q; a.lens_out = kv_lens_out; a.seq = seq; a.pos = pos; a.lacking = lacking;
   a.vec = ((reinterpret_cast<uintptr_t>(seq) | reinterpret_cast<uintptr_t>(pos)) & 15u) == 0;
   const bool many = tokens > 65536;
-  a.blocks = many ? std::min(296, tokens / 1024) : tokens > 8 * kPgThreads ? kPgCluster : 1;
+  a.blocks = many ? std::min(kPgMost, tokens / 1024) : tokens > 8 * kPgThreads ? kPgCluster : 1;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = launch_rows(reserve_kernel, dim3(a.blocks), dim3(kPgThreads), 0, many ? 1 : a.blocks, st, a);
   if (e == cudaSuccess && many) e = launch_rows(reserve_end_kernel, dim3(1), dim3(kPgThreads), 0, 1, st, a);

@@ -84,14 +84,18 @@ Way choose_way(const PAttn& a, int sms) {
   return {false, td_bytes(a, rows, sms)};
 }
 
-// Workspace of launch_pattn_shared where it is taken, else 0.  Its four launches cost
-// some 20 us, and sequences that read the same pages one by one find them in L2: it is
-// taken where they would read 800 thousand rows of keys (positions x KV heads) again, for
-// more than 8 rows per KV head, whose walk costs more, 260 thousand, 450 at head dim 64, and
-// beyond 32 rows, where what lies behind the prefix weighs more, 2048 positions at least.
-// The lengths being on the device, a table's width stands for them.  One by one / shared,
-// us, 8 KV heads, 100 positions behind the prefix.  4 rows, bf16, head dim 128: 8
-// sequences x 8192 26 / 29, 16 x 8192 39 / 29, 64 x 2048 51 / 28, 64 x 8192 168 / 37, 4 x
+// Workspace of launch_pattn_shared where it is taken, else 0.  What is fixed in its four
+// launches is some 25 us, 20 more than in the one launch of the other way, and sequences
+// that read the same pages one by one find them in L2: it is taken where they would
+// read 800 thousand rows of keys (positions x KV heads) again, for more than 8 rows per
+// KV head, whose walk costs more, 260 thousand, 450 at head dim 64, and beyond 32 rows,
+// where what lies behind the prefix weighs more, 2048 positions at least.
+// The lengths being on the device, a table's width stands for them, so over a table much
+// wider than its contexts (8 KV heads, 131072 positions: from two sequences on) sharing is
+// taken where one by one would be faster: 4 x 6 behind 512 then take 18 us for 9, 2 x 1
+// behind 2048 20 for 8.  One by one / shared, us, tables as wide as the contexts, 8 KV
+// heads, 100 positions behind the prefix.  4 rows, bf16, head dim 128: 8 sequences x 8192
+// 26 / 29, 16 x 8192 39 / 29, 64 x 2048 51 / 28, 64 x 8192 168 / 37, 4 x
 // 32768 45 / 50; e4m3: 8 x 8192 29 / 36, 16 x 8192 50 / 35; head dim 64, bf16: 8 x 8192
 // 16 / 28, 16 x 8192 26 / 26.  24 rows, bf16, head dim 128: 4 x 8192 28 / 35, 8 x 8192
 // 47 / 39, 64 x 512 36 / 42, 64 x 2048 90 / 50; e4m3: 8 x 8192 58 / 42, 64 x 8192

@@ -38,8 +38,12 @@ namespace {
 
 constexpr int kShThreads = 256;
 
-// How long things take on one SM, in ns: a unit of the prefix; a key of the rest for one KV head of
-// one sequence, and a block's start in keys (three blocks at a time).
+// Weights by which the SMs are divided between prefix and rest, about ns on one SM: a unit of the
+// prefix; a key of the rest for one KV head of one sequence, and a block's start in keys.  They are
+// estimates, not measurements (the results are right whatever they are).  Measured on all SMs, from
+// 16384 to 65536 prefix positions, a unit is 1.7 us for bf16 and 2.0 for e4m3 at head dim 128, 1.2
+// and 1.9 to 2.0 at 64; a key of the register tiles alone, from 256 to 768 positions, is 10.5 to
+// 11.6 ns and 6.6 to 9.8 at 128, 5.4 to 6.5 and 3.9 to 6.0 at 64 (1 to 6 tokens of 4 rows).
 struct ShCost {
   float unit, key, block;
 };
