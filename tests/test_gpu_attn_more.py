@@ -564,3 +564,40 @@ def test_shared_behind_idle_sequences(dtype, hd, ns, first, shared):
     _shared_check(c, q, cu, lens, ns, ctx, sh, gr, max(ns))
     c.table[torch.tensor(ns, device="cuda") == 0] = 2 ** 30
     _shared_check(c, q, cu, lens, ns, ctx, sh, gr, max(ns))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hk,hd,ps,ns,ctx,window,sinks", [
+    (16, 4, 128, 64, [256, 130], [7000, 3000], 2500, 4),
+    (8, 2, 64, 16, [500], [9000], 3000, 300),
+    (32, 8, 128, 256, [100], [6000], 5000, 0),
+    (8, 2, 128, 32, [300, 200], [2900, 150], 2100, 2000),        # first tokens over many steps; a chunk past its context
+])
+def test_window_keys_cut_between_two_blocks(hq, hk, hd, ps, ns, ctx, window, sinks, dtype):
+    """Few chunks in a long window: two blocks share an item's keys."""
+    c, q, cu, lens = _paged_case(sum(ctx) + hd, hq, hk, hd, ps, dtype, ns, ctx, pad=2)
+    values = _all_values(c, ctx)
+    _evict(c, ns, ctx, window, sinks)
+    a = _window_check(c, q, cu, lens, ns, ctx, window, sinks, values, max_q=max(ns))
+    n = sum(ns)
+    for _ in range(3):
+        again = sv.attn_paged(q, c, cu, lens, max_q=max(ns), window=window, sinks=sinks)
+        assert torch.equal(again[0][:n], a[0][:n]) and torch.equal(again[1][:n], a[1][:n])
+    rows = q[:n]
+    _give_up(lambda o, l: sv.attn_paged(rows, c, cu, lens, max_q=max(ns), out=o, lse=l, window=window, sinks=sinks), rows, (1, 4))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd,groups,each", [(128, 9, 3), (64, 33, 2), (128, 70, 2), (64, 130, 3)])
+def test_shared_many_groups(dtype, hd, groups, each):
+    """More groups than a block's warps, or than a warp has lanes; some share nothing, some have no rows."""
+    r = torch.Generator().manual_seed(groups)
+    draw = lambda hi, n: torch.randint(0, hi, (n,), generator=r).tolist()
+    shared = [0 if i % 7 == 3 else x for i, x in enumerate(draw(400, groups))]
+    ns = [0 if b // each % 5 == 2 else 1 + x for b, x in enumerate(draw(3, groups * each))]
+    rests = [n + x for n, x in zip(ns, draw(60, groups * each))]
+    first = list(range(0, groups * each + 1, each))
+    c, q, cu, lens, ctx = _shared_case(31 + groups, 8, 2, hd, 16, dtype, ns, first, shared, rests, pad=1)
+    c = _wide(c)
+    assert _shares(c, groups, q.shape[0], max(ns), 8)
+    _shared_check(c, q, cu, lens, ns, ctx, _i32(shared), _i32(first), max(ns))
